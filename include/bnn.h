@@ -305,6 +305,59 @@ bnn_status bnn_gemv_act(const void *x, int dtype, int64_t ldx, const uint64_t *w
                         const float *alpha, void *y, int64_t M, int64_t N, int64_t K, int epilogue,
                         void *stream);
 
+/*
+ * bnn_layernorm_fwd -- layer norm over the last dimension, the norm ahead of
+ * a (binarised or other) sub-layer: per row of N values
+ *   mu = mean(x),  r = 1 / sqrt(mean((x - mu)^2) + eps),
+ *   y = (x - mu) * r * gamma + beta.
+ * Sums and statistics are fp32 (two passes: the mean first, then the centred
+ * squares); y is rounded once to its type.
+ *
+ *   x      M rows of N values of type dtype (BNN_FP32 / BNN_BF16), row stride
+ *          ldx >= N elements, element-aligned.
+ *   gamma, beta  N fp32 each, 4-byte aligned; either may be NULL (1 / 0).
+ *   y      M rows of N values of the same type, row stride ldy >= N; only
+ *          the N columns of a row are written.
+ *   mean, rstd   M fp32 each (mu and r, what bnn_layernorm_bwd takes),
+ *          4-byte aligned; either may be NULL (not stored).
+ *   eps    finite and >= 0, else BNN_E_ARG.
+ * N = 0 with M > 0 is BNN_E_SHAPE (an empty row has no mean); M = 0 launches
+ * nothing.  A row holding a NaN or an infinity gives NaN in that row only.
+ * Errors: BNN_E_DTYPE, BNN_E_SHAPE, BNN_E_ARG, BNN_E_NULL, BNN_E_ALIGN,
+ * BNN_E_LAUNCH.
+ */
+bnn_status bnn_layernorm_fwd(const void *x, int dtype, int64_t ldx, const float *gamma,
+                             const float *beta, void *y, int64_t ldy, float *mean, float *rstd,
+                             int64_t M, int64_t N, float eps, void *stream);
+
+/* Bytes of workspace that bnn_layernorm_bwd needs for these sizes (0 when M
+ * or N is <= 0). */
+int64_t bnn_layernorm_bwd_workspace(int64_t M, int64_t N);
+
+/*
+ * bnn_layernorm_bwd -- the gradient of bnn_layernorm_fwd.  With
+ * xh = (x - mean) * rstd and g = dy * gamma:
+ *   dx = rstd * (g - mean_n(g) - xh * mean_n(g * xh)),
+ *   dgamma[n] = sum_m dy * xh,   dbeta[n] = sum_m dy.
+ * All sums are fp32, in a fixed order: equal inputs give equal bits.
+ *
+ *   dy, x  M rows of N values of type dtype, row strides lddy, ldx >= N.
+ *   gamma  N fp32 or NULL (1), as in the forward pass.
+ *   mean, rstd   M fp32 each, from the forward pass.
+ *   dx     M rows of N values of type dtype, row stride lddx >= N.
+ *   dgamma, dbeta  N fp32 each, overwritten; both NULL: not computed.  With
+ *          M = 0 they are written as zeros.
+ *   workspace    at least bnn_layernorm_bwd_workspace(M, N) bytes, 16-byte
+ *          aligned, used on `stream` until the call's kernels have run; may
+ *          be NULL when dgamma and dbeta are.  ws_bytes smaller than needed is
+ *          BNN_E_SHAPE.
+ * Errors: as bnn_layernorm_fwd; one of dgamma / dbeta NULL is BNN_E_NULL.
+ */
+bnn_status bnn_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx, int dtype,
+                             const float *gamma, const float *mean, const float *rstd, void *dx,
+                             int64_t lddx, float *dgamma, float *dbeta, void *workspace,
+                             int64_t ws_bytes, int64_t M, int64_t N, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

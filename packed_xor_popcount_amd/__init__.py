@@ -28,7 +28,7 @@ __all__ = [
     "ALGO_MFMA",
     "library", "library_path", "words", "pack_signs", "gemm_u64", "gemm_u64_scaled",
     "gemm_sign_repack", "gemm_sign_repack_thr", "flip_words", "gemm_signw_bf16", "chain3",
-    "gemm_ex", "gemv_act", "version",
+    "gemm_ex", "gemv_act", "version", "layernorm_fwd", "layernorm_bwd",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -40,7 +40,8 @@ ALGO_AUTO, ALGO_GEMV, ALGO_TILED, ALGO_MFMA = 0, 1, 2, 3
 
 EXPORTED = ("bnn_words", "bnn_status_str", "bnn_version", "bnn_pack_signs", "bnn_gemm_u64",
             "bnn_gemm_u64_scaled", "bnn_gemm_sign_repack", "bnn_gemm_ex", "bnn_gemv_act",
-            "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16", "bnn_chain3")
+            "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16", "bnn_chain3",
+            "bnn_layernorm_fwd", "bnn_layernorm_bwd_workspace", "bnn_layernorm_bwd")
 
 
 class BnnError(RuntimeError):
@@ -76,9 +77,14 @@ def library():
     lib.bnn_gemm_sign_repack_thr.argtypes = [P, P, P, P, P, I64, I64, I64, I, P]
     lib.bnn_gemm_signw_bf16.argtypes = [P, I64, P, P, P, I64, I64, I64, I, P]
     lib.bnn_chain3.argtypes = [P, I, I64, P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, P]
+    F = ctypes.c_float
+    lib.bnn_layernorm_fwd.argtypes = [P, I, I64, P, P, P, I64, P, P, I64, I64, F, P]
+    lib.bnn_layernorm_bwd.argtypes = [P, I64, P, I64, I, P, P, P, P, I64, P, P, P, I64, I64, I64, P]
+    lib.bnn_layernorm_bwd_workspace.argtypes = [I64, I64]
+    lib.bnn_layernorm_bwd_workspace.restype = I64
     for name in ("bnn_pack_signs", "bnn_gemm_u64", "bnn_gemm_u64_scaled", "bnn_gemm_sign_repack",
                  "bnn_gemm_ex", "bnn_gemv_act", "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16",
-                 "bnn_chain3"):
+                 "bnn_chain3", "bnn_layernorm_fwd", "bnn_layernorm_bwd"):
         getattr(lib, name).restype = I
     _lib = lib
     return lib
@@ -360,3 +366,84 @@ def chain3(x, w1, w2, w3, alpha3=None, out=None, thr1=None, flip1=None, thr2=Non
                               N2, N3, _stream(x))
     _check(st, "bnn_chain3")
     return out
+
+
+def _real_rows(name: str, t: torch.Tensor):
+    """(dtype code, rows, columns, row stride) of a 2-D fp32 / bf16 CUDA
+    tensor with unit stride along its last dimension."""
+    _need_cuda(name, t)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit stride along its last dimension")
+    if t.dtype == torch.float32:
+        dt = BNN_FP32
+    elif t.dtype == torch.bfloat16:
+        dt = BNN_BF16
+    else:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    rows, cols = t.shape
+    return dt, rows, cols, (t.stride(0) if rows > 1 else max(cols, 1))
+
+
+def _vector(name: str, t, n: int, device, dtype=torch.float32):
+    _need_cuda(name, t)
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({n},)")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def layernorm_fwd(x, gamma=None, beta=None, eps=1e-5, stats=True, out=None):
+    """Layer norm of the rows of ``x`` (2-D fp32 or bf16 CUDA tensor, rows may
+    be strided): ``(y, mean, rstd)`` with ``y`` of x's type and fp32 ``mean``
+    and ``rstd`` of shape ``(M,)``, or None for both with ``stats=False``
+    (bnn_layernorm_fwd).  ``gamma`` and ``beta`` are None or contiguous
+    float32 ``(N,)``; ``out`` may be a tensor of x's shape and type with unit
+    stride along its last dimension."""
+    dt, M, N, ldx = _real_rows("x", x)
+    if gamma is not None:
+        _vector("gamma", gamma, N, x.device)
+    if beta is not None:
+        _vector("beta", beta, N, x.device)
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        ldy = max(N, 1)
+    else:
+        dto, Mo, No, ldy = _real_rows("out", out)
+        if (dto, Mo, No) != (dt, M, N) or out.device != x.device:
+            raise ValueError("out must have x's shape, type and device")
+    mean = rstd = None
+    if stats:
+        mean = torch.empty((M,), dtype=torch.float32, device=x.device)
+        rstd = torch.empty((M,), dtype=torch.float32, device=x.device)
+    st = library().bnn_layernorm_fwd(_ptr(x), dt, ldx, _ptr(gamma), _ptr(beta), _ptr(out), ldy,
+                                     _ptr(mean), _ptr(rstd), M, N, float(eps), _stream(x))
+    _check(st, "bnn_layernorm_fwd")
+    return out, mean, rstd
+
+
+def layernorm_bwd(dy, x, mean, rstd, gamma=None, params=True):
+    """Gradient of layernorm_fwd: ``(dx, dgamma, dbeta)`` from the output's
+    gradient ``dy`` (x's shape and type), the forward pass's ``x``, ``mean``
+    and ``rstd`` and its ``gamma`` (bnn_layernorm_bwd).  ``params=False``
+    leaves out the sums over the rows (None for dgamma and dbeta)."""
+    dt, M, N, ldx = _real_rows("x", x)
+    dtd, Md, Nd, lddy = _real_rows("dy", dy)
+    if (dtd, Md, Nd) != (dt, M, N) or dy.device != x.device:
+        raise ValueError("dy must have x's shape, type and device")
+    _vector("mean", mean, M, x.device)
+    _vector("rstd", rstd, M, x.device)
+    if gamma is not None:
+        _vector("gamma", gamma, N, x.device)
+    dx = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    dgamma = dbeta = ws = None
+    need = 0
+    if params:
+        dgamma = torch.empty((N,), dtype=torch.float32, device=x.device)
+        dbeta = torch.empty((N,), dtype=torch.float32, device=x.device)
+        need = library().bnn_layernorm_bwd_workspace(M, N)
+        ws = torch.empty((need,), dtype=torch.uint8, device=x.device)
+    st = library().bnn_layernorm_bwd(_ptr(dy), lddy, _ptr(x), ldx, dt, _ptr(gamma), _ptr(mean),
+                                     _ptr(rstd), _ptr(dx), max(N, 1), _ptr(dgamma), _ptr(dbeta),
+                                     _ptr(ws), need, M, N, _stream(x))
+    _check(st, "bnn_layernorm_bwd")
+    return dx, dgamma, dbeta

@@ -5,6 +5,8 @@
 #include "../../include/bnn.h"
 #include "bnn_internal.h"
 
+#include <float.h>
+
 namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;  // M, N, K, rows and ld limits
@@ -166,6 +168,54 @@ bnn_status bnn_chain3(const void *x, int dtype, int64_t ldx, const uint64_t *w1,
   const bnn::Chain3Repack rp{thr1, flip1, thr2, flip2};
   return launch_status(bnn::launch_chain3(x, dtype, ldx, w1, w2, w3, alpha3, y, M, K0, N1, N2, N3,
                                           rp, static_cast<hipStream_t>(stream)));
+}
+
+bnn_status bnn_layernorm_fwd(const void *x, int dtype, int64_t ldx, const float *gamma,
+                             const float *beta, void *y, int64_t ldy, float *mean, float *rstd,
+                             int64_t M, int64_t N, float eps, void *stream) {
+  if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
+  if (M < 0 || N < 0 || M >= kMaxDim || N >= kMaxDim || ldx < N || ldy < N || ldx >= kMaxDim ||
+      ldy >= kMaxDim || (N == 0 && M > 0))
+    return BNN_E_SHAPE;
+  if (!(eps >= 0.0f) || eps > FLT_MAX) return BNN_E_ARG;
+  if (M > 0 && (!x || !y)) return BNN_E_NULL;
+  const uintptr_t es = dtype == BNN_FP32 ? 4 : 2;
+  if (misaligned(x, es) || misaligned(y, es) || misaligned(gamma, 4) || misaligned(beta, 4) ||
+      misaligned(mean, 4) || misaligned(rstd, 4))
+    return BNN_E_ALIGN;
+  if (M == 0) return BNN_OK;
+  return launch_status(bnn::launch_layernorm_fwd(x, dtype, ldx, gamma, beta, y, ldy, mean, rstd, M,
+                                                 N, eps, static_cast<hipStream_t>(stream)));
+}
+
+int64_t bnn_layernorm_bwd_workspace(int64_t M, int64_t N) {
+  if (M <= 0 || N <= 0 || M >= kMaxDim || N >= kMaxDim) return 0;
+  return bnn::layernorm_bwd_partials(M, N) * 2 * N * (int64_t)sizeof(float);
+}
+
+bnn_status bnn_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx, int dtype,
+                             const float *gamma, const float *mean, const float *rstd, void *dx,
+                             int64_t lddx, float *dgamma, float *dbeta, void *workspace,
+                             int64_t ws_bytes, int64_t M, int64_t N, void *stream) {
+  if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
+  if (M < 0 || N < 0 || M >= kMaxDim || N >= kMaxDim || lddy < N || ldx < N || lddx < N ||
+      lddy >= kMaxDim || ldx >= kMaxDim || lddx >= kMaxDim || (N == 0 && M > 0))
+    return BNN_E_SHAPE;
+  if (M > 0 && (!dy || !x || !mean || !rstd || !dx)) return BNN_E_NULL;
+  if (!dgamma != !dbeta) return BNN_E_NULL;
+  const int64_t need = dgamma ? bnn_layernorm_bwd_workspace(M, N) : 0;
+  if (need > 0 && !workspace) return BNN_E_NULL;
+  if (ws_bytes < need) return BNN_E_SHAPE;
+  const uintptr_t es = dtype == BNN_FP32 ? 4 : 2;
+  if (misaligned(dy, es) || misaligned(x, es) || misaligned(dx, es) || misaligned(gamma, 4) ||
+      misaligned(mean, 4) || misaligned(rstd, 4) || misaligned(dgamma, 4) ||
+      misaligned(dbeta, 4) || misaligned(workspace, 16))
+    return BNN_E_ALIGN;
+  if (N == 0 || (M == 0 && !dgamma)) return BNN_OK;
+  return launch_status(bnn::launch_layernorm_bwd(dy, lddy, x, ldx, dtype, gamma, mean, rstd, dx,
+                                                 lddx, dgamma, dbeta,
+                                                 static_cast<float *>(workspace), M, N,
+                                                 static_cast<hipStream_t>(stream)));
 }
 
 bnn_status bnn_gemm_u64(const uint64_t *xp, const uint64_t *wp, int32_t *y, int64_t M, int64_t N,

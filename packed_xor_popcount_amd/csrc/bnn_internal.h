@@ -82,6 +82,17 @@ hipError_t launch_chain3(const void *x, int dtype, int64_t ldx, const uint64_t *
                          int64_t M, int64_t K0, int64_t N1, int64_t N2, int64_t N3,
                          const Chain3Repack &rp, hipStream_t s);
 
+// Layer norm and its gradient (arguments as in the C-ABI).  The gradient's
+// column sums pass through `part`, layernorm_bwd_partials rows of 2 x N fp32.
+int64_t layernorm_bwd_partials(int64_t M, int64_t N);
+hipError_t launch_layernorm_fwd(const void *x, int dtype, int64_t ldx, const float *gamma,
+                                const float *beta, void *y, int64_t ldy, float *mean, float *rstd,
+                                int64_t M, int64_t N, float eps, hipStream_t s);
+hipError_t launch_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                int dtype, const float *gamma, const float *mean,
+                                const float *rstd, void *dx, int64_t lddx, float *dgamma,
+                                float *dbeta, float *part, int64_t M, int64_t N, hipStream_t s);
+
 // Threshold-repack operands, loaded by the kernels before their K loops from
 // clamped (always in-bounds) indexes: the threshold of output column n, and
 // the flip word of 64-column group wi with its bits past column N cleared

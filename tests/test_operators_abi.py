@@ -1,0 +1,66 @@
+"""Refusals of the operators around the packed products: every call below
+fails validation on the host (or has nothing to do), so none reaches a
+device."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+import packed_xor_popcount_amd as bnn
+
+OK, E_NULL, E_SHAPE, E_DTYPE, E_ALIGN, E_LAUNCH, E_ARG = range(7)
+P = ctypes.c_void_p
+FAKE = P(0x1000)
+BIG = 2 ** 30
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return bnn.library()
+
+
+def test_layernorm_fwd_refusals(lib):
+    def f(x=FAKE, dt=0, ldx=8, g=None, b=None, y=FAKE, ldy=8, mu=None, r=None, M=2, N=8, eps=1e-5):
+        return lib.bnn_layernorm_fwd(x, dt, ldx, g, b, y, ldy, mu, r, M, N, eps, None)
+    assert f(dt=2) == E_DTYPE
+    for kw in (dict(M=-1), dict(N=-1), dict(M=BIG), dict(N=BIG, ldx=BIG, ldy=BIG), dict(ldx=7), dict(ldy=7),
+               dict(ldx=BIG), dict(N=0)):
+        assert f(**kw) == E_SHAPE, kw
+    for eps in (-1e-5, float("nan"), float("inf")):
+        assert f(eps=eps) == E_ARG, eps
+    assert f(x=None) == E_NULL and f(y=None) == E_NULL
+    for kw in (dict(x=P(0x1002)), dict(y=P(0x1002)), dict(g=P(0x1002)), dict(b=P(0x1001)), dict(mu=P(0x1002)),
+               dict(r=P(0x1001)), dict(dt=1, x=P(0x1001))):
+        assert f(**kw) == E_ALIGN, kw
+    assert f(x=None, y=None, M=0) == OK and f(x=None, y=None, M=0, N=0) == OK
+
+
+def test_layernorm_bwd_refusals(lib):
+    need = lib.bnn_layernorm_bwd_workspace(2, 8)
+    assert need > 0
+    assert all(lib.bnn_layernorm_bwd_workspace(m, n) == 0 for m, n in ((0, 8), (8, 0), (-1, 8), (BIG, 8), (8, BIG)))
+
+    def f(dy=FAKE, lddy=8, x=FAKE, ldx=8, dt=0, g=None, mu=FAKE, r=FAKE, dx=FAKE, lddx=8, dg=FAKE, db=FAKE, ws=FAKE,
+          wb=need, M=2, N=8):
+        return lib.bnn_layernorm_bwd(dy, lddy, x, ldx, dt, g, mu, r, dx, lddx, dg, db, ws, wb, M, N, None)
+    assert f(dt=-1) == E_DTYPE
+    for kw in (dict(M=-1), dict(N=-1), dict(M=BIG), dict(ldx=7), dict(lddy=7), dict(lddx=7), dict(lddx=BIG),
+               dict(N=0), dict(wb=need - 1), dict(wb=-1)):
+        assert f(**kw) == E_SHAPE, kw
+    for k in ("dy", "x", "mu", "r", "dx", "dg", "db", "ws"):
+        assert f(**{k: None}) == E_NULL, k
+    for k in ("dy", "x", "mu", "r", "dx", "dg", "db"):
+        assert f(**{k: P(0x1002)}) == E_ALIGN, k
+    assert f(ws=P(0x1008)) == E_ALIGN and f(g=P(0x1001)) == E_ALIGN
+    assert f(dy=None, x=None, mu=None, r=None, dx=None, dg=None, db=None, ws=None, wb=0, M=0) == OK
+    assert f(M=0, N=0, wb=0, ws=None) == OK
+
+
+def test_bindings_refuse_cpu_tensors():
+    x, v = torch.zeros(2, 3), torch.zeros(2)
+    with pytest.raises(TypeError):
+        bnn.layernorm_fwd(x)
+    with pytest.raises(TypeError):
+        bnn.layernorm_bwd(x, x, v, v)
