@@ -358,6 +358,62 @@ bnn_status bnn_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_
                              int64_t lddx, float *dgamma, float *dbeta, void *workspace,
                              int64_t ws_bytes, int64_t M, int64_t N, void *stream);
 
+/*
+ * Block-scaled 8-bit matrices, for the layers that are not binarised.  A
+ * matrix of R rows and K columns is two contiguous buffers:
+ *   q  R x bnn_f8_row_bytes(K) bytes (128 * ceil(K / 128)): e4m3 values
+ *      (OCP "fn": 448 largest, no infinities), zeros past K;
+ *   s  R x bnn_f8_scale_bytes(K) bytes (4 * ceil(K / 512)): byte b of a row is
+ *      the biased exponent of the block of elements 128 b .. 128 b + 127,
+ *      which stand for q * 2^(s - 127); bytes past the last block are unused.
+ * Both helpers give 0 for K <= 0.
+ */
+int64_t bnn_f8_row_bytes(int64_t k);
+int64_t bnn_f8_scale_bytes(int64_t k);
+
+/*
+ * bnn_quant_f8 -- real rows to the block-scaled 8-bit form.  A block's scale
+ * is the smallest power of two (at least 2^-127) that brings its largest
+ * finite magnitude to at most 448 (1 for a block of zeros); a value is scaled
+ * exactly and rounded once, to nearest even.  Infinities and NaN become NaN
+ * and do not enter the scale.  Zeros are written past K, zero scale bytes
+ * past the last block.
+ *
+ *   src        rows x k values of type dtype (BNN_FP32 / BNN_BF16), row stride
+ *              ld_src >= k elements, element-aligned.
+ *   transpose  0: the quantised matrix is src (rows rows, k columns, blocks
+ *              along k).  1: it is src transposed (k rows, rows columns,
+ *              blocks along src's rows), the form of a weight or of an
+ *              activation for the gradient products.
+ *   q, s       as above for the quantised matrix; q 16-byte, s 4-byte aligned.
+ * An empty matrix launches nothing.  Errors: BNN_E_DTYPE, BNN_E_SHAPE,
+ * BNN_E_ARG (transpose not 0 or 1), BNN_E_NULL, BNN_E_ALIGN, BNN_E_LAUNCH.
+ */
+bnn_status bnn_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int64_t ld_src,
+                        int transpose, uint8_t *q, uint8_t *s, void *stream);
+
+/*
+ * bnn_gemm_f8 -- product of two block-scaled 8-bit matrices:
+ *   y[m][n] = sum_b 2^(xs[m][b] + ws[n][b] - 254) sum_{k in block b} xq[m][k] * wq[n][k],
+ * sums fp32 on the matrix cores, rounded once to y's type; their order
+ * depends on the sizes and types only.  fp32 outputs: products exact, within
+ * the bound of an fp32 sum of K terms.  bf16 outputs may use the 8-bit matrix
+ * instructions, which cut a product's bits below 2^-13 of the largest among
+ * eight consecutive k (1.6e-5 of the result for normal operands, far below
+ * the rounding to bf16).  Decoded values below 2^-126 may count as zero and
+ * those above bf16's range as infinite; bnn_quant_f8 makes none of the latter.
+ *
+ *   xq, xs   M rows of K columns, wq, ws  N rows of K columns; q buffers
+ *            16-byte, s buffers 4-byte aligned.  The bytes past K have to be
+ *            zero in both (as bnn_quant_f8 writes them).
+ *   y        M x N of type dtype (BNN_FP32 / BNN_BF16), row-major,
+ *            element-aligned.
+ * K = 0 gives y = 0.  Errors: BNN_E_DTYPE, BNN_E_SHAPE, BNN_E_NULL,
+ * BNN_E_ALIGN, BNN_E_LAUNCH.
+ */
+bnn_status bnn_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                       void *y, int dtype, int64_t M, int64_t N, int64_t K, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,6 +29,7 @@ __all__ = [
     "library", "library_path", "words", "pack_signs", "gemm_u64", "gemm_u64_scaled",
     "gemm_sign_repack", "gemm_sign_repack_thr", "flip_words", "gemm_signw_bf16", "chain3",
     "gemm_ex", "gemv_act", "version", "layernorm_fwd", "layernorm_bwd",
+    "f8_row_bytes", "f8_scale_bytes", "quant_f8", "gemm_f8",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,7 +42,8 @@ ALGO_AUTO, ALGO_GEMV, ALGO_TILED, ALGO_MFMA = 0, 1, 2, 3
 EXPORTED = ("bnn_words", "bnn_status_str", "bnn_version", "bnn_pack_signs", "bnn_gemm_u64",
             "bnn_gemm_u64_scaled", "bnn_gemm_sign_repack", "bnn_gemm_ex", "bnn_gemv_act",
             "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16", "bnn_chain3",
-            "bnn_layernorm_fwd", "bnn_layernorm_bwd_workspace", "bnn_layernorm_bwd")
+            "bnn_layernorm_fwd", "bnn_layernorm_bwd_workspace", "bnn_layernorm_bwd",
+            "bnn_f8_row_bytes", "bnn_f8_scale_bytes", "bnn_quant_f8", "bnn_gemm_f8")
 
 
 class BnnError(RuntimeError):
@@ -82,9 +84,14 @@ def library():
     lib.bnn_layernorm_bwd.argtypes = [P, I64, P, I64, I, P, P, P, P, I64, P, P, P, I64, I64, I64, P]
     lib.bnn_layernorm_bwd_workspace.argtypes = [I64, I64]
     lib.bnn_layernorm_bwd_workspace.restype = I64
+    lib.bnn_f8_row_bytes.argtypes, lib.bnn_f8_row_bytes.restype = [I64], I64
+    lib.bnn_f8_scale_bytes.argtypes, lib.bnn_f8_scale_bytes.restype = [I64], I64
+    lib.bnn_quant_f8.argtypes = [P, I, I64, I64, I64, I, P, P, P]
+    lib.bnn_gemm_f8.argtypes = [P, P, P, P, P, I, I64, I64, I64, P]
     for name in ("bnn_pack_signs", "bnn_gemm_u64", "bnn_gemm_u64_scaled", "bnn_gemm_sign_repack",
                  "bnn_gemm_ex", "bnn_gemv_act", "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16",
-                 "bnn_chain3", "bnn_layernorm_fwd", "bnn_layernorm_bwd"):
+                 "bnn_chain3", "bnn_layernorm_fwd", "bnn_layernorm_bwd", "bnn_quant_f8",
+                 "bnn_gemm_f8"):
         getattr(lib, name).restype = I
     _lib = lib
     return lib
@@ -447,3 +454,74 @@ def layernorm_bwd(dy, x, mean, rstd, gamma=None, params=True):
                                      _ptr(ws), need, M, N, _stream(x))
     _check(st, "bnn_layernorm_bwd")
     return dx, dgamma, dbeta
+
+
+def f8_row_bytes(k: int) -> int:
+    """Bytes of 8-bit values per row of k columns: 128 * ceil(k / 128)."""
+    return int(library().bnn_f8_row_bytes(int(k)))
+
+
+def f8_scale_bytes(k: int) -> int:
+    """Scale bytes per row of k columns: 4 * ceil(k / 512), one per block of
+    128 columns and unused ones up to a multiple of four."""
+    return int(library().bnn_f8_scale_bytes(int(k)))
+
+
+def quant_f8(x, transpose=False):
+    """Block-scaled 8-bit form of ``x`` (2-D fp32 or bf16 CUDA tensor, rows may
+    be strided), or of its transpose: ``(q, s)``, two uint8 tensors of shapes
+    ``(R, f8_row_bytes(K))`` (e4m3 values, zeros past K; view them as
+    ``torch.float8_e4m3fn``) and ``(R, f8_scale_bytes(K))`` (biased exponents of
+    the blocks of 128 columns) (bnn_quant_f8)."""
+    dt, rows, k, ld = _real_rows("x", x)
+    R, K = (k, rows) if transpose else (rows, k)
+    q = torch.empty((R, f8_row_bytes(K)), dtype=torch.uint8, device=x.device)
+    s = torch.empty((R, f8_scale_bytes(K)), dtype=torch.uint8, device=x.device)
+    st = library().bnn_quant_f8(_ptr(x), dt, rows, k, ld, int(bool(transpose)), _ptr(q), _ptr(s),
+                                _stream(x))
+    _check(st, "bnn_quant_f8")
+    return q, s
+
+
+def _quantised(name: str, q, s, k: int) -> int:
+    for t in (q, s):
+        _need_cuda(name, t)
+        if t.dtype != torch.uint8 or t.dim() != 2 or not t.is_contiguous():
+            raise TypeError(f"{name} must be two contiguous 2-D uint8 tensors (values, scales)")
+    if (q.shape[1] != f8_row_bytes(k) or s.shape[1] != f8_scale_bytes(k)
+            or q.shape[0] != s.shape[0] or q.device != s.device):
+        raise ValueError(f"{name} does not have the block-scaled form of K={k} columns")
+    return q.shape[0]
+
+
+def gemm_f8(xq, xs, wq, ws, K, dtype=torch.float32, out=None):
+    """``(M, N)`` product of two block-scaled 8-bit matrices of K columns (as
+    quant_f8 makes them): ``x @ w.T`` with fp32 sums, rounded once to ``dtype``
+    (float32 or bfloat16) (bnn_gemm_f8)."""
+    K = int(K)
+    M = _quantised("x", xq, xs, K)
+    N = _quantised("w", wq, ws, K)
+    if wq.device != xq.device:
+        raise ValueError("x and w must be on the same device")
+    out, dt = _real_out(M, N, dtype, xq.device, out)
+    st = library().bnn_gemm_f8(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(out), dt, M, N, K,
+                               _stream(xq))
+    _check(st, "bnn_gemm_f8")
+    return out
+
+
+def _real_out(M: int, N: int, dtype, device, out):
+    """Output tensor and dtype code of a product that stores real values."""
+    if out is not None:
+        dtype = out.dtype
+    if dtype == torch.float32:
+        dt = BNN_FP32
+    elif dtype == torch.bfloat16:
+        dt = BNN_BF16
+    else:
+        raise TypeError("dtype must be float32 or bfloat16")
+    if out is None:
+        return torch.empty((M, N), dtype=dtype, device=device), dt
+    if tuple(out.shape) != (M, N) or not out.is_contiguous() or out.device != device:
+        raise ValueError(f"out must be a contiguous tensor of shape ({M}, {N}) on {device}")
+    return out, dt

@@ -4,6 +4,7 @@
 // synchronization, no state.
 #include "../../include/bnn.h"
 #include "bnn_internal.h"
+#include "f8.h"
 
 #include <float.h>
 
@@ -216,6 +217,38 @@ bnn_status bnn_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_
                                                  lddx, dgamma, dbeta,
                                                  static_cast<float *>(workspace), M, N,
                                                  static_cast<hipStream_t>(stream)));
+}
+
+int64_t bnn_f8_row_bytes(int64_t k) { return k <= 0 ? 0 : bnn::f8_row_bytes(k); }
+
+int64_t bnn_f8_scale_bytes(int64_t k) { return k <= 0 ? 0 : bnn::f8_scale_bytes(k); }
+
+bnn_status bnn_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int64_t ld_src,
+                        int transpose, uint8_t *q, uint8_t *s, void *stream) {
+  if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
+  if (transpose != 0 && transpose != 1) return BNN_E_ARG;
+  if (rows < 0 || k < 0 || ld_src < k || rows >= kMaxDim || k >= kMaxDim || ld_src >= kMaxDim)
+    return BNN_E_SHAPE;
+  if (rows * k > 0 && (!src || !q || !s)) return BNN_E_NULL;
+  if (misaligned(src, dtype == BNN_FP32 ? 4 : 2) || misaligned(q, 16) || misaligned(s, 4))
+    return BNN_E_ALIGN;
+  if (rows == 0 || k == 0) return BNN_OK;
+  return launch_status(bnn::launch_quant_f8(src, dtype, rows, k, ld_src, transpose != 0, q, s,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+bnn_status bnn_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                       void *y, int dtype, int64_t M, int64_t N, int64_t K, void *stream) {
+  if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
+  if (M < 0 || N < 0 || K < 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return BNN_E_SHAPE;
+  if ((M * K > 0 && (!xq || !xs)) || (N * K > 0 && (!wq || !ws)) || (M * N > 0 && !y))
+    return BNN_E_NULL;
+  if (misaligned(xq, 16) || misaligned(wq, 16) || misaligned(xs, 4) || misaligned(ws, 4) ||
+      misaligned(y, dtype == BNN_FP32 ? 4 : 2))
+    return BNN_E_ALIGN;
+  if (M == 0 || N == 0) return BNN_OK;
+  return launch_status(bnn::launch_gemm_f8(xq, xs, wq, ws, y, dtype, M, N, K,
+                                           static_cast<hipStream_t>(stream)));
 }
 
 bnn_status bnn_gemm_u64(const uint64_t *xp, const uint64_t *wp, int32_t *y, int64_t M, int64_t N,

@@ -64,3 +64,46 @@ def test_bindings_refuse_cpu_tensors():
         bnn.layernorm_fwd(x)
     with pytest.raises(TypeError):
         bnn.layernorm_bwd(x, x, v, v)
+
+
+def test_f8_sizes():
+    for k in (-3, 0, 1, 127, 128, 129, 512, 513, 4096, 2 ** 29):
+        nb = 0 if k <= 0 else -(-k // 128)
+        assert bnn.f8_row_bytes(k) == 128 * nb
+        assert bnn.f8_scale_bytes(k) == 4 * -(-nb // 4)
+
+
+def test_quant_f8_refusals(lib):
+    def f(x=FAKE, dt=0, rows=2, k=8, ld=8, t=0, q=FAKE, s=FAKE):
+        return lib.bnn_quant_f8(x, dt, rows, k, ld, t, q, s, None)
+    assert f(dt=2) == E_DTYPE
+    assert f(t=2) == E_ARG and f(t=-1) == E_ARG
+    for kw in (dict(rows=-1), dict(k=-1), dict(rows=BIG), dict(k=BIG, ld=BIG), dict(ld=7), dict(ld=BIG)):
+        assert f(**kw) == E_SHAPE, kw
+    for k in ("x", "q", "s"):
+        assert f(**{k: None}) == E_NULL, k
+    for kw in (dict(x=P(0x1002)), dict(x=P(0x1001), dt=1), dict(q=P(0x1008)), dict(s=P(0x1002))):
+        assert f(**kw) == E_ALIGN, kw
+    assert f(x=None, q=None, s=None, rows=0) == OK and f(x=None, q=None, s=None, k=0) == OK
+
+
+def test_gemm_f8_refusals(lib):
+    def f(xq=FAKE, xs=FAKE, wq=FAKE, ws=FAKE, y=FAKE, dt=0, M=2, N=3, K=8):
+        return lib.bnn_gemm_f8(xq, xs, wq, ws, y, dt, M, N, K, None)
+    assert f(dt=3) == E_DTYPE
+    for kw in (dict(M=-1), dict(N=-1), dict(K=-1), dict(M=BIG), dict(N=BIG), dict(K=BIG)):
+        assert f(**kw) == E_SHAPE, kw
+    for k in ("xq", "xs", "wq", "ws", "y"):
+        assert f(**{k: None}) == E_NULL, k
+    for kw in (dict(xq=P(0x1008)), dict(wq=P(0x1004)), dict(xs=P(0x1002)), dict(ws=P(0x1001)), dict(y=P(0x1002)),
+               dict(y=P(0x1001), dt=1)):
+        assert f(**kw) == E_ALIGN, kw
+    assert f(xq=None, xs=None, y=None, M=0) == OK and f(wq=None, ws=None, y=None, N=0) == OK
+
+
+def test_f8_bindings_refuse():
+    x = torch.zeros(2, 128)
+    with pytest.raises(TypeError):
+        bnn.quant_f8(x)
+    with pytest.raises(TypeError):
+        bnn.gemm_f8(x, x, x, x, 128)
