@@ -414,6 +414,44 @@ bnn_status bnn_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int
 bnn_status bnn_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
                        void *y, int dtype, int64_t M, int64_t N, int64_t K, void *stream);
 
+/*
+ * bnn_gemm_signw_grouped -- bnn_gemm_signw_bf16 grouped by expert: a mixture
+ * of experts whose weights are packed signs.  Row r of the output belongs to
+ * the expert e with offsets[e] <= r < offsets[e + 1]:
+ *   y[r][n] = row_scale[r] * (alpha[e][n] * sum_{k<K} x[src(r)][k] * w_e,n[k]),
+ * src(r) = rows[r], or r when rows is NULL.  The group sizes are ragged and
+ * live on the device; a group may be empty.  Up projection: rows gathers the
+ * tokens' rows in the experts' order.  Down projection: row_scale applies the
+ * router's weights.
+ *
+ * Arithmetic: as bnn_gemm_signw_bf16 (products exact, fp32 sums in an order
+ * the kernel chooses from the sizes), one fp32 multiply by alpha, one by
+ * row_scale, one rounding to y's type.  Elements past K and pad bits are
+ * never used.
+ *
+ *   x        xrows rows of bf16 values, row stride ldx >= K elements, 2-byte
+ *            aligned.  Without rows, xrows >= R.
+ *   rows     R int32 row indices in [0, xrows), or NULL.  (An index outside is
+ *            clamped, so no memory outside x is read.)
+ *   offsets  E + 1 int32, non-decreasing, within [0, R]; rows of y before
+ *            offsets[0] and from offsets[E] on are not written.  (Other
+ *            values are clamped: memory outside the buffers is never touched,
+ *            but which outputs are written is then unspecified.)
+ *   wp       E x N x bnn_words(K) packed sign weights, 8-byte aligned.
+ *   alpha    E x N fp32 scales, or NULL (1).  row_scale  R fp32, or NULL (1).
+ *   y        R x N of type dtype (BNN_FP32 / BNN_BF16), row-major.
+ *   algo     BNN_ALGO_AUTO; BNN_ALGO_GEMV (few rows per group: streams the
+ *            weights of each group once per 8 of its rows); or BNN_ALGO_MFMA
+ *            (matrix cores).  BNN_ALGO_TILED -> BNN_E_ARG.
+ * R = 0, E = 0 or N = 0 launches nothing; K = 0 gives y = 0 in the groups'
+ * rows.  E < 2^20.  Errors: BNN_E_DTYPE, BNN_E_ARG, BNN_E_SHAPE, BNN_E_NULL,
+ * BNN_E_ALIGN, BNN_E_LAUNCH.
+ */
+bnn_status bnn_gemm_signw_grouped(const void *x, int64_t ldx, int64_t xrows, const int32_t *rows,
+                                  const int32_t *offsets, const uint64_t *wp, const float *alpha,
+                                  const float *row_scale, void *y, int dtype, int64_t R, int64_t E,
+                                  int64_t N, int64_t K, int algo, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,6 +30,7 @@ __all__ = [
     "gemm_sign_repack", "gemm_sign_repack_thr", "flip_words", "gemm_signw_bf16", "chain3",
     "gemm_ex", "gemv_act", "version", "layernorm_fwd", "layernorm_bwd",
     "f8_row_bytes", "f8_scale_bytes", "quant_f8", "gemm_f8",
+    "gemm_signw_grouped",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -43,7 +44,8 @@ EXPORTED = ("bnn_words", "bnn_status_str", "bnn_version", "bnn_pack_signs", "bnn
             "bnn_gemm_u64_scaled", "bnn_gemm_sign_repack", "bnn_gemm_ex", "bnn_gemv_act",
             "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16", "bnn_chain3",
             "bnn_layernorm_fwd", "bnn_layernorm_bwd_workspace", "bnn_layernorm_bwd",
-            "bnn_f8_row_bytes", "bnn_f8_scale_bytes", "bnn_quant_f8", "bnn_gemm_f8")
+            "bnn_f8_row_bytes", "bnn_f8_scale_bytes", "bnn_quant_f8", "bnn_gemm_f8",
+            "bnn_gemm_signw_grouped")
 
 
 class BnnError(RuntimeError):
@@ -88,10 +90,11 @@ def library():
     lib.bnn_f8_scale_bytes.argtypes, lib.bnn_f8_scale_bytes.restype = [I64], I64
     lib.bnn_quant_f8.argtypes = [P, I, I64, I64, I64, I, P, P, P]
     lib.bnn_gemm_f8.argtypes = [P, P, P, P, P, I, I64, I64, I64, P]
+    lib.bnn_gemm_signw_grouped.argtypes = [P, I64, I64, P, P, P, P, P, P, I, I64, I64, I64, I64, I, P]
     for name in ("bnn_pack_signs", "bnn_gemm_u64", "bnn_gemm_u64_scaled", "bnn_gemm_sign_repack",
                  "bnn_gemm_ex", "bnn_gemv_act", "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16",
                  "bnn_chain3", "bnn_layernorm_fwd", "bnn_layernorm_bwd", "bnn_quant_f8",
-                 "bnn_gemm_f8"):
+                 "bnn_gemm_f8", "bnn_gemm_signw_grouped"):
         getattr(lib, name).restype = I
     _lib = lib
     return lib
@@ -525,3 +528,51 @@ def _real_out(M: int, N: int, dtype, device, out):
     if tuple(out.shape) != (M, N) or not out.is_contiguous() or out.device != device:
         raise ValueError(f"out must be a contiguous tensor of shape ({M}, {N}) on {device}")
     return out, dt
+
+
+def gemm_signw_grouped(x, wp, offsets, K=None, alpha=None, rows=None, row_scale=None,
+                       dtype=torch.float32, algo=ALGO_AUTO, out=None):
+    """``(R, N)`` sign-weight products grouped by expert
+    (bnn_gemm_signw_grouped): row r, ``offsets[e] <= r < offsets[e + 1]``, is
+    ``row_scale[r] * alpha[e] * (x[rows[r]] @ w[e].T)`` with real bf16
+    activations ``x`` (2-D CUDA tensor, unit stride along the last dimension;
+    the first ``K`` columns are used) and packed sign weights ``wp``, a
+    contiguous int64 tensor ``(E, N, words(K))``.  ``offsets`` is a contiguous
+    int32 CUDA tensor ``(E + 1,)``, non-decreasing (it is not read on the
+    host); ``rows`` None (row r is x's row r) or contiguous int32 ``(R,)``;
+    ``alpha`` None or contiguous float32 ``(E, N)``; ``row_scale`` None or
+    contiguous float32 ``(R,)``; ``dtype`` float32 or bfloat16; ``algo``
+    ALGO_AUTO, ALGO_GEMV or ALGO_MFMA.  Rows outside the groups are not
+    written."""
+    dt, xrows, cols, ldx = _real_rows("x", x)
+    if dt != BNN_BF16:
+        raise TypeError("x must be bfloat16")
+    K = cols if K is None else int(K)
+    if K > cols:
+        raise ValueError(f"x has {cols} columns, K={K}")
+    _need_cuda("wp", wp)
+    if wp.dtype != torch.int64 or wp.dim() != 3 or not wp.is_contiguous():
+        raise TypeError("wp must be a contiguous 3-D int64 tensor of packed words")
+    E, N, kw = wp.shape
+    if kw != words(K):
+        raise ValueError(f"wp has {kw} words per row, K={K} needs {words(K)}")
+    if wp.device != x.device:
+        raise ValueError("x and wp must be on the same device")
+    _vector("offsets", offsets, E + 1, x.device, torch.int32)
+    R = xrows
+    if rows is not None:
+        R = rows.shape[0] if isinstance(rows, torch.Tensor) and rows.dim() == 1 else -1
+        _vector("rows", rows, R, x.device, torch.int32)
+    if alpha is not None:
+        _need_cuda("alpha", alpha)
+        if (alpha.dtype != torch.float32 or tuple(alpha.shape) != (E, N)
+                or not alpha.is_contiguous() or alpha.device != x.device):
+            raise ValueError(f"alpha must be a contiguous float32 tensor of shape ({E}, {N})")
+    if row_scale is not None:
+        _vector("row_scale", row_scale, R, x.device)
+    out, dto = _real_out(R, N, dtype, x.device, out)
+    st = library().bnn_gemm_signw_grouped(_ptr(x), ldx, xrows, _ptr(rows), _ptr(offsets), _ptr(wp),
+                                          _ptr(alpha), _ptr(row_scale), _ptr(out), dto, R, E, N, K,
+                                          int(algo), _stream(x))
+    _check(st, "bnn_gemm_signw_grouped")
+    return out

@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;  // M, N, K, rows and ld limits
 constexpr int64_t kGemvMaxM = 8;               // AUTO picks the GEMV kernel up to here
+constexpr int64_t kMaxGroups = int64_t(1) << 20;  // experts of a grouped product
 
 bool misaligned(const void *p, uintptr_t a) { return ((uintptr_t)p) % a != 0; }
 
@@ -249,6 +250,29 @@ bnn_status bnn_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, 
   if (M == 0 || N == 0) return BNN_OK;
   return launch_status(bnn::launch_gemm_f8(xq, xs, wq, ws, y, dtype, M, N, K,
                                            static_cast<hipStream_t>(stream)));
+}
+
+bnn_status bnn_gemm_signw_grouped(const void *x, int64_t ldx, int64_t xrows, const int32_t *rows,
+                                  const int32_t *offsets, const uint64_t *wp, const float *alpha,
+                                  const float *row_scale, void *y, int dtype, int64_t R, int64_t E,
+                                  int64_t N, int64_t K, int algo, void *stream) {
+  if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
+  if (algo != BNN_ALGO_AUTO && algo != BNN_ALGO_GEMV && algo != BNN_ALGO_MFMA) return BNN_E_ARG;
+  if (R < 0 || E < 0 || N < 0 || K < 0 || xrows < 0 || R >= kMaxDim || N >= kMaxDim ||
+      K >= kMaxDim || xrows >= kMaxDim || E >= kMaxGroups || ldx < K || ldx >= kMaxDim ||
+      (!rows && xrows < R) || (xrows == 0 && R > 0))
+    return BNN_E_SHAPE;
+  const int64_t kw = bnn_words(K);
+  const bool any = R > 0 && E > 0 && N > 0;
+  if (any && (!offsets || !y || (K > 0 && !x) || (kw > 0 && !wp))) return BNN_E_NULL;
+  if (misaligned(x, 2) || misaligned(rows, 4) || misaligned(offsets, 4) || misaligned(wp, 8) ||
+      misaligned(alpha, 4) || misaligned(row_scale, 4) ||
+      misaligned(y, dtype == BNN_FP32 ? 4 : 2))
+    return BNN_E_ALIGN;
+  if (!any) return BNN_OK;
+  return launch_status(bnn::launch_signw_grouped(static_cast<const uint16_t *>(x), ldx, xrows, rows,
+                                                 offsets, wp, alpha, row_scale, y, dtype, R, E, N,
+                                                 K, algo, static_cast<hipStream_t>(stream)));
 }
 
 bnn_status bnn_gemm_u64(const uint64_t *xp, const uint64_t *wp, int32_t *y, int64_t M, int64_t N,

@@ -100,6 +100,12 @@ hipError_t launch_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *w
                           const uint8_t *ws, void *y, int dtype, int64_t M, int64_t N, int64_t K,
                           hipStream_t s);
 
+// Sign-weight products grouped by expert (bnn_gemm_signw_grouped).
+hipError_t launch_signw_grouped(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows,
+                                const int32_t *off, const uint64_t *wp, const float *alpha,
+                                const float *row_scale, void *y, int dtype, int64_t R, int64_t E,
+                                int64_t N, int64_t K, int algo, hipStream_t s);
+
 // Threshold-repack operands, loaded by the kernels before their K loops from
 // clamped (always in-bounds) indexes: the threshold of output column n, and
 // the flip word of 64-column group wi with its bits past column N cleared

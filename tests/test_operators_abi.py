@@ -107,3 +107,28 @@ def test_f8_bindings_refuse():
         bnn.quant_f8(x)
     with pytest.raises(TypeError):
         bnn.gemm_f8(x, x, x, x, 128)
+
+
+def test_signw_grouped_refusals(lib):
+    def f(x=FAKE, ldx=64, xrows=4, rows=None, off=FAKE, wp=FAKE, a=None, rs=None, y=FAKE, dt=0, R=4, E=2, N=3, K=64,
+          algo=0):
+        return lib.bnn_gemm_signw_grouped(x, ldx, xrows, rows, off, wp, a, rs, y, dt, R, E, N, K, algo, None)
+    assert f(dt=5) == E_DTYPE
+    assert f(algo=bnn.ALGO_TILED) == E_ARG and f(algo=9) == E_ARG
+    for kw in (dict(R=-1), dict(E=-1), dict(N=-1), dict(K=-1), dict(xrows=-1), dict(R=BIG, xrows=4), dict(N=BIG),
+               dict(K=BIG, ldx=BIG), dict(E=2 ** 20), dict(ldx=63), dict(ldx=BIG), dict(xrows=3),
+               dict(xrows=0, rows=FAKE), dict(xrows=BIG)):
+        assert f(**kw) == E_SHAPE, kw
+    for k in ("x", "off", "wp", "y"):
+        assert f(**{k: None}) == E_NULL, k
+    for kw in (dict(x=P(0x1001)), dict(rows=P(0x1002)), dict(off=P(0x1002)), dict(wp=P(0x1004)), dict(a=P(0x1002)),
+               dict(rs=P(0x1001)), dict(y=P(0x1002)), dict(y=P(0x1001), dt=1)):
+        assert f(**kw) == E_ALIGN, kw
+    none = dict(x=None, off=None, wp=None, y=None)
+    assert f(R=0, xrows=0, **none) == OK and f(E=0, **none) == OK and f(N=0, **none) == OK
+
+
+def test_signw_grouped_binding_refuses():
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        bnn.gemm_signw_grouped(x, torch.zeros(1, 3, 1, dtype=torch.int64), torch.zeros(2, dtype=torch.int32))
