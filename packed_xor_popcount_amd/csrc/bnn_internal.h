@@ -83,7 +83,8 @@ hipError_t launch_chain3(const void *x, int dtype, int64_t ldx, const uint64_t *
                          const Chain3Repack &rp, hipStream_t s);
 
 // Layer norm and its gradient (arguments as in the C-ABI).  The gradient's
-// column sums pass through `part`, layernorm_bwd_partials rows of 2 x N fp32.
+// column sums pass through `part`, layernorm_bwd_partials rows of 2 x N fp32
+// (none where they are taken in one launch).
 int64_t layernorm_bwd_partials(int64_t M, int64_t N);
 hipError_t launch_layernorm_fwd(const void *x, int dtype, int64_t ldx, const float *gamma,
                                 const float *beta, void *y, int64_t ldy, float *mean, float *rstd,
