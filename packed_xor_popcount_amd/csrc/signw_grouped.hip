@@ -25,22 +25,22 @@ typedef __bf16 bf16_t;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-// The 32 operands (+-0.5, natural order) of a 32-bit chunk: op[q] holds
-// elements 8q .. 8q + 7.
-__device__ __forceinline__ void half_signs(uint32_t c, bf16x8 op[4]) {
-  uint32_t s[8];
+// The upper bytes of a 32-bit chunk's 32 operands: byte q of s[p] belongs to
+// element 8q + p.
+__device__ __forceinline__ void sign_bytes(uint32_t c, uint32_t s[8]) {
 #pragma unroll
   for (int p = 0; p < 8; ++p) s[p] = ((c << (7 - p)) & 0x80808080u) | 0x3F3F3F3Fu;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint32_t sel = 0x040C000Cu + (uint32_t)q * 0x01000100u;
-    uint4 r;
-    r.x = __builtin_amdgcn_perm(s[1], s[0], sel);
-    r.y = __builtin_amdgcn_perm(s[3], s[2], sel);
-    r.z = __builtin_amdgcn_perm(s[5], s[4], sel);
-    r.w = __builtin_amdgcn_perm(s[7], s[6], sel);
-    op[q] = __builtin_bit_cast(bf16x8, r);
-  }
+}
+
+// Operands (+-0.5) of elements 8q .. 8q + 7.
+__device__ __forceinline__ bf16x8 sign_operand(const uint32_t s[8], int q) {
+  const uint32_t sel = 0x040C000Cu + (uint32_t)q * 0x01000100u;
+  uint4 r;
+  r.x = __builtin_amdgcn_perm(s[1], s[0], sel);
+  r.y = __builtin_amdgcn_perm(s[3], s[2], sel);
+  r.z = __builtin_amdgcn_perm(s[5], s[4], sel);
+  r.w = __builtin_amdgcn_perm(s[7], s[6], sel);
+  return __builtin_bit_cast(bf16x8, r);
 }
 
 // Row range of group e, whatever the offsets hold: 0 <= lo <= hi <= T.
@@ -82,71 +82,202 @@ __device__ __forceinline__ bool find_tile(const int32_t *off, int E, int T, int6
   return false;
 }
 
-// One 32 x 32 tile per wave, operands straight from memory.
-template <typename T>
-__global__ void __launch_bounds__(256)
+// ---------------------------------------------------------------------------
+// Matrix-core kernel.  Eight waves side by side along N, each RB x CB tiles of
+// 32 x 32, two waves per SIMD: one wave's sign operands are made while the
+// other's matrix instructions run.  The weights need next to no bytes, so the
+// tile is wide (every activation row read from L2 serves 8 CB 32 columns) and
+// low (few rows are wasted at a group's end).
+//
+// Per 64-element step the block's activation rows (128 bytes each, their
+// 16-byte pieces swapped by row so that the reads spread over the banks) and
+// its columns' weight words pass through one of two LDS buffers; the step
+// after is on its way through registers, loaded at any alignment, zero past
+// K.  Bound by the bf16 matrix rate.
+
+constexpr int kGroupThreads = 512;
+
+template <int RB, int CB, typename T>
+__global__ void __launch_bounds__(kGroupThreads, 2)
     signw_grouped_kernel(const uint16_t *__restrict__ x, int64_t ldx, int xrows,
                          const int32_t *__restrict__ rows, const int32_t *__restrict__ off,
                          const uint64_t *__restrict__ wp, const float *__restrict__ alpha,
                          const float *__restrict__ row_scale, T *__restrict__ y, int R, int E,
-                         int N, int K) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+                         int N, int K, int tiles_n, int64_t most) {
+  constexpr int BM = RB * 32, BN = 8 * CB * 32;
+  constexpr int PIECES = BM * 8 / kGroupThreads;  // 16-byte pieces a thread stages
+  static_assert(PIECES >= 1 && BN <= kGroupThreads, "every thread stages");
+  __shared__ __attribute__((aligned(16))) unsigned char as[2][BM * 128];
+  __shared__ __attribute__((aligned(16))) uint64_t ws[2][BN];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, h = lane >> 5;
-  const int kw = (K + 63) / 64;
-  const int tiles_n = (N + 63) / 64;
-  for (int64_t tile = blockIdx.x;; tile += gridDim.x) {
+  const int kw = (K + 63) / 64, nfull = K / 64;
+
+  // Tiles: consecutive blocks go to the eight XCDs in turn, so block b takes a
+  // row tile of its XCD's own (b % 8) and walks along N first: an XCD's L2
+  // then reads an activation row once.
+  for (int64_t b = blockIdx.x; b < most; b += gridDim.x) {
+    const int64_t u = b >> 3;
+    const int tn = (int)(u % tiles_n);
     int e, r0, hi;
-    if (!find_tile<64>(off, E, R, tile / tiles_n, e, r0, hi)) return;
-    r0 += (wave >> 1) * 32;
-    const int n0 = (int)(tile % tiles_n) * 64 + (wave & 1) * 32;
-    const int r = r0 + li < hi ? r0 + li : hi - 1, n = n0 + li < N ? n0 + li : N - 1;
-    int src = rows ? rows[r] : r;
-    src = src < 0 ? 0 : (src < xrows ? src : xrows - 1);
-    const uint16_t *xr = x + src * ldx + 32 * h;
-    const uint64_t *wr = wp + ((int64_t)e * N + n) * kw;
-    v16f acc;
+    if (!find_tile<BM>(off, E, R, (u / tiles_n) * 8 + (b & 7), e, r0, hi)) continue;
+    const int n0 = tn * BN + wave * (CB * 32);
+
+    const uint16_t *xr[PIECES];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
-    for (int w = 0; w < kw; ++w) {
-      bf16x8 b[4];
-      half_signs((uint32_t)(wr[w] >> (32 * h)), b);
+    for (int i = 0; i < PIECES; ++i) {
+      int r = r0 + (tid >> 3) + i * (kGroupThreads / 8);
+      r = r < hi ? r : hi - 1;
+      int src = rows ? rows[r] : r;
+      src = src < 0 ? 0 : (src < xrows ? src : xrows - 1);
+      xr[i] = x + src * ldx + 8 * (tid & 7);
+    }
+    const uint64_t *wr;
+    {
+      int n = tn * BN + (tid < BN ? tid : BN - 1);
+      n = n < N ? n : N - 1;
+      wr = wp + ((int64_t)e * N + n) * kw;
+    }
+    struct Stage {
+      uint4 a[PIECES];
+      uint64_t w;
+    };
+    auto load = [&](int s, Stage &st) __attribute__((always_inline)) {  // a whole step
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) __builtin_memcpy(&st.a[i], xr[i] + 64 * (int64_t)s, 16);
+      st.w = wr[s];
+    };
+    auto load_tail = [&](Stage &st) __attribute__((always_inline)) {  // the last, partial one
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (64 * nfull + 8 * (tid & 7) + j < K)
+            v[j / 2] |= (uint32_t)xr[i][64 * (int64_t)nfull + j] << (16 * (j & 1));
+        st.a[i] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+      st.w = wr[nfull];
+    };
+    auto stage = [&](const Stage &st, int buf) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int row = (tid >> 3) + i * (kGroupThreads / 8);
+        *reinterpret_cast<uint4 *>(as[buf] + row * 128 + (((tid & 7) ^ (row & 7)) << 4)) = st.a[i];
+      }
+      if (BN == kGroupThreads || tid < BN) ws[buf][tid] = st.w;
+    };
+    v16f acc[RB][CB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[rb][cb][v] = 0.0f;
+    auto compute = [&](int buf) __attribute__((always_inline)) {
+      uint32_t sg[CB][8];
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+        sign_bytes(reinterpret_cast<const uint32_t *>(ws[buf])[2 * (wave * CB * 32 + cb * 32 + li) + h],
+                   sg[cb]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        uint16_t a[8];
+        bf16x8 a[RB], bo[CB];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int k = 64 * w + 8 * t + j;
-          a[j] = k + 32 * h < K ? xr[k] : (uint16_t)0;
-        }
-        bf16x8 av;
-        __builtin_memcpy(&av, a, 16);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, b[t], acc, 0, 0, 0);
+        for (int rb = 0; rb < RB; ++rb)
+          a[rb] = __builtin_bit_cast(
+              bf16x8, *reinterpret_cast<const uint4 *>(as[buf] + (rb * 32 + li) * 128 +
+                                                       (((4 * h + t) ^ (li & 7)) << 4)));
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) bo[cb] = sign_operand(sg[cb], t);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb)
+            acc[rb][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[rb], bo[cb], acc[rb][cb], 0, 0, 0);
       }
+    };
+
+    // Loads past the last whole step read it again (in bounds, not used), so
+    // that the loop has no branches and its waits are exact.
+    Stage sa, sb;
+    __syncthreads();  // the last tile's reads of LDS are done
+    if (nfull > 0) {
+      const int last = nfull - 1;
+      load(0, sa);
+      load(last < 1 ? last : 1, sb);
+      stage(sa, 0);
+      __syncthreads();
+      for (int s = 0; s + 1 < nfull; s += 2) {
+        stage(sb, 1);
+        load(s + 2 < last ? s + 2 : last, sa);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(0);
+        __syncthreads();
+        stage(sa, 0);
+        load(s + 3 < last ? s + 3 : last, sb);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(1);
+        __syncthreads();
+      }
+      if (nfull & 1) compute(0);
     }
-    if (n0 + li < N) {
-      const float al = 2.0f * (alpha ? alpha[(int64_t)e * N + n] : 1.0f);
+    if (nfull < kw) {
+      load_tail(sa);
+      __syncthreads();
+      stage(sa, 0);
+      __syncthreads();
+      compute(0);
+    }
+
+    float al[CB];
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+      int n = n0 + cb * 32 + li;
+      n = n < N ? n : N - 1;
+      al[cb] = 2.0f * (alpha ? alpha[(int64_t)e * N + n] : 1.0f);
+    }
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const int rr = r0 + 8 * (v >> 2) + 4 * h + (v & 3);
-        if (rr < hi) {
-          float o = acc[v] * al;
-          if (row_scale) o *= row_scale[rr];
-          y[(int64_t)rr * N + n] = (T)o;
-        }
+        const int r = r0 + rb * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
+        if (r >= hi) continue;
+        const float rs = row_scale ? row_scale[r] : 1.0f;
+        T *yr = y + (int64_t)r * N + n0 + li;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          if (n0 + cb * 32 + li < N) yr[cb * 32] = (T)(acc[rb][cb][v] * al[cb] * rs);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+}
+
+template <int RB, int CB, typename T>
+void launch_tile(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows,
+                 const int32_t *off, const uint64_t *wp, const float *alpha,
+                 const float *row_scale, void *y, int64_t R, int64_t E, int64_t N, int64_t K,
+                 hipStream_t s) {
+  constexpr int BM = RB * 32, BN = 8 * CB * 32;
+  const int64_t tiles_n = (N + BN - 1) / BN;
+  // Row tiles of any grouping of R rows: the whole ones and one partial tile
+  // for each group that has rows; a multiple of the eight XCDs.
+  const int64_t tiles_m = (R / BM + (E < R ? E : R) + 7) / 8 * 8;
+  const int64_t most = tiles_m * tiles_n;
+  const int64_t blocks = most < (1 << 20) ? most : (1 << 20);
+  hipLaunchKernelGGL((signw_grouped_kernel<RB, CB, T>), dim3((unsigned)blocks),
+                     dim3(kGroupThreads), 0, s, x, ldx, (int)xrows, rows, off, wp, alpha, row_scale,
+                     static_cast<T *>(y), (int)R, (int)E, (int)N, (int)K, (int)tiles_n, most);
 }
 
 template <typename T>
 void launch(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows, const int32_t *off,
             const uint64_t *wp, const float *alpha, const float *row_scale, void *y, int64_t R,
             int64_t E, int64_t N, int64_t K, hipStream_t s) {
-  const int64_t tiles = (R / 64 + (E < R ? E : R)) * ((N + 63) / 64);
-  const int64_t blocks = tiles < (1 << 16) ? tiles : (1 << 16);
-  hipLaunchKernelGGL((signw_grouped_kernel<T>), dim3((unsigned)blocks), dim3(256), 0, s, x, ldx,
-                     (int)xrows, rows, off, wp, alpha, row_scale, static_cast<T *>(y), (int)R,
-                     (int)E, (int)N, (int)K);
+  const auto run = R / E >= 128 && N > 256 ? launch_tile<4, 2, T> : launch_tile<2, 1, T>;
+  run(x, ldx, xrows, rows, off, wp, alpha, row_scale, y, R, E, N, K, s);
 }
 
 }  // namespace
