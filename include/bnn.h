@@ -408,8 +408,8 @@ bnn_status bnn_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int
  *            zero in both (as bnn_quant_f8 writes them).
  *   y        M x N of type dtype (BNN_FP32 / BNN_BF16), row-major,
  *            element-aligned.
- * K = 0 gives y = 0.  Errors: BNN_E_DTYPE, BNN_E_SHAPE, BNN_E_NULL,
- * BNN_E_ALIGN, BNN_E_LAUNCH.
+ * K = 0 gives y = 0; K <= 2^24 (else BNN_E_SHAPE).  Errors: BNN_E_DTYPE,
+ * BNN_E_SHAPE, BNN_E_NULL, BNN_E_ALIGN, BNN_E_LAUNCH.
  */
 bnn_status bnn_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
                        void *y, int dtype, int64_t M, int64_t N, int64_t K, void *stream);

@@ -241,7 +241,8 @@ bnn_status bnn_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int
 bnn_status bnn_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
                        void *y, int dtype, int64_t M, int64_t N, int64_t K, void *stream) {
   if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
-  if (M < 0 || N < 0 || K < 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return BNN_E_SHAPE;
+  if (M < 0 || N < 0 || K < 0 || M >= kMaxDim || N >= kMaxDim || K > bnn::kF8MaxK)
+    return BNN_E_SHAPE;
   if ((M * K > 0 && (!xq || !xs)) || (N * K > 0 && (!wq || !ws)) || (M * N > 0 && !y))
     return BNN_E_NULL;
   if (misaligned(xq, 16) || misaligned(wq, 16) || misaligned(xs, 4) || misaligned(ws, 4) ||

@@ -16,6 +16,7 @@
 namespace bnn {
 
 constexpr int kF8Block = 128;
+constexpr int64_t kF8MaxK = int64_t(1) << 24;  // columns of a product's operands
 
 __host__ __device__ inline int64_t f8_blocks(int64_t k) { return (k + kF8Block - 1) / kF8Block; }
 __host__ __device__ inline int64_t f8_row_bytes(int64_t k) { return f8_blocks(k) * kF8Block; }

@@ -35,14 +35,6 @@ __device__ __forceinline__ v16f mfma_f8(v8i a, v8i b, v16f c, int sa, int sb) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
 }
 
-__device__ __forceinline__ v8i load32(const uint8_t *p) {
-  const int4 a = reinterpret_cast<const int4 *>(p)[0], b = reinterpret_cast<const int4 *>(p)[1];
-  v8i r;
-  r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
-  r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
-  return r;
-}
-
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -58,62 +50,214 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi, float scale) 
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// acc += the products of 32 bytes of A and B per lane.
-template <bool WIDE>
-__device__ __forceinline__ v16f step(v8i a, v8i b, v16f acc, int sa, int sb) {
-  if (!WIDE) return mfma_f8(a, b, acc, sa, sb);
-  const float fa = pow2_of(sa), fb = pow2_of(sb);
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8(a[2 * t], a[2 * t + 1], fa),
-                                                  widen8(b[2 * t], b[2 * t + 1], fb), acc, 0, 0, 0);
-  return acc;
+// ---------------------------------------------------------------------------
+// Tiled kernel: WR x WC = 8 waves, each RB x CB tiles of 32 x 32, two waves per
+// SIMD.  Per block of 128 elements of K (one scale) the tile's rows of both
+// operands go straight from memory into one of two LDS buffers (the format
+// keeps rows 16-byte aligned) while the other one is multiplied.  The 16-byte
+// pieces of a row are swapped by the row's number, so that the reads spread
+// over the banks.  Each lane loads the scale bytes of its rows with them.
+
+constexpr int kF8Threads = 512;
+
+// 16 bytes per lane from base + off to LDS at lds + 16 * lane, past the
+// registers (lds: a wave-uniform LDS byte address).  Counted by vmcnt;
+// lds_loads_done waits for all of them.
+__device__ __forceinline__ void load_to_lds(const uint8_t *base, uint32_t off, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(lds), "v"(off), "s"(base)
+      : "memory");
+}
+__device__ __forceinline__ void lds_loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
-// One 32 x 32 tile per wave, operands straight from memory.
-template <typename T>
-__global__ void __launch_bounds__(256)
+template <int WR, int WC, int RB, int CB, typename T>
+__global__ void __launch_bounds__(kF8Threads, 2)
     gemm_f8_kernel(const uint8_t *__restrict__ xq, const uint8_t *__restrict__ xs,
                    const uint8_t *__restrict__ wq, const uint8_t *__restrict__ ws,
-                   T *__restrict__ y, int M, int N, int nb, int sb) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+                   T *__restrict__ y, int M, int N, int nb, int sb, int tiles_m, int64_t tiles) {
+  static_assert(WR * WC == 8, "eight waves");
+  constexpr bool WIDE = sizeof(T) == 4;
+  constexpr int BM = WR * RB * 32, BN = WC * CB * 32;
+  constexpr int PA = BM * 8 / kF8Threads, PB = BN * 8 / kF8Threads;  // loads of a thread per step
+  static_assert(PA >= 1 && PB >= 1, "every thread stages");
+  __shared__ __attribute__((aligned(16))) unsigned char as[2][BM * 128], bs[2][BN * 128];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, h = lane >> 5;
-  const int64_t tiles_m = (M + 63) / 64, tiles = tiles_m * ((N + 63) / 64);
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int m0 = (int)(tile % tiles_m) * 64 + (wave >> 1) * 32;
-    const int n0 = (int)(tile / tiles_m) * 64 + (wave & 1) * 32;
-    const int m = m0 + li < M ? m0 + li : M - 1, n = n0 + li < N ? n0 + li : N - 1;
-    const uint8_t *xr = xq + (int64_t)m * nb * kF8Block + 32 * h;
-    const uint8_t *wr = wq + (int64_t)n * nb * kF8Block + 32 * h;
-    const uint8_t *xsr = xs + (int64_t)m * sb, *wsr = ws + (int64_t)n * sb;
-    v16f acc;
+  const int wm = (wave / WC) * (RB * 32), wn = (wave % WC) * (CB * 32);
+  const int64_t ldq = (int64_t)nb * kF8Block;
+
+  for (int64_t b = blockIdx.x; b < tiles; b += gridDim.x) {
+    // Block b runs on XCD b % 8: each XCD takes a contiguous range of tiles.
+    const int64_t per = tiles >> 3;
+    const int64_t tile = (tiles & 7) == 0 ? (b & 7) * per + (b >> 3) : b;
+    const int m0 = (int)(tile % tiles_m) * BM, n0 = (int)(tile / tiles_m) * BN;
+
+    // Row offsets inside a tile fit 32 bits: 256 rows of at most 2^24 bytes.
+    // Thread tid fills place tid + 512 i of the tile's pieces: row tid / 8 + 64 i,
+    // place tid % 8, which holds piece (tid % 8) ^ (row % 8).
+    const uint8_t *xt = xq + m0 * ldq, *wt = wq + n0 * ldq;
+    const uint8_t *xst = xs + (int64_t)m0 * sb, *wst = ws + (int64_t)n0 * sb;
+    const uint32_t piece = 16 * ((tid & 7) ^ ((tid >> 3) & 7));
+    uint32_t ox[PA], ow[PB], osx[RB], osw[CB];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
-    for (int b = 0; b < nb; ++b) {
-      const int sa = xsr[b], sw = wsr[b];
-      const int64_t o = (int64_t)b * kF8Block;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        acc = step<sizeof(T) == 4>(load32(xr + o + 64 * t), load32(wr + o + 64 * t), acc, sa, sw);
+    for (int i = 0; i < PA; ++i) {
+      const int r = (tid >> 3) + i * (kF8Threads / 8);
+      ox[i] = (uint32_t)(m0 + r < M ? r : M - 1 - m0) * (uint32_t)ldq + piece;
     }
-    if (n0 + li < N) {
+#pragma unroll
+    for (int i = 0; i < PB; ++i) {
+      const int r = (tid >> 3) + i * (kF8Threads / 8);
+      ow[i] = (uint32_t)(n0 + r < N ? r : N - 1 - n0) * (uint32_t)ldq + piece;
+    }
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int r = wm + i * 32 + li;
+      osx[i] = (uint32_t)(m0 + r < M ? r : M - 1 - m0) * (uint32_t)sb;
+    }
+#pragma unroll
+    for (int i = 0; i < CB; ++i) {
+      const int r = wn + i * 32 + li;
+      osw[i] = (uint32_t)(n0 + r < N ? r : N - 1 - n0) * (uint32_t)sb;
+    }
+    auto load = [&](int s, int buf) __attribute__((always_inline)) {
+      const uint32_t la = lds_address(as[buf]) + wave * 1024;
+      const uint32_t lb = lds_address(bs[buf]) + wave * 1024;
+      const uint8_t *xb = xt + (int64_t)s * kF8Block, *wb = wt + (int64_t)s * kF8Block;
+#pragma unroll
+      for (int i = 0; i < PA; ++i) load_to_lds(xb, ox[i], la + i * (kF8Threads * 16));
+#pragma unroll
+      for (int i = 0; i < PB; ++i) load_to_lds(wb, ow[i], lb + i * (kF8Threads * 16));
+    };
+    auto frag = [&](const unsigned char *buf, int row, int t) __attribute__((always_inline)) {
+      const int p0 = ((4 * t + 2 * h) ^ (li & 7)) << 4, p1 = ((4 * t + 2 * h + 1) ^ (li & 7)) << 4;
+      const uint4 lo = *reinterpret_cast<const uint4 *>(buf + row * 128 + p0);
+      const uint4 hi = *reinterpret_cast<const uint4 *>(buf + row * 128 + p1);
+      return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,
+                 (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    v16f acc[RB][CB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    uint32_t ca[RB], cw[CB], na[RB], nw[CB];  // scale bytes of this and the next block
+    auto load_scales = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < RB; ++i) na[i] = (xst + s)[osx[i]];
+#pragma unroll
+      for (int i = 0; i < CB; ++i) nw[i] = (wst + s)[osw[i]];
+    };
+    auto arrived = [&]() __attribute__((always_inline)) {  // the next block is in place
+      lds_loads_done();
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < RB; ++i) ca[i] = na[i];
+#pragma unroll
+      for (int i = 0; i < CB; ++i) cw[i] = nw[i];
+    };
+    auto compute = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        v8i fa[RB], fb[CB];
+#pragma unroll
+        for (int j = 0; j < CB; ++j) fb[j] = frag(bs[buf], wn + j * 32 + li, t);
+#pragma unroll
+        for (int i = 0; i < RB; ++i) fa[i] = frag(as[buf], wm + i * 32 + li, t);
+        if (!WIDE) {
+#pragma unroll
+          for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < CB; ++j)
+              acc[i][j] = mfma_f8(fa[i], fb[j], acc[i][j], (int)ca[i], (int)cw[j]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            bf16x8 va[RB], vb[CB];
+#pragma unroll
+            for (int j = 0; j < CB; ++j)
+              vb[j] = widen8(fb[j][2 * k], fb[j][2 * k + 1], pow2_of(cw[j] & 255));
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+              va[i] = widen8(fa[i][2 * k], fa[i][2 * k + 1], pow2_of(ca[i] & 255));
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+              for (int j = 0; j < CB; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[i], vb[j], acc[i][j], 0, 0, 0);
+          }
+        }
+      }
+    };
+    __syncthreads();  // the last tile's reads of LDS are done
+    if (nb > 0) {
+      load(0, 0);
+      load_scales(0);
+      arrived();
+      const int last = nb - 1;
+      int s = 0;
+      for (; s + 2 <= last; s += 2) {
+        load(s + 1, 1);
+        load_scales(s + 1);
+        compute(0);
+        arrived();
+        load(s + 2, 0);
+        load_scales(s + 2);
+        compute(1);
+        arrived();
+      }
+      if (s < last) {
+        load(last, 1);
+        load_scales(last);
+        compute(0);
+        arrived();
+      }
+      compute(last & 1);
+    }
+
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const int mm = m0 + 8 * (v >> 2) + 4 * h + (v & 3);
-        if (mm < M) y[(int64_t)mm * N + n0 + li] = (T)acc[v];
+        const int m = m0 + wm + i * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
+        if (m >= M) continue;
+        T *yr = y + (int64_t)m * N + n0 + wn + li;
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
+          if (n0 + wn + j * 32 + li < N) yr[j * 32] = (T)acc[i][j][v];
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+}
+
+template <int WR, int WC, int RB, int CB, typename T>
+void launch_tile(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                 void *y, int64_t M, int64_t N, int64_t K, hipStream_t s) {
+  constexpr int BM = WR * RB * 32, BN = WC * CB * 32;
+  const int64_t tiles_m = (M + BM - 1) / BM, tiles = tiles_m * ((N + BN - 1) / BN);
+  const int64_t blocks = tiles < (1 << 20) ? tiles : (1 << 20);
+  hipLaunchKernelGGL((gemm_f8_kernel<WR, WC, RB, CB, T>), dim3((unsigned)blocks), dim3(kF8Threads),
+                     0, s, xq, xs, wq, ws, static_cast<T *>(y), (int)M, (int)N,
+                     (int)f8_blocks(K), (int)f8_scale_bytes(K), (int)tiles_m, tiles);
 }
 
 template <typename T>
 void launch(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws, void *y,
             int64_t M, int64_t N, int64_t K, hipStream_t s) {
-  const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64);
-  const int64_t blocks = tiles < (1 << 20) ? tiles : (1 << 20);
-  hipLaunchKernelGGL((gemm_f8_kernel<T>), dim3((unsigned)blocks), dim3(256), 0, s, xq, xs, wq,
-                     ws, static_cast<T *>(y), (int)M, (int)N, (int)f8_blocks(K),
-                     (int)f8_scale_bytes(K));
+  const bool large = ((M + 255) / 256) * ((N + 255) / 256) >= 128;
+  const auto run = large ? launch_tile<2, 4, 4, 2, T> : launch_tile<2, 4, 1, 1, T>;
+  run(xq, xs, wq, ws, y, M, N, K, s);
 }
 
 }  // namespace

@@ -91,7 +91,8 @@ def test_gemm_f8_refusals(lib):
     def f(xq=FAKE, xs=FAKE, wq=FAKE, ws=FAKE, y=FAKE, dt=0, M=2, N=3, K=8):
         return lib.bnn_gemm_f8(xq, xs, wq, ws, y, dt, M, N, K, None)
     assert f(dt=3) == E_DTYPE
-    for kw in (dict(M=-1), dict(N=-1), dict(K=-1), dict(M=BIG), dict(N=BIG), dict(K=BIG)):
+    for kw in (dict(M=-1), dict(N=-1), dict(K=-1), dict(M=BIG), dict(N=BIG), dict(K=BIG),
+               dict(K=2 ** 24 + 1)):
         assert f(**kw) == E_SHAPE, kw
     for k in ("xq", "xs", "wq", "ws", "y"):
         assert f(**{k: None}) == E_NULL, k
