@@ -441,8 +441,9 @@ bnn_status bnn_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, 
  *   alpha    E x N fp32 scales, or NULL (1).  row_scale  R fp32, or NULL (1).
  *   y        R x N of type dtype (BNN_FP32 / BNN_BF16), row-major.
  *   algo     BNN_ALGO_AUTO; BNN_ALGO_GEMV (few rows per group: streams the
- *            weights of each group once per 8 of its rows); or BNN_ALGO_MFMA
- *            (matrix cores).  BNN_ALGO_TILED -> BNN_E_ARG.
+ *            weights of each group once per 16 to 64 of its rows); or
+ *            BNN_ALGO_MFMA (large tiles).  Any grouping is served by both; AUTO
+ *            goes by the mean R / E.  BNN_ALGO_TILED -> BNN_E_ARG.
  * R = 0, E = 0 or N = 0 launches nothing; K = 0 gives y = 0 in the groups'
  * rows.  E < 2^20.  Errors: BNN_E_DTYPE, BNN_E_ARG, BNN_E_SHAPE, BNN_E_NULL,
  * BNN_E_ALIGN, BNN_E_LAUNCH.

@@ -241,6 +241,92 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few-row kernel: 16 columns x 16 RM rows per block, the blocks of K dealt out
+// to the block's waves and their sums joined through LDS in a fixed order.
+// Every wave streams its part of the weight rows from memory exactly once, so
+// small products keep the whole card busy; bound by the weights' bytes.
+// Always on bf16 instructions: the matrix rate does not matter here.
+//
+// v_mfma_f32_16x16x32_bf16: lane l supplies row / column l % 16; lane group
+// l / 16 takes bytes 32 (l / 16) .. + 31 of a block of 128, eight per
+// instruction.  Output: register v -> row 4 (l / 16) + v, column l % 16.
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+template <int RM, typename T>
+__global__ void __launch_bounds__(1024)
+    gemm_f8_rows_kernel(const uint8_t *__restrict__ xq, const uint8_t *__restrict__ xs,
+                        const uint8_t *__restrict__ wq, const uint8_t *__restrict__ ws,
+                        T *__restrict__ y, int M, int N, int nb, int sb, int64_t tiles_n,
+                        int64_t tiles) {
+  __shared__ float join[16][256];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int li = lane & 15, g = lane >> 4;
+  const int64_t ldq = (int64_t)nb * kF8Block;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int n0 = (int)(tile % tiles_n) * 16, m0 = (int)(tile / tiles_n) * (16 * RM);
+    const int n = n0 + li < N ? n0 + li : N - 1;
+    const uint8_t *wr = wq + n * ldq + 32 * g, *wsr = ws + (int64_t)n * sb;
+    const uint8_t *xr[RM], *xsr[RM];
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      const int m = m0 + i * 16 + li < M ? m0 + i * 16 + li : M - 1;
+      xr[i] = xq + m * ldq + 32 * g;
+      xsr[i] = xs + (int64_t)m * sb;
+    }
+    v4f acc[RM];
+#pragma unroll
+    for (int i = 0; i < RM; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = wave; b < nb; b += waves) {
+      const int64_t o = (int64_t)b * kF8Block;
+      const v4u w0 = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wr + o));
+      const v4u w1 = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wr + o + 16));
+      const float sw = pow2_of(wsr[b]);
+      const bf16x8 vb[4] = {widen8(w0.x, w0.y, sw), widen8(w0.z, w0.w, sw),
+                            widen8(w1.x, w1.y, sw), widen8(w1.z, w1.w, sw)};
+#pragma unroll
+      for (int i = 0; i < RM; ++i) {
+        const v4u a0 = *reinterpret_cast<const v4u *>(xr[i] + o);
+        const v4u a1 = *reinterpret_cast<const v4u *>(xr[i] + o + 16);
+        const float sx = pow2_of(xsr[i][b]);
+        const bf16x8 va[4] = {widen8(a0.x, a0.y, sx), widen8(a0.z, a0.w, sx),
+                              widen8(a1.x, a1.y, sx), widen8(a1.z, a1.w, sx)};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va[k], vb[k], acc[i], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      __syncthreads();  // join is free
+#pragma unroll
+      for (int v = 0; v < 4; ++v) join[wave][(4 * g + v) * 16 + li] = acc[i][v];
+      __syncthreads();
+      for (int e = threadIdx.x; e < 256; e += blockDim.x) {
+        float sum = 0.0f;
+        for (int w = 0; w < waves; ++w) sum += join[w][e];
+        const int m = m0 + i * 16 + (e >> 4), c = n0 + (e & 15);
+        if (m < M && c < N) y[(int64_t)m * N + c] = (T)sum;
+      }
+    }
+  }
+}
+
+template <int RM, typename T>
+void launch_rows(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                 void *y, int64_t M, int64_t N, int64_t K, hipStream_t s) {
+  const int64_t tiles_n = (N + 15) / 16, tiles = tiles_n * ((M + 16 * RM - 1) / (16 * RM));
+  const int64_t blocks = tiles < (1 << 20) ? tiles : (1 << 20);
+  const int64_t nb = f8_blocks(K);
+  const int waves = nb >= 16 ? 16 : (nb < 1 ? 1 : (int)nb);
+  hipLaunchKernelGGL((gemm_f8_rows_kernel<RM, T>), dim3((unsigned)blocks), dim3(64 * waves), 0, s,
+                     xq, xs, wq, ws, static_cast<T *>(y), (int)M, (int)N, (int)nb,
+                     (int)f8_scale_bytes(K), tiles_n, tiles);
+}
+
 template <int WR, int WC, int RB, int CB, typename T>
 void launch_tile(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
                  void *y, int64_t M, int64_t N, int64_t K, hipStream_t s) {
@@ -255,8 +341,12 @@ void launch_tile(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const 
 template <typename T>
 void launch(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws, void *y,
             int64_t M, int64_t N, int64_t K, hipStream_t s) {
-  const bool large = ((M + 255) / 256) * ((N + 255) / 256) >= 128;
-  const auto run = large ? launch_tile<2, 4, 4, 2, T> : launch_tile<2, 4, 1, 1, T>;
+  const auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  auto run = launch_tile<2, 4, 4, 2, T>;
+  if (M <= 16) run = launch_rows<1, T>;
+  else if (M <= 32) run = launch_rows<2, T>;
+  else if (M <= 64 || tiles(64, 128) < 128) run = launch_rows<4, T>;
+  else if (tiles(256, 256) < 128) run = launch_tile<2, 4, 1, 1, T>;
   run(xq, xs, wq, ws, y, M, N, K, s);
 }
 

@@ -255,6 +255,125 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few-row kernel: 16 columns x 16 RM rows of a group per block, steps of 512
+// elements of K dealt out to the block's waves, their sums joined through LDS
+// in a fixed order.  Each weight word is read once per 16 RM rows of its group,
+// by 16-byte loads of 16 columns at a time, and groups without rows are not
+// touched; bound by the active groups' weight bytes and, for one token, by
+// the launch.
+//
+// v_mfma_f32_16x16x32_bf16: lane l supplies row / column l % 16; lane group
+// g = l / 16 takes elements 128 g .. 128 g + 127 of a step, eight per
+// instruction.  Output: register v -> row 4 g + v, column l % 16.
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+template <int RM, typename T>
+__global__ void __launch_bounds__(512)
+    signw_grouped_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, int xrows,
+                              const int32_t *__restrict__ rows, const int32_t *__restrict__ off,
+                              const uint64_t *__restrict__ wp, const float *__restrict__ alpha,
+                              const float *__restrict__ row_scale, T *__restrict__ y, int R, int E,
+                              int N, int K, int tiles_n, int64_t most) {
+  __shared__ float join[8][256];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int li = lane & 15, g = lane >> 4;
+  const int kw = (K + 63) / 64, steps = (K + 511) / 512;
+  for (int64_t tile = blockIdx.x; tile < most; tile += gridDim.x) {
+    int e, r0, hi;
+    if (!find_tile<16 * RM>(off, E, R, tile / tiles_n, e, r0, hi)) return;
+    const int n0 = (int)(tile % tiles_n) * 16;
+    const int n = n0 + li < N ? n0 + li : N - 1;
+    const uint64_t *wr = wp + ((int64_t)e * N + n) * kw;
+    const uint16_t *xr[RM];
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      const int r = r0 + i * 16 + li < hi ? r0 + i * 16 + li : hi - 1;
+      int src = rows ? rows[r] : r;
+      src = src < 0 ? 0 : (src < xrows ? src : xrows - 1);
+      xr[i] = x + src * ldx;
+    }
+    v4f acc[RM];
+#pragma unroll
+    for (int i = 0; i < RM; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int st = wave; st < steps; st += waves) {
+      const int k0 = 512 * st + 128 * g;
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (k0 + 128 <= K) {
+        __builtin_memcpy(w, wr + k0 / 64, 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (k0 + 64 * j < K) __builtin_memcpy(w + 2 * j, wr + k0 / 64 + j, 8);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t sg[8];
+        sign_bytes(w[c], sg);
+        uint4 a[RM][4];
+        if (k0 + 32 * c + 32 <= K) {
+#pragma unroll
+          for (int i = 0; i < RM; ++i) __builtin_memcpy(a[i], xr[i] + k0 + 32 * c, 64);
+        } else {  // zero past K
+#pragma unroll
+          for (int i = 0; i < RM; ++i) {
+            uint32_t v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int k = k0 + 32 * c + 2 * j;
+              v[j] = k < K ? xr[i][k] : 0u;
+              v[j] |= k + 1 < K ? (uint32_t)xr[i][k + 1] << 16 : 0u;
+            }
+            __builtin_memcpy(a[i], v, 64);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bf16x8 b = sign_operand(sg, q);
+#pragma unroll
+          for (int i = 0; i < RM; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i][q]), b,
+                                                             acc[i], 0, 0, 0);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      __syncthreads();  // join is free
+#pragma unroll
+      for (int v = 0; v < 4; ++v) join[wave][(4 * g + v) * 16 + li] = acc[i][v];
+      __syncthreads();
+      for (int q = threadIdx.x; q < 256; q += blockDim.x) {
+        float sum = 0.0f;
+        for (int w = 0; w < waves; ++w) sum += join[w][q];
+        const int r = r0 + i * 16 + (q >> 4), c = n0 + (q & 15);
+        if (r < hi && c < N) {
+          float o = sum * (2.0f * (alpha ? alpha[(int64_t)e * N + c] : 1.0f));
+          if (row_scale) o *= row_scale[r];
+          y[(int64_t)r * N + c] = (T)o;
+        }
+      }
+    }
+  }
+}
+
+template <int RM, typename T>
+void launch_rows(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows,
+                 const int32_t *off, const uint64_t *wp, const float *alpha,
+                 const float *row_scale, void *y, int64_t R, int64_t E, int64_t N, int64_t K,
+                 hipStream_t s) {
+  const int64_t tiles_n = (N + 15) / 16;
+  const int64_t most = tiles_n * (R / (16 * RM) + (E < R ? E : R));
+  const int64_t blocks = most < (1 << 20) ? most : (1 << 20);
+  const int64_t steps = (K + 511) / 512;
+  const int waves = steps >= 8 ? 8 : (steps < 1 ? 1 : (int)steps);
+  hipLaunchKernelGGL((signw_grouped_rows_kernel<RM, T>), dim3((unsigned)blocks), dim3(64 * waves),
+                     0, s, x, ldx, (int)xrows, rows, off, wp, alpha, row_scale,
+                     static_cast<T *>(y), (int)R, (int)E, (int)N, (int)K, (int)tiles_n, most);
+}
+
 template <int RB, int CB, typename T>
 void launch_tile(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows,
                  const int32_t *off, const uint64_t *wp, const float *alpha,
@@ -275,8 +394,14 @@ void launch_tile(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *r
 template <typename T>
 void launch(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows, const int32_t *off,
             const uint64_t *wp, const float *alpha, const float *row_scale, void *y, int64_t R,
-            int64_t E, int64_t N, int64_t K, hipStream_t s) {
-  const auto run = R / E >= 128 && N > 256 ? launch_tile<4, 2, T> : launch_tile<2, 1, T>;
+            int64_t E, int64_t N, int64_t K, int algo, hipStream_t s) {
+  const int64_t mean = R / E;  // rows of a group: all the host knows of them
+  if (algo == BNN_ALGO_AUTO) algo = mean <= 32 ? BNN_ALGO_GEMV : BNN_ALGO_MFMA;
+  auto run = launch_tile<2, 1, T>;
+  if (algo == BNN_ALGO_GEMV)
+    run = mean <= 8 ? launch_rows<1, T> : mean <= 16 ? launch_rows<2, T> : launch_rows<4, T>;
+  else if (mean >= 128 && N > 256)
+    run = launch_tile<4, 2, T>;
   run(x, ldx, xrows, rows, off, wp, alpha, row_scale, y, R, E, N, K, s);
 }
 
@@ -286,9 +411,8 @@ hipError_t launch_signw_grouped(const uint16_t *x, int64_t ldx, int64_t xrows, c
                                 const int32_t *off, const uint64_t *wp, const float *alpha,
                                 const float *row_scale, void *y, int dtype, int64_t R, int64_t E,
                                 int64_t N, int64_t K, int algo, hipStream_t s) {
-  (void)algo;
-  if (dtype == BNN_FP32) launch<float>(x, ldx, xrows, rows, off, wp, alpha, row_scale, y, R, E, N, K, s);
-  else launch<bf16_t>(x, ldx, xrows, rows, off, wp, alpha, row_scale, y, R, E, N, K, s);
+  const auto run = dtype == BNN_FP32 ? launch<float> : launch<bf16_t>;
+  run(x, ldx, xrows, rows, off, wp, alpha, row_scale, y, R, E, N, K, algo, s);
   return hipGetLastError();
 }
 
