@@ -330,8 +330,8 @@ bnn_status bnn_layernorm_fwd(const void *x, int dtype, int64_t ldx, const float 
                              const float *beta, void *y, int64_t ldy, float *mean, float *rstd,
                              int64_t M, int64_t N, float eps, void *stream);
 
-/* Bytes of workspace that bnn_layernorm_bwd needs for these sizes (0 when M
- * or N is <= 0). */
+/* Bytes of workspace that bnn_layernorm_bwd needs for these sizes (0 for few
+ * rows, and when M or N is <= 0). */
 int64_t bnn_layernorm_bwd_workspace(int64_t M, int64_t N);
 
 /*

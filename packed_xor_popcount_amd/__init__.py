@@ -57,6 +57,7 @@ class BnnError(RuntimeError):
 
 
 _lib = None
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def library():
@@ -119,11 +120,13 @@ def _check(status: int, where: str) -> None:
 
 
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    # the current stream's handle, without building a Stream object (a
+    # microsecond of a decode step's host time)
+    return _raw_stream(t.device.index)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need_cuda(name: str, t: torch.Tensor) -> None:
@@ -423,8 +426,7 @@ def layernorm_fwd(x, gamma=None, beta=None, eps=1e-5, stats=True, out=None):
             raise ValueError("out must have x's shape, type and device")
     mean = rstd = None
     if stats:
-        mean = torch.empty((M,), dtype=torch.float32, device=x.device)
-        rstd = torch.empty((M,), dtype=torch.float32, device=x.device)
+        mean, rstd = torch.empty((2, M), dtype=torch.float32, device=x.device).unbind(0)
     st = library().bnn_layernorm_fwd(_ptr(x), dt, ldx, _ptr(gamma), _ptr(beta), _ptr(out), ldy,
                                      _ptr(mean), _ptr(rstd), M, N, float(eps), _stream(x))
     _check(st, "bnn_layernorm_fwd")
@@ -448,10 +450,10 @@ def layernorm_bwd(dy, x, mean, rstd, gamma=None, params=True):
     dgamma = dbeta = ws = None
     need = 0
     if params:
-        dgamma = torch.empty((N,), dtype=torch.float32, device=x.device)
-        dbeta = torch.empty((N,), dtype=torch.float32, device=x.device)
+        dgamma, dbeta = torch.empty((2, N), dtype=torch.float32, device=x.device).unbind(0)
         need = library().bnn_layernorm_bwd_workspace(M, N)
-        ws = torch.empty((need,), dtype=torch.uint8, device=x.device)
+        if need > 0:
+            ws = torch.empty((need,), dtype=torch.uint8, device=x.device)
     st = library().bnn_layernorm_bwd(_ptr(dy), lddy, _ptr(x), ldx, dt, _ptr(gamma), _ptr(mean),
                                      _ptr(rstd), _ptr(dx), max(N, 1), _ptr(dgamma), _ptr(dbeta),
                                      _ptr(ws), need, M, N, _stream(x))
@@ -461,13 +463,13 @@ def layernorm_bwd(dy, x, mean, rstd, gamma=None, params=True):
 
 def f8_row_bytes(k: int) -> int:
     """Bytes of 8-bit values per row of k columns: 128 * ceil(k / 128)."""
-    return int(library().bnn_f8_row_bytes(int(k)))
+    return max(0, -(-int(k) // 128) * 128)
 
 
 def f8_scale_bytes(k: int) -> int:
     """Scale bytes per row of k columns: 4 * ceil(k / 512), one per block of
     128 columns and unused ones up to a multiple of four."""
-    return int(library().bnn_f8_scale_bytes(int(k)))
+    return max(0, -(-int(k) // 512) * 4)
 
 
 def quant_f8(x, transpose=False):
@@ -554,7 +556,7 @@ def gemm_signw_grouped(x, wp, offsets, K=None, alpha=None, rows=None, row_scale=
     if wp.dtype != torch.int64 or wp.dim() != 3 or not wp.is_contiguous():
         raise TypeError("wp must be a contiguous 3-D int64 tensor of packed words")
     E, N, kw = wp.shape
-    if kw != words(K):
+    if kw != -(-K // 64):
         raise ValueError(f"wp has {kw} words per row, K={K} needs {words(K)}")
     if wp.device != x.device:
         raise ValueError("x and wp must be on the same device")

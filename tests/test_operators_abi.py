@@ -38,12 +38,12 @@ def test_layernorm_fwd_refusals(lib):
 
 
 def test_layernorm_bwd_refusals(lib):
-    need = lib.bnn_layernorm_bwd_workspace(2, 8)
+    need = lib.bnn_layernorm_bwd_workspace(5000, 8)  # few rows need none
     assert need > 0
     assert all(lib.bnn_layernorm_bwd_workspace(m, n) == 0 for m, n in ((0, 8), (8, 0), (-1, 8), (BIG, 8), (8, BIG)))
 
     def f(dy=FAKE, lddy=8, x=FAKE, ldx=8, dt=0, g=None, mu=FAKE, r=FAKE, dx=FAKE, lddx=8, dg=FAKE, db=FAKE, ws=FAKE,
-          wb=need, M=2, N=8):
+          wb=need, M=5000, N=8):
         return lib.bnn_layernorm_bwd(dy, lddy, x, ldx, dt, g, mu, r, dx, lddx, dg, db, ws, wb, M, N, None)
     assert f(dt=-1) == E_DTYPE
     for kw in (dict(M=-1), dict(N=-1), dict(M=BIG), dict(ldx=7), dict(lddy=7), dict(lddx=7), dict(lddx=BIG),
@@ -71,6 +71,8 @@ def test_f8_sizes():
         nb = 0 if k <= 0 else -(-k // 128)
         assert bnn.f8_row_bytes(k) == 128 * nb
         assert bnn.f8_scale_bytes(k) == 4 * -(-nb // 4)
+        assert bnn.library().bnn_f8_row_bytes(k) == 128 * nb
+        assert bnn.library().bnn_f8_scale_bytes(k) == 4 * -(-nb // 4)
 
 
 def test_quant_f8_refusals(lib):
