@@ -51,18 +51,18 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi, float scale) 
 }
 
 // ---------------------------------------------------------------------------
-// Tiled kernel: WR x WC = 8 waves, each RB x CB tiles of 32 x 32, two waves per
-// SIMD.  Per block of 128 elements of K (one scale) the tile's rows of both
-// operands go straight from memory into one of two LDS buffers (the format
-// keeps rows 16-byte aligned) while the other one is multiplied.  The 16-byte
-// pieces of a row are swapped by the row's number, so that the reads spread
-// over the banks.  Each lane loads the scale bytes of its rows with them.
+// Tiled kernel: WR x WC = 8 waves, each RB x CB tiles of 32 x 32.  Per step of
+// 128 elements of K (one scale) the tile's rows of both operands and their
+// scale bytes go straight from memory into one of NBUF LDS buffers (the
+// format keeps rows 16-byte aligned); NBUF - 1 steps are in flight ahead of
+// the one that is multiplied.  The 16-byte pieces of a row are swapped by the
+// row's number, so that the reads spread over the banks.
 
 constexpr int kF8Threads = 512;
 
 // 16 bytes per lane from base + off to LDS at lds + 16 * lane, past the
-// registers (lds: a wave-uniform LDS byte address).  Counted by vmcnt;
-// lds_loads_done waits for all of them.
+// registers (lds: a wave-uniform LDS byte address), or 4 bytes.  Counted by
+// vmcnt, in order.
 __device__ __forceinline__ void load_to_lds(const uint8_t *base, uint32_t off, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
@@ -72,13 +72,26 @@ __device__ __forceinline__ void load_to_lds(const uint8_t *base, uint32_t off, u
       : "s"(lds), "v"(off), "s"(base)
       : "memory");
 }
-__device__ __forceinline__ void lds_loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void load4_to_lds(const uint8_t *base, uint32_t off, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, %2"
+      :
+      : "s"(lds), "v"(off), "s"(base)
+      : "memory");
+}
+// Waits until at most LEFT of this wave's loads are outstanding.
+template <int LEFT>
+__device__ __forceinline__ void lds_loads_done() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
+}
 
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
-template <int WR, int WC, int RB, int CB, typename T>
+template <int WR, int WC, int RB, int CB, int NBUF, typename T>
 __global__ void __launch_bounds__(kF8Threads, 2)
     gemm_f8_kernel(const uint8_t *__restrict__ xq, const uint8_t *__restrict__ xs,
                    const uint8_t *__restrict__ wq, const uint8_t *__restrict__ ws,
@@ -88,7 +101,13 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   constexpr int BM = WR * RB * 32, BN = WC * CB * 32;
   constexpr int PA = BM * 8 / kF8Threads, PB = BN * 8 / kF8Threads;  // loads of a thread per step
   static_assert(PA >= 1 && PB >= 1, "every thread stages");
-  __shared__ __attribute__((aligned(16))) unsigned char as[2][BM * 128], bs[2][BN * 128];
+  // Scale words (four steps' bytes) of the tile's BM + BN rows: a load of 64
+  // rows per wave, the waves past the last row repeating others' loads, so
+  // that every wave has the same number of loads in a step.
+  constexpr int SROWS = BM + BN, SCHUNKS = SROWS / 64, LOADS = PA + PB + 1;
+  static_assert(SROWS % 64 == 0 && SCHUNKS <= 8, "scale rows per wave");
+  constexpr int A0 = 0, B0 = BM * 128, S0 = B0 + BN * 128, STEP = S0 + SROWS * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[NBUF * STEP];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, h = lane >> 5;
@@ -105,9 +124,8 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     // Thread tid fills place tid + 512 i of the tile's pieces: row tid / 8 + 64 i,
     // place tid % 8, which holds piece (tid % 8) ^ (row % 8).
     const uint8_t *xt = xq + m0 * ldq, *wt = wq + n0 * ldq;
-    const uint8_t *xst = xs + (int64_t)m0 * sb, *wst = ws + (int64_t)n0 * sb;
     const uint32_t piece = 16 * ((tid & 7) ^ ((tid >> 3) & 7));
-    uint32_t ox[PA], ow[PB], osx[RB], osw[CB];
+    uint32_t ox[PA], ow[PB], os;
 #pragma unroll
     for (int i = 0; i < PA; ++i) {
       const int r = (tid >> 3) + i * (kF8Threads / 8);
@@ -118,24 +136,25 @@ __global__ void __launch_bounds__(kF8Threads, 2)
       const int r = (tid >> 3) + i * (kF8Threads / 8);
       ow[i] = (uint32_t)(n0 + r < N ? r : N - 1 - n0) * (uint32_t)ldq + piece;
     }
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      const int r = wm + i * 32 + li;
-      osx[i] = (uint32_t)(m0 + r < M ? r : M - 1 - m0) * (uint32_t)sb;
+    const int schunk = wave % SCHUNKS;  // scale rows 64 schunk .. + 63 of (X's, then W's)
+    const bool sx = schunk < BM / 64;
+    const uint8_t *st = sx ? xs + (int64_t)m0 * sb : ws + (int64_t)n0 * sb;
+    {
+      const int r = (sx ? schunk : schunk - BM / 64) * 64 + lane;
+      const int most = sx ? M - 1 - m0 : N - 1 - n0;
+      os = (uint32_t)(r < most ? r : most) * (uint32_t)sb;
     }
-#pragma unroll
-    for (int i = 0; i < CB; ++i) {
-      const int r = wn + i * 32 + li;
-      osw[i] = (uint32_t)(n0 + r < N ? r : N - 1 - n0) * (uint32_t)sb;
-    }
+    const uint32_t lds0 = lds_address(lds);
     auto load = [&](int s, int buf) __attribute__((always_inline)) {
-      const uint32_t la = lds_address(as[buf]) + wave * 1024;
-      const uint32_t lb = lds_address(bs[buf]) + wave * 1024;
+      const uint32_t l = lds0 + buf * STEP;
       const uint8_t *xb = xt + (int64_t)s * kF8Block, *wb = wt + (int64_t)s * kF8Block;
 #pragma unroll
-      for (int i = 0; i < PA; ++i) load_to_lds(xb, ox[i], la + i * (kF8Threads * 16));
+      for (int i = 0; i < PA; ++i)
+        load_to_lds(xb, ox[i], l + A0 + wave * 1024 + i * (kF8Threads * 16));
 #pragma unroll
-      for (int i = 0; i < PB; ++i) load_to_lds(wb, ow[i], lb + i * (kF8Threads * 16));
+      for (int i = 0; i < PB; ++i)
+        load_to_lds(wb, ow[i], l + B0 + wave * 1024 + i * (kF8Threads * 16));
+      load4_to_lds(st + (s & ~3), os, l + S0 + schunk * 256);
     };
     auto frag = [&](const unsigned char *buf, int row, int t) __attribute__((always_inline)) {
       const int p0 = ((4 * t + 2 * h) ^ (li & 7)) << 4, p1 = ((4 * t + 2 * h + 1) ^ (li & 7)) << 4;
@@ -151,29 +170,21 @@ __global__ void __launch_bounds__(kF8Threads, 2)
       for (int j = 0; j < CB; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    uint32_t ca[RB], cw[CB], na[RB], nw[CB];  // scale bytes of this and the next block
-    auto load_scales = [&](int s) __attribute__((always_inline)) {
+    auto compute = [&](int s, int buf) __attribute__((always_inline)) {
+      const unsigned char *as = lds + buf * STEP + A0, *bs = lds + buf * STEP + B0;
+      const unsigned char *sc = lds + buf * STEP + S0 + (s & 3);
+      uint32_t ca[RB], cw[CB];
 #pragma unroll
-      for (int i = 0; i < RB; ++i) na[i] = (xst + s)[osx[i]];
+      for (int i = 0; i < RB; ++i) ca[i] = sc[(wm + i * 32 + li) * 4];
 #pragma unroll
-      for (int i = 0; i < CB; ++i) nw[i] = (wst + s)[osw[i]];
-    };
-    auto arrived = [&]() __attribute__((always_inline)) {  // the next block is in place
-      lds_loads_done();
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < RB; ++i) ca[i] = na[i];
-#pragma unroll
-      for (int i = 0; i < CB; ++i) cw[i] = nw[i];
-    };
-    auto compute = [&](int buf) __attribute__((always_inline)) {
+      for (int i = 0; i < CB; ++i) cw[i] = sc[(BM + wn + i * 32 + li) * 4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         v8i fa[RB], fb[CB];
 #pragma unroll
-        for (int j = 0; j < CB; ++j) fb[j] = frag(bs[buf], wn + j * 32 + li, t);
+        for (int j = 0; j < CB; ++j) fb[j] = frag(bs, wn + j * 32 + li, t);
 #pragma unroll
-        for (int i = 0; i < RB; ++i) fa[i] = frag(as[buf], wm + i * 32 + li, t);
+        for (int i = 0; i < RB; ++i) fa[i] = frag(as, wm + i * 32 + li, t);
         if (!WIDE) {
 #pragma unroll
           for (int i = 0; i < RB; ++i)
@@ -186,10 +197,10 @@ __global__ void __launch_bounds__(kF8Threads, 2)
             bf16x8 va[RB], vb[CB];
 #pragma unroll
             for (int j = 0; j < CB; ++j)
-              vb[j] = widen8(fb[j][2 * k], fb[j][2 * k + 1], pow2_of(cw[j] & 255));
+              vb[j] = widen8(fb[j][2 * k], fb[j][2 * k + 1], pow2_of(cw[j]));
 #pragma unroll
             for (int i = 0; i < RB; ++i)
-              va[i] = widen8(fa[i][2 * k], fa[i][2 * k + 1], pow2_of(ca[i] & 255));
+              va[i] = widen8(fa[i][2 * k], fa[i][2 * k + 1], pow2_of(ca[i]));
 #pragma unroll
             for (int i = 0; i < RB; ++i)
 #pragma unroll
@@ -199,30 +210,23 @@ __global__ void __launch_bounds__(kF8Threads, 2)
         }
       }
     };
+    // Loads past the last step read it again (in bounds, into a buffer that
+    // nobody reads), so that the waits' counts stay exact.
     __syncthreads();  // the last tile's reads of LDS are done
     if (nb > 0) {
-      load(0, 0);
-      load_scales(0);
-      arrived();
       const int last = nb - 1;
-      int s = 0;
-      for (; s + 2 <= last; s += 2) {
-        load(s + 1, 1);
-        load_scales(s + 1);
-        compute(0);
-        arrived();
-        load(s + 2, 0);
-        load_scales(s + 2);
-        compute(1);
-        arrived();
+#pragma unroll
+      for (int d = 0; d < NBUF - 1; ++d) load(d < last ? d : last, d);
+      int buf = 0;
+      for (int s = 0; s < nb; ++s) {
+        lds_loads_done<LOADS *(NBUF - 2)>();
+        __syncthreads();  // step s has arrived; everyone is done with step s - 1
+        const int into = buf == 0 ? NBUF - 1 : buf - 1;
+        load(s + NBUF - 1 < last ? s + NBUF - 1 : last, into);
+        compute(s, buf);
+        buf = buf == NBUF - 1 ? 0 : buf + 1;
       }
-      if (s < last) {
-        load(last, 1);
-        load_scales(last);
-        compute(0);
-        arrived();
-      }
-      compute(last & 1);
+      lds_loads_done<0>();
     }
 
 #pragma unroll
@@ -327,13 +331,13 @@ void launch_rows(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const 
                      (int)f8_scale_bytes(K), tiles_n, tiles);
 }
 
-template <int WR, int WC, int RB, int CB, typename T>
+template <int WR, int WC, int RB, int CB, int NBUF, typename T>
 void launch_tile(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
                  void *y, int64_t M, int64_t N, int64_t K, hipStream_t s) {
   constexpr int BM = WR * RB * 32, BN = WC * CB * 32;
   const int64_t tiles_m = (M + BM - 1) / BM, tiles = tiles_m * ((N + BN - 1) / BN);
   const int64_t blocks = tiles < (1 << 20) ? tiles : (1 << 20);
-  hipLaunchKernelGGL((gemm_f8_kernel<WR, WC, RB, CB, T>), dim3((unsigned)blocks), dim3(kF8Threads),
+  hipLaunchKernelGGL((gemm_f8_kernel<WR, WC, RB, CB, NBUF, T>), dim3((unsigned)blocks), dim3(kF8Threads),
                      0, s, xq, xs, wq, ws, static_cast<T *>(y), (int)M, (int)N,
                      (int)f8_blocks(K), (int)f8_scale_bytes(K), (int)tiles_m, tiles);
 }
@@ -342,11 +346,11 @@ template <typename T>
 void launch(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws, void *y,
             int64_t M, int64_t N, int64_t K, hipStream_t s) {
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  auto run = launch_tile<2, 4, 4, 2, T>;
+  auto run = launch_tile<2, 4, 4, 2, 2, T>;
   if (M <= 16) run = launch_rows<1, T>;
   else if (M <= 32) run = launch_rows<2, T>;
   else if (M <= 64 || tiles(64, 128) < 128) run = launch_rows<4, T>;
-  else if (tiles(256, 256) < 128) run = launch_tile<2, 4, 1, 1, T>;
+  else if (tiles(256, 256) < 128) run = launch_tile<2, 4, 1, 1, 3, T>;
   run(xq, xs, wq, ws, y, M, N, K, s);
 }
 
