@@ -115,10 +115,16 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   const int64_t ldq = (int64_t)nb * kF8Block;
 
   for (int64_t b = blockIdx.x; b < tiles; b += gridDim.x) {
-    // Block b runs on XCD b % 8: each XCD takes a contiguous range of tiles.
-    const int64_t per = tiles >> 3;
-    const int64_t tile = (tiles & 7) == 0 ? (b & 7) * per + (b >> 3) : b;
-    const int m0 = (int)(tile % tiles_m) * BM, n0 = (int)(tile / tiles_m) * BN;
+    // Block b runs on XCD b % 8: each XCD takes a contiguous range of tiles (the
+    // first tiles % 8 XCDs one more), in bands of eight row tiles, so that the
+    // 32 blocks it runs at a time share 8 row and 4 column slabs in its L2.
+    const int xcd = (int)(b & 7), extra = (int)(tiles & 7);
+    const int64_t tile = xcd * (tiles >> 3) + (xcd < extra ? xcd : extra) + (b >> 3);
+    const int64_t tiles_n = tiles / tiles_m;
+    const int band = (int)(tile / (8 * tiles_n));
+    const int high = tiles_m - 8 * band < 8 ? tiles_m - 8 * band : 8;
+    const int64_t in = tile - 8 * tiles_n * band;
+    const int m0 = (8 * band + (int)(in % high)) * BM, n0 = (int)(in / high) * BN;
 
     // Row offsets inside a tile fit 32 bits: 256 rows of at most 2^24 bytes.
     // Thread tid fills place tid + 512 i of the tile's pieces: row tid / 8 + 64 i,
@@ -349,7 +355,6 @@ void launch(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8
   auto run = launch_tile<2, 4, 4, 2, 2, T>;
   if (M <= 16) run = launch_rows<1, T>;
   else if (M <= 32) run = launch_rows<2, T>;
-  else if (M <= 64 || tiles(64, 128) < 128) run = launch_rows<4, T>;
   else if (tiles(256, 256) < 128) run = launch_tile<2, 4, 1, 1, 3, T>;
   run(xq, xs, wq, ws, y, M, N, K, s);
 }
