@@ -90,10 +90,11 @@ __device__ __forceinline__ bool find_tile(const int32_t *off, int E, int T, int6
 // low (few rows are wasted at a group's end).
 //
 // Per 64-element step the block's activation rows (128 bytes each, their
-// 16-byte pieces swapped by row so that the reads spread over the banks) and
-// its columns' weight words pass through one of two LDS buffers; the step
-// after is on its way through registers, loaded at any alignment, zero past
-// K.  Bound by the bf16 matrix rate.
+// 16-byte pieces swapped by row so that the reads spread over the banks) pass
+// through one of two LDS buffers; the step after is on its way through
+// registers, loaded at any alignment, zero past K.  The columns' weight words
+// go the same way, eight steps at a time: one word of a column per step would
+// move a cache line for eight of its bytes.  Bound by the bf16 matrix rate.
 
 constexpr int kGroupThreads = 512;
 
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
   constexpr int PIECES = BM * 8 / kGroupThreads;  // 16-byte pieces a thread stages
   static_assert(PIECES >= 1 && BN <= kGroupThreads, "every thread stages");
   __shared__ __attribute__((aligned(16))) unsigned char as[2][BM * 128];
-  __shared__ __attribute__((aligned(16))) uint64_t ws[2][BN];
+  __shared__ __attribute__((aligned(16))) uint64_t ws[2][8][BN];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, h = lane >> 5;
@@ -141,12 +142,10 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
     }
     struct Stage {
       uint4 a[PIECES];
-      uint64_t w;
     };
     auto load = [&](int s, Stage &st) __attribute__((always_inline)) {  // a whole step
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) __builtin_memcpy(&st.a[i], xr[i] + 64 * (int64_t)s, 16);
-      st.w = wr[s];
     };
     auto load_tail = [&](Stage &st) __attribute__((always_inline)) {  // the last, partial one
 #pragma unroll
@@ -158,7 +157,6 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
             v[j / 2] |= (uint32_t)xr[i][64 * (int64_t)nfull + j] << (16 * (j & 1));
         st.a[i] = make_uint4(v[0], v[1], v[2], v[3]);
       }
-      st.w = wr[nfull];
     };
     auto stage = [&](const Stage &st, int buf) __attribute__((always_inline)) {
 #pragma unroll
@@ -166,7 +164,21 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
         const int row = (tid >> 3) + i * (kGroupThreads / 8);
         *reinterpret_cast<uint4 *>(as[buf] + row * 128 + (((tid & 7) ^ (row & 7)) << 4)) = st.a[i];
       }
-      if (BN == kGroupThreads || tid < BN) ws[buf][tid] = st.w;
+    };
+    uint64_t wn[8];  // this thread's column's words of the next eight steps
+    auto load_words = [&](int q) __attribute__((always_inline)) {
+      if (8 * q + 8 <= kw) {
+        __builtin_memcpy(wn, wr + 8 * q, 64);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wn[j] = wr[8 * q + j < kw ? 8 * q + j : kw - 1];
+      }
+    };
+    auto stage_words = [&](int q) __attribute__((always_inline)) {
+      if (BN == kGroupThreads || tid < BN) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ws[q & 1][j][tid] = wn[j];
+      }
     };
     v16f acc[RB][CB];
 #pragma unroll
@@ -175,12 +187,12 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
       for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[rb][cb][v] = 0.0f;
-    auto compute = [&](int buf) __attribute__((always_inline)) {
+    auto compute = [&](int s, int buf) __attribute__((always_inline)) {
+      const uint32_t *w = reinterpret_cast<const uint32_t *>(ws[(s >> 3) & 1][s & 7]);
       uint32_t sg[CB][8];
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb)
-        sign_bytes(reinterpret_cast<const uint32_t *>(ws[buf])[2 * (wave * CB * 32 + cb * 32 + li) + h],
-                   sg[cb]);
+        sign_bytes(w[2 * (wave * CB * 32 + cb * 32 + li) + h], sg[cb]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         bf16x8 a[RB], bo[CB];
@@ -203,6 +215,10 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
     // that the loop has no branches and its waits are exact.
     Stage sa, sb;
     __syncthreads();  // the last tile's reads of LDS are done
+    if (kw > 0) {
+      load_words(0);
+      stage_words(0);
+    }
     if (nfull > 0) {
       const int last = nfull - 1;
       load(0, sa);
@@ -210,25 +226,29 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
       stage(sa, 0);
       __syncthreads();
       for (int s = 0; s + 1 < nfull; s += 2) {
+        const int q = (s >> 3) + 1;
+        const bool more = 8 * q < kw;
+        if ((s & 7) == 0 && more) load_words(q);
         stage(sb, 1);
         load(s + 2 < last ? s + 2 : last, sa);
         __builtin_amdgcn_sched_barrier(0);
-        compute(0);
+        compute(s, 0);
         __syncthreads();
+        if ((s & 7) == 6 && more) stage_words(q);
         stage(sa, 0);
         load(s + 3 < last ? s + 3 : last, sb);
         __builtin_amdgcn_sched_barrier(0);
-        compute(1);
+        compute(s + 1, 1);
         __syncthreads();
       }
-      if (nfull & 1) compute(0);
+      if (nfull & 1) compute(last, 0);
     }
     if (nfull < kw) {
       load_tail(sa);
       __syncthreads();
       stage(sa, 0);
       __syncthreads();
-      compute(0);
+      compute(nfull, 0);
     }
 
     float al[CB];
