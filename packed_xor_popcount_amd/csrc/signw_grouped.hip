@@ -276,12 +276,13 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
 }
 
 // ---------------------------------------------------------------------------
-// Few-row kernel: 16 columns x 16 RM rows of a group per block, steps of 512
-// elements of K dealt out to the block's waves, their sums joined through LDS
-// in a fixed order.  Each weight word is read once per 16 RM rows of its group,
-// by 16-byte loads of 16 columns at a time, and groups without rows are not
-// touched; bound by the active groups' weight bytes and, for one token, by
-// the launch.
+// Few-row kernel: 16 RC columns x 16 RM rows of a group per block, steps of
+// 512 elements of K dealt out to the block's waves, their sums joined through
+// LDS in a fixed order.  Each weight word is read once per 16 RM rows of its
+// group, by 16-byte loads of 16 columns at a time, and groups without rows are
+// not touched.  Bound by the launch for one token (RC = 1: many blocks), by the
+// activation rows' way from L2 where many groups are active (RC = 4: one
+// reading of a row serves 64 columns).
 //
 // v_mfma_f32_16x16x32_bf16: lane l supplies row / column l % 16; lane group
 // g = l / 16 takes elements 128 g .. 128 g + 127 of a step, eight per
@@ -289,14 +290,14 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-template <int RM, typename T>
+template <int RM, int RC, typename T>
 __global__ void __launch_bounds__(512)
     signw_grouped_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, int xrows,
                               const int32_t *__restrict__ rows, const int32_t *__restrict__ off,
                               const uint64_t *__restrict__ wp, const float *__restrict__ alpha,
                               const float *__restrict__ row_scale, T *__restrict__ y, int R, int E,
                               int N, int K, int tiles_n, int64_t most) {
-  __shared__ float join[8][256];
+  __shared__ float join[8][256 * RC];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int li = lane & 15, g = lane >> 4;
@@ -304,9 +305,13 @@ __global__ void __launch_bounds__(512)
   for (int64_t tile = blockIdx.x; tile < most; tile += gridDim.x) {
     int e, r0, hi;
     if (!find_tile<16 * RM>(off, E, R, tile / tiles_n, e, r0, hi)) return;
-    const int n0 = (int)(tile % tiles_n) * 16;
-    const int n = n0 + li < N ? n0 + li : N - 1;
-    const uint64_t *wr = wp + ((int64_t)e * N + n) * kw;
+    const int n0 = (int)(tile % tiles_n) * (16 * RC);
+    const uint64_t *wr[RC];
+#pragma unroll
+    for (int c = 0; c < RC; ++c) {
+      const int n = n0 + c * 16 + li < N ? n0 + c * 16 + li : N - 1;
+      wr[c] = wp + ((int64_t)e * N + n) * kw;
+    }
     const uint16_t *xr[RM];
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
@@ -315,47 +320,57 @@ __global__ void __launch_bounds__(512)
       src = src < 0 ? 0 : (src < xrows ? src : xrows - 1);
       xr[i] = x + src * ldx;
     }
-    v4f acc[RM];
+    v4f acc[RM][RC];
 #pragma unroll
-    for (int i = 0; i < RM; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+      for (int c = 0; c < RC; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     for (int st = wave; st < steps; st += waves) {
       const int k0 = 512 * st + 128 * g;
-      uint32_t w[4] = {0, 0, 0, 0};
-      if (k0 + 128 <= K) {
-        __builtin_memcpy(w, wr + k0 / 64, 16);
-      } else {
+      uint32_t w[RC][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (k0 + 64 * j < K) __builtin_memcpy(w + 2 * j, wr + k0 / 64 + j, 8);
+      for (int c = 0; c < RC; ++c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[c][j] = 0;
+        if (k0 + 128 <= K) {
+          __builtin_memcpy(w[c], wr[c] + k0 / 64, 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (k0 + 64 * j < K) __builtin_memcpy(w[c] + 2 * j, wr[c] + k0 / 64 + j, 8);
+        }
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t sg[8];
-        sign_bytes(w[c], sg);
+      for (int t = 0; t < 4; ++t) {
+        const int k = k0 + 32 * t;
         uint4 a[RM][4];
-        if (k0 + 32 * c + 32 <= K) {
+        if (k + 32 <= K) {
 #pragma unroll
-          for (int i = 0; i < RM; ++i) __builtin_memcpy(a[i], xr[i] + k0 + 32 * c, 64);
+          for (int i = 0; i < RM; ++i) __builtin_memcpy(a[i], xr[i] + k, 64);
         } else {  // zero past K
 #pragma unroll
           for (int i = 0; i < RM; ++i) {
             uint32_t v[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int k = k0 + 32 * c + 2 * j;
-              v[j] = k < K ? xr[i][k] : 0u;
-              v[j] |= k + 1 < K ? (uint32_t)xr[i][k + 1] << 16 : 0u;
+              v[j] = k + 2 * j < K ? xr[i][k + 2 * j] : 0u;
+              v[j] |= k + 2 * j + 1 < K ? (uint32_t)xr[i][k + 2 * j + 1] << 16 : 0u;
             }
             __builtin_memcpy(a[i], v, 64);
           }
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const bf16x8 b = sign_operand(sg, q);
+        for (int c = 0; c < RC; ++c) {
+          uint32_t sg[8];
+          sign_bytes(w[c][t], sg);
 #pragma unroll
-          for (int i = 0; i < RM; ++i)
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i][q]), b,
-                                                             acc[i], 0, 0, 0);
+          for (int q = 0; q < 4; ++q) {
+            const bf16x8 b = sign_operand(sg, q);
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+              acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8, a[i][q]), b, acc[i][c], 0, 0, 0);
+          }
         }
       }
     }
@@ -363,12 +378,15 @@ __global__ void __launch_bounds__(512)
     for (int i = 0; i < RM; ++i) {
       __syncthreads();  // join is free
 #pragma unroll
-      for (int v = 0; v < 4; ++v) join[wave][(4 * g + v) * 16 + li] = acc[i][v];
+      for (int c = 0; c < RC; ++c)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          join[wave][(4 * g + v) * (16 * RC) + c * 16 + li] = acc[i][c][v];
       __syncthreads();
-      for (int q = threadIdx.x; q < 256; q += blockDim.x) {
+      for (int q = threadIdx.x; q < 256 * RC; q += blockDim.x) {
         float sum = 0.0f;
         for (int w = 0; w < waves; ++w) sum += join[w][q];
-        const int r = r0 + i * 16 + (q >> 4), c = n0 + (q & 15);
+        const int r = r0 + i * 16 + q / (16 * RC), c = n0 + q % (16 * RC);
         if (r < hi && c < N) {
           float o = sum * (2.0f * (alpha ? alpha[(int64_t)e * N + c] : 1.0f));
           if (row_scale) o *= row_scale[r];
@@ -379,18 +397,18 @@ __global__ void __launch_bounds__(512)
   }
 }
 
-template <int RM, typename T>
+template <int RM, int RC, typename T>
 void launch_rows(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows,
                  const int32_t *off, const uint64_t *wp, const float *alpha,
                  const float *row_scale, void *y, int64_t R, int64_t E, int64_t N, int64_t K,
                  hipStream_t s) {
-  const int64_t tiles_n = (N + 15) / 16;
+  const int64_t tiles_n = (N + 16 * RC - 1) / (16 * RC);
   const int64_t most = tiles_n * (R / (16 * RM) + (E < R ? E : R));
   const int64_t blocks = most < (1 << 20) ? most : (1 << 20);
   const int64_t steps = (K + 511) / 512;
   const int waves = steps >= 8 ? 8 : (steps < 1 ? 1 : (int)steps);
-  hipLaunchKernelGGL((signw_grouped_rows_kernel<RM, T>), dim3((unsigned)blocks), dim3(64 * waves),
-                     0, s, x, ldx, (int)xrows, rows, off, wp, alpha, row_scale,
+  hipLaunchKernelGGL((signw_grouped_rows_kernel<RM, RC, T>), dim3((unsigned)blocks),
+                     dim3(64 * waves), 0, s, x, ldx, (int)xrows, rows, off, wp, alpha, row_scale,
                      static_cast<T *>(y), (int)R, (int)E, (int)N, (int)K, (int)tiles_n, most);
 }
 
@@ -415,13 +433,30 @@ template <typename T>
 void launch(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows, const int32_t *off,
             const uint64_t *wp, const float *alpha, const float *row_scale, void *y, int64_t R,
             int64_t E, int64_t N, int64_t K, int algo, hipStream_t s) {
-  const int64_t mean = R / E;  // rows of a group: all the host knows of them
-  if (algo == BNN_ALGO_AUTO) algo = mean <= 32 ? BNN_ALGO_GEMV : BNN_ALGO_MFMA;
+  // All the host knows of the groups is R and E.  The few-row kernel serves
+  // small groups and products with too few tiles to fill the card; measured
+  // (device, bf16 out, N x K): 256 rows on 64 experts of 1024 x 4096 27 us
+  // against 45 us on tiles, 602 on 10 of 700 x 1000 12 against 18; 2000 on 128
+  // of 1024 x 512 35 against 22.
+  const int64_t mean = R / E, active = E < R ? E : R;
+  const auto tiles = [&](int64_t bm, int64_t bn) {  // about; half a tile lost per group
+    return (R / bm + active / 2) * ((N + bn - 1) / bn);
+  };
+  if (algo == BNN_ALGO_AUTO)
+    algo = mean <= 12 || tiles(64, 256) < 64 ? BNN_ALGO_GEMV : BNN_ALGO_MFMA;
   auto run = launch_tile<2, 1, T>;
-  if (algo == BNN_ALGO_GEMV)
-    run = mean <= 8 ? launch_rows<1, T> : mean <= 16 ? launch_rows<2, T> : launch_rows<4, T>;
-  else if (mean >= 128 && N > 256)
-    run = launch_tile<4, 2, T>;
+  if (algo == BNN_ALGO_GEMV) {
+    // 16 columns a block while 64 would leave CUs idle (one token on 8 experts
+    // of 1024 x 4096: 7 us); 64 beyond (256 rows on 64 experts: 39 -> 27 us).
+    run = active * ((N + 63) / 64) < 512 ? launch_rows<1, 1, T>
+          : mean <= 8                    ? launch_rows<1, 4, T>
+                                         : launch_rows<2, 4, T>;
+  } else if (mean >= 128) {
+    // 128-row tiles waste more of a group's last tile: 4000 rows on 32 experts
+    // of 2048 x 2048 61 us on 64-row tiles, 96 on 128; 2000 on 8 of 1001 x
+    // 1001 49 against 36.  512 columns once that still fills the card.
+    run = tiles(128, 512) >= 512 ? launch_tile<4, 2, T> : launch_tile<4, 1, T>;
+  }
   run(x, ldx, xrows, rows, off, wp, alpha, row_scale, y, R, E, N, K, s);
 }
 
