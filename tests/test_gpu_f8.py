@@ -300,3 +300,20 @@ def test_side_stream():
         y = bnn.gemm_f8(*bnn.quant_f8(x), *bnn.quant_f8(w), 777)
     s.synchronize()
     assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("rows,k", [(2100, 2001), (2100, 2048), (4097, 1030), (257, 20001)])
+def test_quant_many_tiles(rows, k):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(rows + k)
+    for dtype in DT.values():
+        for pad in (0, 1):
+            x = spread(g, rows, k, dtype, pad)
+            for transpose in (False, True):
+                check_quant(x, transpose)
+
+
+@pytest.mark.parametrize("M,N,K", [(2900, 2999, 300), (3073, 2817, 1024), (5000, 2000, 129)])
+def test_product_large(M, N, K):
+    test_product_exact(M, N, K)
+    test_product_rounding(M, N, K)

@@ -249,3 +249,10 @@ def test_side_stream():
         gotb = bnn.layernorm_bwd(got[0], x, got[1], got[2])
     s.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(ref + refb, got + gotb))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,N", [(600, 1500), (600, 7000), (1100, 12001), (257, 3000), (1025, 16384), (513, 8192)])
+def test_partial_rows(M, N, dtype):
+    """Enough rows that the column sums pass through partial rows."""
+    check(M, N, DT[dtype], seed=M + N)

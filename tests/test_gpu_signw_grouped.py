@@ -270,3 +270,14 @@ def test_side_stream(algo):
         y = c.run(ALGOS[algo], torch.float32)
     s.synchronize()
     assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("algo", list(ALGOS))
+@pytest.mark.parametrize("counts,N,K", [([9000, 0, 4100], 2561, 130), ([140, 300, 17, 190], 1000, 1100),
+                                        ([20, 9, 0, 30] * 20, 500, 600), ([1, 0, 7, 2] * 40, 300, 1030)])
+def test_every_tile(counts, N, K, algo):
+    """Groupings that reach each tile of both kernels."""
+    for integers in (True, False):
+        c = Case(13, counts, N, K, gather=True, pad=1, integers=integers)
+        for dtype in DT.values():
+            check(c, ALGOS[algo], dtype, integers)
