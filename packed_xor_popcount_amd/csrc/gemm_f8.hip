@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
 
     // Row offsets inside a tile fit 32 bits: 256 rows of at most 2^24 bytes.
     // Thread tid fills place tid + 512 i of the tile's pieces: row tid / 8 + 64 i,
-    // place tid % 8, which holds piece (tid % 8) ^ (row % 8).
+    // place tid % 8, which holds piece (tid % 8) ^ (row / 2 % 8).
     const uint8_t *xt = xq + m0 * ldq, *wt = wq + n0 * ldq;
     const uint32_t piece = 16 * ((tid & 7) ^ ((tid >> 4) & 7));
     uint32_t ox[PA], ow[PB], os;
