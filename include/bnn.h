@@ -395,13 +395,10 @@ bnn_status bnn_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int
 /*
  * bnn_gemm_f8 -- product of two block-scaled 8-bit matrices:
  *   y[m][n] = sum_b 2^(xs[m][b] + ws[n][b] - 254) sum_{k in block b} xq[m][k] * wq[n][k],
- * sums fp32 on the matrix cores, rounded once to y's type; their order
- * depends on the sizes and types only.  fp32 outputs: products exact, within
- * the bound of an fp32 sum of K terms.  bf16 outputs may use the 8-bit matrix
- * instructions, which cut a product's bits below 2^-13 of the largest among
- * eight consecutive k (1.6e-5 of the result for normal operands, far below
- * the rounding to bf16).  Decoded values below 2^-126 may count as zero and
- * those above bf16's range as infinite; bnn_quant_f8 makes none of the latter.
+ * products exact, sums fp32 on the matrix cores (within the bound of an fp32
+ * sum of K terms), rounded once to y's type; their order depends on the sizes
+ * and types only.  Decoded values below 2^-126 may count as zero and those
+ * above bf16's range as infinite; bnn_quant_f8 makes none of the latter.
  *
  *   xq, xs   M rows of K columns, wq, ws  N rows of K columns; q buffers
  *            16-byte, s buffers 4-byte aligned.  The bytes past K have to be
@@ -413,6 +410,23 @@ bnn_status bnn_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int
  */
 bnn_status bnn_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
                        void *y, int dtype, int64_t M, int64_t N, int64_t K, void *stream);
+
+/*
+ * bnn_gemm_f8_fast -- bnn_gemm_f8 with bf16 outputs, on the 8-bit matrix
+ * instructions where they are faster (more than 32 rows; up to 32 rows are
+ * computed as by bnn_gemm_f8).  The instructions hold fewer bits: inside a
+ * group of eight consecutive k (8 g .. 8 g + 7) what a product has below 2^-13
+ * of the group's largest product is dropped; sums over groups are fp32.  For
+ * normal operands that is 1.6e-5 of the result, a hundredth of the rounding to
+ * bf16.  Where large products of a group cancel, the small ones beside them
+ * are lost, and a row's result then depends on whether the call has more than
+ * 32 rows: operands with that structure belong to bnn_gemm_f8.
+ *
+ * Arguments and errors as bnn_gemm_f8; y is M x N bf16.
+ */
+bnn_status bnn_gemm_f8_fast(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
+                            const uint8_t *ws, void *y, int64_t M, int64_t N, int64_t K,
+                            void *stream);
 
 /*
  * bnn_gemm_signw_grouped -- bnn_gemm_signw_bf16 grouped by expert: a mixture

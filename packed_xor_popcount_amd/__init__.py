@@ -45,7 +45,7 @@ EXPORTED = ("bnn_words", "bnn_status_str", "bnn_version", "bnn_pack_signs", "bnn
             "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16", "bnn_chain3",
             "bnn_layernorm_fwd", "bnn_layernorm_bwd_workspace", "bnn_layernorm_bwd",
             "bnn_f8_row_bytes", "bnn_f8_scale_bytes", "bnn_quant_f8", "bnn_gemm_f8",
-            "bnn_gemm_signw_grouped")
+            "bnn_gemm_f8_fast", "bnn_gemm_signw_grouped")
 
 
 class BnnError(RuntimeError):
@@ -91,11 +91,12 @@ def library():
     lib.bnn_f8_scale_bytes.argtypes, lib.bnn_f8_scale_bytes.restype = [I64], I64
     lib.bnn_quant_f8.argtypes = [P, I, I64, I64, I64, I, P, P, P]
     lib.bnn_gemm_f8.argtypes = [P, P, P, P, P, I, I64, I64, I64, P]
+    lib.bnn_gemm_f8_fast.argtypes = [P, P, P, P, P, I64, I64, I64, P]
     lib.bnn_gemm_signw_grouped.argtypes = [P, I64, I64, P, P, P, P, P, P, I, I64, I64, I64, I64, I, P]
     for name in ("bnn_pack_signs", "bnn_gemm_u64", "bnn_gemm_u64_scaled", "bnn_gemm_sign_repack",
                  "bnn_gemm_ex", "bnn_gemv_act", "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16",
                  "bnn_chain3", "bnn_layernorm_fwd", "bnn_layernorm_bwd", "bnn_quant_f8",
-                 "bnn_gemm_f8", "bnn_gemm_signw_grouped"):
+                 "bnn_gemm_f8", "bnn_gemm_f8_fast", "bnn_gemm_signw_grouped"):
         getattr(lib, name).restype = I
     _lib = lib
     return lib
@@ -499,16 +500,25 @@ def _quantised(name: str, q, s, k: int) -> int:
     return q.shape[0]
 
 
-def gemm_f8(xq, xs, wq, ws, K, dtype=torch.float32, out=None):
+def gemm_f8(xq, xs, wq, ws, K, dtype=torch.float32, out=None, fast=False):
     """``(M, N)`` product of two block-scaled 8-bit matrices of K columns (as
     quant_f8 makes them): ``x @ w.T`` with fp32 sums, rounded once to ``dtype``
-    (float32 or bfloat16) (bnn_gemm_f8)."""
+    (float32 or bfloat16) (bnn_gemm_f8).  ``fast=True``, for bfloat16 outputs:
+    the 8-bit matrix instructions, which drop what a product has below 2^-13 of
+    the largest among eight neighbours along K (bnn_gemm_f8_fast)."""
     K = int(K)
     M = _quantised("x", xq, xs, K)
     N = _quantised("w", wq, ws, K)
     if wq.device != xq.device:
         raise ValueError("x and w must be on the same device")
     out, dt = _real_out(M, N, dtype, xq.device, out)
+    if fast:
+        if dt != BNN_BF16:
+            raise TypeError("fast products have bfloat16 outputs")
+        st = library().bnn_gemm_f8_fast(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(out), M, N, K,
+                                        _stream(xq))
+        _check(st, "bnn_gemm_f8_fast")
+        return out
     st = library().bnn_gemm_f8(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(out), dt, M, N, K,
                                _stream(xq))
     _check(st, "bnn_gemm_f8")

@@ -59,6 +59,23 @@ bnn_status run_gemm(const uint64_t *xp, const uint64_t *wp, const bnn::EpiParams
   return launch_status(bnn::launch_gemm_tiled(xp, wp, ep, y, M, N, K, epilogue, s));
 }
 
+// Checks and launch of both 8-bit products.
+bnn_status run_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                       void *y, int dtype, bool fast, int64_t M, int64_t N, int64_t K,
+                       void *stream) {
+  if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
+  if (M < 0 || N < 0 || K < 0 || M >= kMaxDim || N >= kMaxDim || K > bnn::kF8MaxK)
+    return BNN_E_SHAPE;
+  if ((M * K > 0 && (!xq || !xs)) || (N * K > 0 && (!wq || !ws)) || (M * N > 0 && !y))
+    return BNN_E_NULL;
+  if (misaligned(xq, 16) || misaligned(wq, 16) || misaligned(xs, 4) || misaligned(ws, 4) ||
+      misaligned(y, dtype == BNN_FP32 ? 4 : 2))
+    return BNN_E_ALIGN;
+  if (M == 0 || N == 0) return BNN_OK;
+  return launch_status(bnn::launch_gemm_f8(xq, xs, wq, ws, y, dtype, fast, M, N, K,
+                                           static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -240,17 +257,13 @@ bnn_status bnn_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int
 
 bnn_status bnn_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
                        void *y, int dtype, int64_t M, int64_t N, int64_t K, void *stream) {
-  if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
-  if (M < 0 || N < 0 || K < 0 || M >= kMaxDim || N >= kMaxDim || K > bnn::kF8MaxK)
-    return BNN_E_SHAPE;
-  if ((M * K > 0 && (!xq || !xs)) || (N * K > 0 && (!wq || !ws)) || (M * N > 0 && !y))
-    return BNN_E_NULL;
-  if (misaligned(xq, 16) || misaligned(wq, 16) || misaligned(xs, 4) || misaligned(ws, 4) ||
-      misaligned(y, dtype == BNN_FP32 ? 4 : 2))
-    return BNN_E_ALIGN;
-  if (M == 0 || N == 0) return BNN_OK;
-  return launch_status(bnn::launch_gemm_f8(xq, xs, wq, ws, y, dtype, M, N, K,
-                                           static_cast<hipStream_t>(stream)));
+  return run_gemm_f8(xq, xs, wq, ws, y, dtype, false, M, N, K, stream);
+}
+
+bnn_status bnn_gemm_f8_fast(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
+                            const uint8_t *ws, void *y, int64_t M, int64_t N, int64_t K,
+                            void *stream) {
+  return run_gemm_f8(xq, xs, wq, ws, y, BNN_BF16, true, M, N, K, stream);
 }
 
 bnn_status bnn_gemm_signw_grouped(const void *x, int64_t ldx, int64_t xrows, const int32_t *rows,

@@ -94,12 +94,13 @@ hipError_t launch_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int
                                 const float *rstd, void *dx, int64_t lddx, float *dgamma,
                                 float *dbeta, float *part, int64_t M, int64_t N, hipStream_t s);
 
-// Block-scaled 8-bit quantiser and product (arguments as in the C-ABI).
+// Block-scaled 8-bit quantiser and product (arguments as in the C-ABI; fast:
+// bf16 outputs by the 8-bit matrix instructions).
 hipError_t launch_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int64_t ld,
                            bool transpose, uint8_t *q, uint8_t *s, hipStream_t st);
 hipError_t launch_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
-                          const uint8_t *ws, void *y, int dtype, int64_t M, int64_t N, int64_t K,
-                          hipStream_t s);
+                          const uint8_t *ws, void *y, int dtype, bool fast, int64_t M, int64_t N,
+                          int64_t K, hipStream_t s);
 
 // Sign-weight products grouped by expert (bnn_gemm_signw_grouped).
 hipError_t launch_signw_grouped(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows,

@@ -2,20 +2,21 @@
 //
 //   y[m][n] = sum_b 2^(xs[m][b] + ws[n][b] - 254) sum_{k in block b} xq[m][k] wq[n][k]
 //
-// Two ways through the matrix cores, chosen by the output's precision:
+// Two ways through the matrix cores, the second only where the caller asks for
+// it (bnn_gemm_f8_fast):
 //
-//  * bf16 outputs: v_mfma_scale_f32_32x32x64_f8f6f4 takes the 8-bit values and
-//    the scale byte of each operand row as they are, so a block boundary costs
-//    nothing.  Measured on this unit: the sum over groups of eight consecutive
-//    k and onto the accumulator keeps fp32 precision, but inside a group the
-//    products are cut below 2^-13 of the group's largest.  For normally
-//    distributed operands that is an error of 1.6e-5 of the result, a
-//    hundredth of the bf16 rounding that follows.
-//  * fp32 outputs: the values are widened to bf16 with their scale applied
+//  * the values are widened to bf16 with their scale applied
 //    (v_cvt_scalef32_pk_bf16_fp8: exact, an e4m3 significand has 4 bits) and
 //    multiplied by v_mfma_f32_32x32x16_bf16, which keeps fp32 precision
 //    throughout (products down to 2^-23 of the largest were measured to
-//    count), at half the rate.
+//    count), at half the 8-bit rate.
+//  * v_mfma_scale_f32_32x32x64_f8f6f4 takes the 8-bit values and the scale byte
+//    of each operand row as they are.  Measured on this unit: the sum over
+//    groups of eight consecutive k and onto the accumulator keeps fp32
+//    precision, but inside a group the products are cut below 2^-13 of the
+//    group's largest.  For normally distributed operands that is an error of
+//    1.6e-5 of the result, a hundredth of a bf16 rounding; where the large
+//    products of a group cancel, the small ones are lost.
 //
 // Lane l supplies row / column l % 32 and half of the k values of an
 // instruction (which half is free as long as both operands agree).  Output
@@ -59,10 +60,11 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi, float scale) 
 // the row's number, so that 16 neighbouring rows meet all 64 banks (by the whole
 // number, rows 8 apart collided; the conflict counter now reads 0).
 //
-// 4096 x 11008 x 4096, bf16 out: 182 us, 2.0 PFLOP/s (a library product of one
-// scale: 189 us); fp32 out, on bf16 instructions: 299 us.  Bound by the matrix
-// cores' clock and the tiles' way from L2: bands of row tiles (below) took it
-// from 250 us.  Under about 100 tiles the steps' latency bounds it, 0.5 us each.
+// 4096 x 11008 x 4096, bf16 out: 293 us, 1.26 PFLOP/s (a large library product
+// of bf16 matrices: 1.38); FAST 177 us, 2.09 PFLOP/s (a library product of one
+// scale: 189 us).  256 x 4096 x 4096: 22 and 17 us; 2048 x 4096 x 4096: 86 and
+// 51 us.  Bands of row tiles (below) took the large FAST product from 250 us.
+// Under about 100 tiles the steps' latency bounds it, 0.5 us each.
 
 constexpr int kF8Threads = 512;
 
@@ -97,13 +99,12 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
-template <int WR, int WC, int RB, int CB, int NBUF, typename T>
+template <int WR, int WC, int RB, int CB, int NBUF, bool FAST, typename T>
 __global__ void __launch_bounds__(kF8Threads, 2)
     gemm_f8_kernel(const uint8_t *__restrict__ xq, const uint8_t *__restrict__ xs,
                    const uint8_t *__restrict__ wq, const uint8_t *__restrict__ ws,
                    T *__restrict__ y, int M, int N, int nb, int sb, int tiles_m, int64_t tiles) {
   static_assert(WR * WC == 8, "eight waves");
-  constexpr bool WIDE = sizeof(T) == 4;
   constexpr int BM = WR * RB * 32, BN = WC * CB * 32;
   constexpr int PA = BM * 8 / kF8Threads, PB = BN * 8 / kF8Threads;  // loads of a thread per step
   static_assert(PA >= 1 && PB >= 1, "every thread stages");
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
         for (int j = 0; j < CB; ++j) fb[j] = frag(bs, wn + j * 32 + li, t);
 #pragma unroll
         for (int i = 0; i < RB; ++i) fa[i] = frag(as, wm + i * 32 + li, t);
-        if (!WIDE) {
+        if (FAST) {
 #pragma unroll
           for (int i = 0; i < RB; ++i)
 #pragma unroll
@@ -343,35 +344,37 @@ void launch_rows(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const 
                      (int)f8_scale_bytes(K), tiles_n, tiles);
 }
 
-template <int WR, int WC, int RB, int CB, int NBUF, typename T>
+template <int WR, int WC, int RB, int CB, int NBUF, bool FAST, typename T>
 void launch_tile(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
                  void *y, int64_t M, int64_t N, int64_t K, hipStream_t s) {
   constexpr int BM = WR * RB * 32, BN = WC * CB * 32;
   const int64_t tiles_m = (M + BM - 1) / BM, tiles = tiles_m * ((N + BN - 1) / BN);
   const int64_t blocks = tiles < (1 << 20) ? tiles : (1 << 20);
-  hipLaunchKernelGGL((gemm_f8_kernel<WR, WC, RB, CB, NBUF, T>), dim3((unsigned)blocks), dim3(kF8Threads),
-                     0, s, xq, xs, wq, ws, static_cast<T *>(y), (int)M, (int)N,
+  hipLaunchKernelGGL((gemm_f8_kernel<WR, WC, RB, CB, NBUF, FAST, T>), dim3((unsigned)blocks),
+                     dim3(kF8Threads), 0, s, xq, xs, wq, ws, static_cast<T *>(y), (int)M, (int)N,
                      (int)f8_blocks(K), (int)f8_scale_bytes(K), (int)tiles_m, tiles);
 }
 
-template <typename T>
+template <bool FAST, typename T>
 void launch(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws, void *y,
             int64_t M, int64_t N, int64_t K, hipStream_t s) {
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  auto run = launch_tile<2, 4, 4, 2, 2, T>;
+  auto run = launch_tile<2, 4, 4, 2, 2, FAST, T>;
   if (M <= 16) run = launch_rows<1, T>;
   else if (M <= 32) run = launch_rows<2, T>;
-  else if (tiles(256, 256) < 128) run = launch_tile<2, 4, 1, 1, 3, T>;
+  else if (tiles(256, 256) < 128) run = launch_tile<2, 4, 1, 1, 3, FAST, T>;
   run(xq, xs, wq, ws, y, M, N, K, s);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
-                          const uint8_t *ws, void *y, int dtype, int64_t M, int64_t N, int64_t K,
-                          hipStream_t s) {
-  if (dtype == BNN_FP32) launch<float>(xq, xs, wq, ws, y, M, N, K, s);
-  else launch<bf16_t>(xq, xs, wq, ws, y, M, N, K, s);
+                          const uint8_t *ws, void *y, int dtype, bool fast, int64_t M, int64_t N,
+                          int64_t K, hipStream_t s) {
+  const auto run = dtype == BNN_FP32 ? launch<false, float>
+                   : fast            ? launch<true, bf16_t>
+                                     : launch<false, bf16_t>;
+  run(xq, xs, wq, ws, y, M, N, K, s);
   return hipGetLastError();
 }
 
