@@ -397,8 +397,10 @@ bnn_status bnn_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int
  *   y[m][n] = sum_b 2^(xs[m][b] + ws[n][b] - 254) sum_{k in block b} xq[m][k] * wq[n][k],
  * products exact, sums fp32 on the matrix cores (within the bound of an fp32
  * sum of K terms), rounded once to y's type; their order depends on the sizes
- * and types only.  Decoded values below 2^-126 may count as zero and those
- * above bf16's range as infinite; bnn_quant_f8 makes none of the latter.
+ * and types only, but for outputs beside a block of scale byte 247 or more.
+ * Decoded values below 2^-126 may count as zero and those above 2^128 as
+ * infinite; bnn_quant_f8 makes none of the latter (2^128 itself, and with it
+ * scale byte 247, is what it makes of magnitudes from 1.9375 * 2^127 on).
  *
  *   xq, xs   M rows of K columns, wq, ws  N rows of K columns; q buffers
  *            16-byte, s buffers 4-byte aligned.  The bytes past K have to be

@@ -51,6 +51,45 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi, float scale) 
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+// From scale byte 247 (2^120) on a value can decode to 2^128, past bf16's range
+// (the quantiser makes it of magnitudes from 1.9375 * 2^127 on).  The kernels
+// note the largest scale byte that a wave meets, and a wave that met such a
+// one computes its sums again here, with operands in two parts: twice the half
+// of such a block's values, once those of other blocks and then zeros.  Rare,
+// so nothing is staged, and one copy of the arithmetic keeps the registers of the
+// ordinary path: 4096 x 11008 x 4096 with 2^128 in one row of x 2.4 ms, in every
+// row 4.4 ms (0.29 ms without).  The 8-bit instructions need none of this: they
+// apply the scales past bf16's range.
+constexpr uint32_t kF8Split = 247;
+
+// Sums of 16 x 16 outputs over blocks b0, b0 + step, ...: xr, wr the lane's
+// operand rows + 32 (lane / 16), xs, ws their scale bytes; lanes, instruction
+// and output as in the few-row kernel.
+__device__ __forceinline__ v4f split_16x16(const uint8_t *xr, const uint8_t *xs, const uint8_t *wr,
+                                           const uint8_t *ws, int b0, int step, int nb) {
+  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int b = b0; b < nb; b += step) {
+    const int64_t o = (int64_t)b * kF8Block;
+    const uint32_t sx = xs[b], sw = ws[b];
+    const bool bx = sx >= kF8Split, bw = sw >= kF8Split;
+    const float fx = pow2_of(bx ? sx - 1 : sx), fw = pow2_of(bw ? sw - 1 : sw);
+    const bool any_x = __any(bx), any_w = __any(bw);
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {  // halves of the block, up to four times each
+      if (((i & 1) && !any_x) || ((i & 2) && !any_w)) continue;
+      const v4u x = *reinterpret_cast<const v4u *>(xr + o + 16 * (i >> 2));
+      const v4u w = *reinterpret_cast<const v4u *>(wr + o + 16 * (i >> 2));
+      const v4u p = x & (bx || !(i & 1) ? ~0u : 0u), q = w & (bw || !(i & 2) ? ~0u : 0u);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(p.x, p.y, fx), widen8(q.x, q.y, fw), acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(p.z, p.w, fx), widen8(q.z, q.w, fw), acc, 0, 0, 0);
+    }
+  }
+  return acc;
+}
+
 // ---------------------------------------------------------------------------
 // Tiled kernel: WR x WC = 8 waves, each RB x CB tiles of 32 x 32.  Per step of
 // 128 elements of K (one scale) the tile's rows of both operands and their
@@ -183,6 +222,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
       for (int j = 0; j < CB; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    uint32_t top = 0;  // largest scale byte met
     auto compute = [&](int s, int buf) __attribute__((always_inline)) {
       const unsigned char *as = lds + buf * STEP + A0, *bs = lds + buf * STEP + B0;
       const unsigned char *sc = lds + buf * STEP + S0 + (s & 3);
@@ -191,6 +231,12 @@ __global__ void __launch_bounds__(kF8Threads, 2)
       for (int i = 0; i < RB; ++i) ca[i] = sc[(wm + i * 32 + li) * 4];
 #pragma unroll
       for (int i = 0; i < CB; ++i) cw[i] = sc[(BM + wn + i * 32 + li) * 4];
+      if (!FAST) {
+#pragma unroll
+        for (int i = 0; i < RB; ++i) top = ca[i] > top ? ca[i] : top;
+#pragma unroll
+        for (int i = 0; i < CB; ++i) top = cw[i] > top ? cw[i] : top;
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         v8i fa[RB], fb[CB];
@@ -242,6 +288,21 @@ __global__ void __launch_bounds__(kF8Threads, 2)
       lds_loads_done<0>();
     }
 
+    if (!FAST && __any(top >= kF8Split)) {
+      const int l16 = lane & 15, g = lane >> 4;
+#pragma unroll 1
+      for (int t = 0; t < RB * CB * 4; ++t) {
+        const int mt = m0 + wm + 16 * (t / (2 * CB)), nt = n0 + wn + 16 * (t % (2 * CB));
+        const int m = mt + l16 < M ? mt + l16 : M - 1, n = nt + l16 < N ? nt + l16 : N - 1;
+        const v4f sum = split_16x16(xq + m * ldq + 32 * g, xs + (int64_t)m * sb,
+                                    wq + n * ldq + 32 * g, ws + (int64_t)n * sb, 0, 1, nb);
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (mt + 4 * g + v < M && nt + l16 < N)
+            y[(int64_t)(mt + 4 * g + v) * N + nt + l16] = (T)sum[v];
+      }
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
 #pragma unroll
@@ -269,9 +330,6 @@ __global__ void __launch_bounds__(kF8Threads, 2)
 // l / 16 takes bytes 32 (l / 16) .. + 31 of a block of 128, eight per
 // instruction.  Output: register v -> row 4 (l / 16) + v, column l % 16.
 
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-
 template <int RM, typename T>
 __global__ void __launch_bounds__(1024)
     gemm_f8_rows_kernel(const uint8_t *__restrict__ xq, const uint8_t *__restrict__ xs,
@@ -297,24 +355,33 @@ __global__ void __launch_bounds__(1024)
     v4f acc[RM];
 #pragma unroll
     for (int i = 0; i < RM; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t top = 0;  // largest scale byte met
     for (int b = wave; b < nb; b += waves) {
       const int64_t o = (int64_t)b * kF8Block;
       const v4u w0 = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wr + o));
       const v4u w1 = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wr + o + 16));
-      const float sw = pow2_of(wsr[b]);
+      const uint32_t cw = wsr[b];
+      top = cw > top ? cw : top;
+      const float sw = pow2_of(cw);
       const bf16x8 vb[4] = {widen8(w0.x, w0.y, sw), widen8(w0.z, w0.w, sw),
                             widen8(w1.x, w1.y, sw), widen8(w1.z, w1.w, sw)};
 #pragma unroll
       for (int i = 0; i < RM; ++i) {
         const v4u a0 = *reinterpret_cast<const v4u *>(xr[i] + o);
         const v4u a1 = *reinterpret_cast<const v4u *>(xr[i] + o + 16);
-        const float sx = pow2_of(xsr[i][b]);
+        const uint32_t cx = xsr[i][b];
+        top = cx > top ? cx : top;
+        const float sx = pow2_of(cx);
         const bf16x8 va[4] = {widen8(a0.x, a0.y, sx), widen8(a0.z, a0.w, sx),
                               widen8(a1.x, a1.y, sx), widen8(a1.z, a1.w, sx)};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va[k], vb[k], acc[i], 0, 0, 0);
       }
+    }
+    if (__any(top >= kF8Split)) {
+#pragma unroll
+      for (int i = 0; i < RM; ++i) acc[i] = split_16x16(xr[i], xsr[i], wr, wsr, wave, waves, nb);
     }
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
