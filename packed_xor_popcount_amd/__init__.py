@@ -57,7 +57,7 @@ class BnnError(RuntimeError):
 
 
 _lib = None
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = None  # device index -> handle of its current stream, found at the first call
 
 
 def library():
@@ -122,7 +122,11 @@ def _check(status: int, where: str) -> None:
 
 def _stream(t: torch.Tensor) -> int:
     # the current stream's handle, without building a Stream object (a
-    # microsecond of a decode step's host time)
+    # microsecond of a decode step's host time) where torch has that lookup
+    global _raw_stream
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
     return _raw_stream(t.device.index)
 
 
