@@ -10,7 +10,7 @@
 // | 0x3F3F3F3F holds in byte q the upper byte of element 8q + p, and one byte
 // permute of (S_2i, S_2i+1) makes the operand pair (8q + 2i, 8q + 2i + 1). That
 // is one VALU operation per element (8 + 8 + 16 for 32), and the activations
-// stay in their natural order.  The factor 2 is applied with alpha, exactly.
+// stay in their natural order.  The factor 2 is applied to the sum, exactly.
 //
 // v_mfma_f32_32x32x16_bf16: lane l supplies row / column l % 32; lanes 0-31
 // take the first 32 elements of a 64-element step, lanes 32-63 the last 32,
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
     for (int cb = 0; cb < CB; ++cb) {
       int n = n0 + cb * 32 + li;
       n = n < N ? n : N - 1;
-      al[cb] = 2.0f * (alpha ? alpha[(int64_t)e * N + n] : 1.0f);
+      al[cb] = alpha ? alpha[(int64_t)e * N + n] : 1.0f;
     }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kGroupThreads, 2)
         T *yr = y + (int64_t)r * N + n0 + li;
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
-          if (n0 + cb * 32 + li < N) yr[cb * 32] = (T)(acc[rb][cb][v] * al[cb] * rs);
+          if (n0 + cb * 32 + li < N) yr[cb * 32] = (T)(2.0f * acc[rb][cb][v] * al[cb] * rs);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(512)
         for (int w = 0; w < waves; ++w) sum += join[w][q];
         const int r = r0 + i * 16 + q / (16 * RC), c = n0 + q % (16 * RC);
         if (r < hi && c < N) {
-          float o = sum * (2.0f * (alpha ? alpha[(int64_t)e * N + c] : 1.0f));
+          float o = 2.0f * sum * (alpha ? alpha[(int64_t)e * N + c] : 1.0f);
           if (row_scale) o *= row_scale[r];
           y[(int64_t)r * N + c] = (T)o;
         }
