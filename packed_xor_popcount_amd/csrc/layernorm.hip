@@ -397,26 +397,30 @@ __global__ void __launch_bounds__(kLongThreads)
 }
 
 // Columns' sums over the P partial rows, in a fixed order: 16 columns x 16
-// parts of the rows per block, the parts joined through LDS.
+// parts of the rows per block and turn, the parts joined through LDS.
 __global__ void __launch_bounds__(256)
     ln_bwd_finish_kernel(const float *__restrict__ part, int P, int N, float *__restrict__ dgamma,
                          float *__restrict__ dbeta) {
   __shared__ float lds[16][17];
   const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
-  const int64_t i = (int64_t)blockIdx.x * 16 + c;
-  float s = 0.0f;
-  if (i < 2 * (int64_t)N) {
+  const int64_t columns = 2 * (int64_t)N;
+  for (int64_t i0 = (int64_t)blockIdx.x * 16; i0 < columns; i0 += (int64_t)gridDim.x * 16) {
+    const int64_t i = i0 + c;
+    float s = 0.0f;
+    if (i < columns) {
 #pragma unroll 8
-    for (int p = q; p < P; p += 16) s += part[(int64_t)p * 2 * N + i];
-  }
-  lds[q][c] = s;
-  __syncthreads();
-  if (q != 0 || i >= 2 * (int64_t)N) return;
-  s = 0.0f;
+      for (int p = q; p < P; p += 16) s += part[p * columns + i];
+    }
+    __syncthreads();  // the last turn's parts have been read
+    lds[q][c] = s;
+    __syncthreads();
+    if (q != 0 || i >= columns) continue;
+    s = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) s += lds[k][c];
-  if (i < N) dgamma[i] = s;
-  else dbeta[i - N] = s;
+    for (int k = 0; k < 16; ++k) s += lds[k][c];
+    if (i < N) dgamma[i] = s;
+    else dbeta[i - N] = s;
+  }
 }
 
 // Threads per row and chunks per thread by the row's length: a wave holds up
@@ -532,8 +536,10 @@ hipError_t launch_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int
     if (e != hipSuccess) return e;
   }
   if (dgamma && (M == 0 || layernorm_bwd_partials(M, N) > 0)) {
-    hipLaunchKernelGGL(ln_bwd_finish_kernel, dim3((unsigned)((2 * N + 15) / 16)), dim3(256), 0, s,
-                       part, (int)P, (int)N, dgamma, dbeta);
+    // A launch takes less than 2^32 threads: wider rows go round in turns.
+    const int64_t want = (2 * N + 15) / 16, blocks = want < (1 << 20) ? want : (1 << 20);
+    hipLaunchKernelGGL(ln_bwd_finish_kernel, dim3((unsigned)blocks), dim3(256), 0, s, part, (int)P,
+                       (int)N, dgamma, dbeta);
     return hipGetLastError();
   }
   return hipSuccess;

@@ -4,8 +4,10 @@ of the register kernels."""
 from __future__ import annotations
 
 import pytest
+import torch
 
-from tests.test_gpu_layernorm import DT, check
+import packed_xor_popcount_amd as bnn
+from tests.test_gpu_layernorm import DEV, DT, check, gam
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +23,23 @@ def test_second_rows(M, N, dtype):
 def test_second_rows_strided(N):
     for dtype in DT.values():
         check(2100 if N == 4096 else 600, N, dtype, pad=5, shift=3, affine=False, seed=N)
+
+
+def test_rows_past_2_27_columns():
+    """More columns than one launch of 16 threads each covers with 2^32
+    threads.  Sums over two rows: gamma(M + 20) sum|dy xh| as for any M."""
+    M, N = 2, 2 ** 27 + 13
+    print("layernorm", M, N, flush=True)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(27)
+    x = torch.randn(M, N, generator=g, device=DEV).to(torch.bfloat16)
+    dy = torch.randn(M, N, generator=g, device=DEV).to(torch.bfloat16)
+    mean, rstd = torch.tensor([0.1, -0.2], device=DEV), torch.tensor([0.9, 1.1], device=DEV)
+    dx, dg, db = bnn.layernorm_bwd(dy, x, mean, rstd)
+    for lo in range(0, N, 2 ** 24):
+        part = slice(lo, min(N, lo + 2 ** 24))
+        d = dy[:, part].double()
+        xh = (x[:, part].double() - mean.double()[:, None]) * rstd.double()[:, None]
+        assert ((dg[part].double() - (d * xh).sum(0)).abs() <= gam(M + 20) * (d * xh).abs().sum(0)).all()
+        assert ((db[part].double() - d.sum(0)).abs() <= gam(M + 16) * d.abs().sum(0)).all()
+        assert dx[:, part].isfinite().all()
