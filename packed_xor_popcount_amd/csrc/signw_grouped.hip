@@ -84,33 +84,41 @@ __device__ __forceinline__ bool find_tile(const int32_t *off, int E, int T, int6
 
 // ---------------------------------------------------------------------------
 // Matrix-core kernel.  Eight waves side by side along N, each RB x CB tiles of
-// 32 x 32, two waves per SIMD: one wave's sign operands are made while the
-// other's matrix instructions run.  The weights need next to no bytes, so the
-// tile is wide (every activation row read from L2 serves 8 CB 32 columns) and
-// low (few rows are wasted at a group's end).
+// 32 x 32: one wave's sign operands are made while another's matrix
+// instructions run.  The weights need next to no bytes, so the tile is wide
+// (every activation row read from L2 serves 256 columns) and low (few rows are
+// wasted at a group's end); two blocks share a CU and hide each other's
+// barriers.  Tiles of 128 x 512, one block a CU, read the activations half as
+// often, but lose more at the groups' ends: 16384 routed rows on 32 experts of
+// 4096 x 4096 622-652 us against 587-615 us, on 64 experts 701-709 against
+// 625-628, one group of them all 523 against 532; 16384 x 1024 x 1024 on 8
+// experts at 128 x 256 71 against 47.
 //
 // Per 64-element step the block's activation rows (128 bytes each, their
 // 16-byte pieces swapped by row so that the reads spread over the banks) pass
 // through one of two LDS buffers; the step after is on its way through
 // registers, loaded at any alignment, zero past K.  The columns' weight words
 // go the same way, eight steps at a time: one word of a column per step would
-// move a cache line for eight of its bytes (719 -> 633 us below).
+// move a cache line for eight of its bytes.
 //
-// 16384 rows on 32 experts of 4096 x 4096, bf16 out: 600 us, 0.92 PFLOP/s; one
-// group of them all 485 us, 1.13 PFLOP/s (a dense library product of bf16
-// weights: 431 us).  Bound by the bf16 matrix rate, the last rows of each
-// group's tiles and the last round of blocks.
+// 16384 routed rows on 32 experts of 4096 x 4096, bf16 out: 547 us, 1.0 PFLOP/s
+// (a launch among others; single launches under a profiler 585-620 us); one group
+// of them all 499 us, 1.1 PFLOP/s (a dense library product of bf16 weights:
+// 355 us).  The matrix cores are busy 47 % of the cycles, the VALU, which makes the
+// operands and addresses, about as long; 6 % of the instructions are for rows
+// past a group's end.
 
 constexpr int kGroupThreads = 512;
+constexpr int kGroupRB = 2, kGroupCB = 1;  // a wave's tiles
 
-template <int RB, int CB, typename T>
+template <typename T>
 __global__ void __launch_bounds__(kGroupThreads, 2)
     signw_grouped_kernel(const uint16_t *__restrict__ x, int64_t ldx, int xrows,
                          const int32_t *__restrict__ rows, const int32_t *__restrict__ off,
                          const uint64_t *__restrict__ wp, const float *__restrict__ alpha,
                          const float *__restrict__ row_scale, T *__restrict__ y, int R, int E,
                          int N, int K, int tiles_n, int64_t most) {
-  constexpr int BM = RB * 32, BN = 8 * CB * 32;
+  constexpr int RB = kGroupRB, CB = kGroupCB, BM = RB * 32, BN = 8 * CB * 32;
   constexpr int PIECES = BM * 8 / kGroupThreads;  // 16-byte pieces a thread stages
   static_assert(PIECES >= 1 && BN <= kGroupThreads, "every thread stages");
   __shared__ __attribute__((aligned(16))) unsigned char as[2][BM * 128];
@@ -417,19 +425,19 @@ void launch_rows(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *r
                      static_cast<T *>(y), (int)R, (int)E, (int)N, (int)K, (int)tiles_n, most);
 }
 
-template <int RB, int CB, typename T>
+template <typename T>
 void launch_tile(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows,
                  const int32_t *off, const uint64_t *wp, const float *alpha,
                  const float *row_scale, void *y, int64_t R, int64_t E, int64_t N, int64_t K,
                  hipStream_t s) {
-  constexpr int BM = RB * 32, BN = 8 * CB * 32;
+  constexpr int BM = kGroupRB * 32, BN = 8 * kGroupCB * 32;
   const int64_t tiles_n = (N + BN - 1) / BN;
   // Row tiles of any grouping of R rows: the whole ones and one partial tile
   // for each group that has rows; a multiple of the eight XCDs.
   const int64_t tiles_m = (R / BM + (E < R ? E : R) + 7) / 8 * 8;
   const int64_t most = tiles_m * tiles_n;
   const int64_t blocks = most < (1 << 20) ? most : (1 << 20);
-  hipLaunchKernelGGL((signw_grouped_kernel<RB, CB, T>), dim3((unsigned)blocks),
+  hipLaunchKernelGGL((signw_grouped_kernel<T>), dim3((unsigned)blocks),
                      dim3(kGroupThreads), 0, s, x, ldx, (int)xrows, rows, off, wp, alpha, row_scale,
                      static_cast<T *>(y), (int)R, (int)E, (int)N, (int)K, (int)tiles_n, most);
 }
@@ -440,27 +448,22 @@ void launch(const uint16_t *x, int64_t ldx, int64_t xrows, const int32_t *rows, 
             int64_t E, int64_t N, int64_t K, int algo, hipStream_t s) {
   // All the host knows of the groups is R and E.  The few-row kernel serves
   // small groups and products with too few tiles to fill the card; measured
-  // (device, bf16 out, N x K): 256 rows on 64 experts of 1024 x 4096 27 us
-  // against 45 us on tiles, 602 on 10 of 700 x 1000 12 against 18; 2000 on 128
-  // of 1024 x 512 35 against 22.
+  // (device, bf16 out, N x K): 256 rows on 64 experts of 1024 x 4096 25 us
+  // against 44 us on tiles, 602 on 10 of 700 x 1000 12 against 17; 2000 on 128
+  // of 1024 x 512 27 against 15.  A small mean can hide a large group: 640 rows
+  // on 64 experts of 1024 x 4096, 577 of them on one, 62 us against 61; 1280 on
+  // 128 of 4096 x 4096, 1153 on one, 449 against 319 (a caller who knows of such
+  // a router names BNN_ALGO_MFMA).
   const int64_t mean = R / E, active = E < R ? E : R;
-  const auto tiles = [&](int64_t bm, int64_t bn) {  // about; half a tile lost per group
-    return (R / bm + active / 2) * ((N + bn - 1) / bn);
-  };
-  if (algo == BNN_ALGO_AUTO)
-    algo = mean <= 12 || tiles(64, 256) < 64 ? BNN_ALGO_GEMV : BNN_ALGO_MFMA;
-  auto run = launch_tile<2, 1, T>;
+  const int64_t tiles = (R / 64 + active / 2) * ((N + 255) / 256);  // half a tile lost per group
+  if (algo == BNN_ALGO_AUTO) algo = mean <= 12 || tiles < 64 ? BNN_ALGO_GEMV : BNN_ALGO_MFMA;
+  auto run = launch_tile<T>;
   if (algo == BNN_ALGO_GEMV) {
-    // 16 columns a block while 64 would leave CUs idle (one token on 8 experts
-    // of 1024 x 4096: 7 us); 64 beyond (256 rows on 64 experts: 39 -> 27 us).
+    // 16 columns a block while 64 would leave CUs idle (8 rows on 8 of 64 experts
+    // of 1024 x 4096: 7 us against 9); 64 beyond (256 rows on 64: 45 -> 25 us).
     run = active * ((N + 63) / 64) < 512 ? launch_rows<1, 1, T>
           : mean <= 8                    ? launch_rows<1, 4, T>
                                          : launch_rows<2, 4, T>;
-  } else if (mean >= 128) {
-    // 128-row tiles waste more of a group's last tile: 4000 rows on 32 experts
-    // of 2048 x 2048 61 us on 64-row tiles, 96 on 128; 2000 on 8 of 1001 x
-    // 1001 49 against 36.  512 columns once that still fills the card.
-    run = tiles(128, 512) >= 512 ? launch_tile<4, 2, T> : launch_tile<4, 1, T>;
   }
   run(x, ldx, xrows, rows, off, wp, alpha, row_scale, y, R, E, N, K, s);
 }
