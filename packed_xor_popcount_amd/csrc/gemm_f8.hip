@@ -425,11 +425,20 @@ void launch_tile(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const 
 template <bool FAST, typename T>
 void launch(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws, void *y,
             int64_t M, int64_t N, int64_t K, hipStream_t s) {
-  const auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  // Large tiles once the outputs fill enough of them, whole or not; measured
+  // (device, bf16 out, small against large tiles, and the same FAST):
+  //   2048 x 4096 x 4096 (128 of them)  77 / 89 us    62 / 54 us
+  //   300 x 30000 x 2048 (137)          49 / 55       36 / 34
+  //   3000 x 5000 x 1000 (229)          45 / 33       33 / 23
+  //   4096 x 4096 x 4096 (256)         154 / 105     124 / 60
+  //   33 x 65536 x 1024 (33, of 256)    15 / 29       13 / 19
+  // Few-row kernel against small tiles: 33 x 4096 x 4096 18 / 21 us, 64 rows 22 /
+  // 21, 33 x 65536 x 1024 48 / 15.
+  const int64_t filled = M * N / (256 * 256);
   auto run = launch_tile<2, 4, 4, 2, 2, FAST, T>;
   if (M <= 16) run = launch_rows<1, T>;
   else if (M <= 32) run = launch_rows<2, T>;
-  else if (tiles(256, 256) < 128) run = launch_tile<2, 4, 1, 1, 3, FAST, T>;
+  else if (filled < (FAST ? 128 : 160)) run = launch_tile<2, 4, 1, 1, 3, FAST, T>;
   run(xq, xs, wq, ws, y, M, N, K, s);
 }
 

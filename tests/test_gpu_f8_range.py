@@ -12,13 +12,14 @@ import pytest
 import torch
 
 import packed_xor_popcount_amd as bnn
-from tests.test_gpu_f8 import DEV, DT, U, decode
+from tests.test_gpu_f8 import DEV, DT, U, decode, test_nan_reaches_its_row_and_column_only as check_nan
+from tests.test_gpu_f8 import test_product_exact as check_exact, test_product_rounding as check_rounding
 
 pytestmark = pytest.mark.gpu
 
 # Row counts and widths that reach each kernel: few rows (16 and 32 at a
 # time), small tiles, large tiles.
-PLACES = [(1, 70), (16, 33), (17, 70), (32, 65), (33, 70), (300, 129), (2900, 2999)]
+PLACES = [(1, 70), (16, 33), (17, 70), (32, 65), (33, 70), (300, 129), (2900, 2999), (3300, 3301)]
 
 
 def cancelling(g, rows, k, weight):
@@ -136,3 +137,19 @@ def test_smallest_scale(M, N, where, dtype):
     else:
         x, w = plain(M), tiny(N)
     check_sizes(x, w, K, dtype, 2.0 ** -90)  # above it no product is near the subnormals
+
+
+@pytest.mark.parametrize("M,N,K", [(3300, 3301, 300), (2600, 4300, 1024), (10700, 1000, 129), (4096, 2600, 0)])
+def test_large_tiles(M, N, K):
+    """Products of enough outputs for the large tiles, whole and partial."""
+    if K == 0:
+        z = torch.empty(max(M, N), 0, dtype=torch.uint8, device=DEV)
+        for dtype in DT.values():
+            assert not bnn.gemm_f8(z[:M], z[:M], z[:N], z[:N], 0, out=torch.full((M, N), 9.0, device=DEV, dtype=dtype)).any()
+        return
+    check_exact(M, N, K)
+    check_rounding(M, N, K)
+
+
+def test_nan_in_large_tiles():
+    check_nan(160000)  # by 70 columns: as many outputs as 170 large tiles
