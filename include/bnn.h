@@ -323,6 +323,9 @@ bnn_status bnn_gemv_act(const void *x, int dtype, int64_t ldx, const uint64_t *w
  *   eps    finite and >= 0, else BNN_E_ARG.
  * N = 0 with M > 0 is BNN_E_SHAPE (an empty row has no mean); M = 0 launches
  * nothing.  A row holding a NaN or an infinity gives NaN in that row only.
+ * Sums and squares have the range of fp32: a row whose sum overflows gives an
+ * infinite mean and y = NaN, one whose centred squares do (values of about 1e19)
+ * r = 0 and y = beta; with eps = 0 a constant row gives NaN.
  * Errors: BNN_E_DTYPE, BNN_E_SHAPE, BNN_E_ARG, BNN_E_NULL, BNN_E_ALIGN,
  * BNN_E_LAUNCH.
  */
@@ -397,10 +400,11 @@ bnn_status bnn_quant_f8(const void *src, int dtype, int64_t rows, int64_t k, int
  *   y[m][n] = sum_b 2^(xs[m][b] + ws[n][b] - 254) sum_{k in block b} xq[m][k] * wq[n][k],
  * products exact, sums fp32 on the matrix cores (within the bound of an fp32
  * sum of K terms), rounded once to y's type; their order depends on the sizes
- * and types only, but for outputs beside a block of scale byte 247 or more.
- * Decoded values below 2^-126 may count as zero and those above 2^128 as
- * infinite; bnn_quant_f8 makes none of the latter (2^128 itself, and with it
- * scale byte 247, is what it makes of magnitudes from 1.9375 * 2^127 on).
+ * and types only, but for outputs near a block of scale byte 247 or more (a
+ * block with a magnitude above 1.75 * 2^127), which take a slower way.  Decoded
+ * values below 2^-126 may count as zero and those above 2^128 as infinite;
+ * bnn_quant_f8 makes none of the latter (2^128 itself is what it makes of
+ * magnitudes from 1.9375 * 2^127 on).
  *
  *   xq, xs   M rows of K columns, wq, ws  N rows of K columns; q buffers
  *            16-byte, s buffers 4-byte aligned.  The bytes past K have to be

@@ -54,8 +54,8 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi, float scale) 
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-// From scale byte 247 (2^120) on a value can decode to 2^128, past bf16's range
-// (the quantiser makes it of magnitudes from 1.9375 * 2^127 on).  The kernels
+// Under scale byte 247 (2^120) and larger ones a value can decode to 2^128, past
+// bf16's range (the quantiser makes it of magnitudes from 1.9375 * 2^127 on).  The kernels
 // note the largest scale byte that a wave meets, and a wave that met such a
 // one computes its sums again here, with operands in two parts: twice the half
 // of such a block's values, once those of other blocks and then zeros.  Rare,
@@ -99,11 +99,13 @@ __device__ __forceinline__ v4f split_16x16(const uint8_t *xr, const uint8_t *xs,
 // the row's number, so that 16 neighbouring rows meet all 64 banks (by the whole
 // number, rows 8 apart collided; the conflict counter now reads 0).
 //
-// 4096 x 11008 x 4096, bf16 out: 293 us, 1.26 PFLOP/s (a large library product
-// of bf16 matrices: 1.38); FAST 177 us, 2.09 PFLOP/s (a library product of one
-// scale: 189 us).  256 x 4096 x 4096: 22 and 17 us; 2048 x 4096 x 4096: 86 and
-// 51 us.  Bands of row tiles (below) took the large FAST product from 250 us.
-// Under about 100 tiles the steps' latency bounds it, 0.5 us each.
+// 4096 x 11008 x 4096, bf16 out, a launch among others: 293-302 us, 1.2 PFLOP/s (a
+// large library product of bf16 matrices: 1.38); FAST 177 us, 2.09 PFLOP/s (a
+// library product of one scale: 189 us).  The widening product's matrix cores
+// are busy 56 % of the cycles (2.1 GHz); the rest goes to the widening between
+// them and to a last round of 176 of 256 blocks.  256 x 4096 x 4096: 22 and 17 us.
+// Bands of row tiles (below) took the large FAST product from 250 us.  Under
+// about 100 tiles the steps' latency bounds it, 0.5 us each.
 
 constexpr int kF8Threads = 512;
 
@@ -323,7 +325,8 @@ __global__ void __launch_bounds__(kF8Threads, 2)
 // Few-row kernel: 16 columns x 16 RM rows per block, the blocks of K dealt out
 // to the block's waves and their sums joined through LDS in a fixed order.
 // Every wave streams its part of the weight rows from memory exactly once, so
-// small products keep the whole card busy; bound by the weights' bytes.
+// small products keep the whole card busy.  1 x 4096 x 4096: 7.4 us, two blocks of K
+// a wave one after the other; 1 x 65536 x 4096: 60 us, 4.5 TB/s, the weights' bytes.
 // Always on bf16 instructions: the matrix rate does not matter here.
 //
 // v_mfma_f32_16x16x32_bf16: lane l supplies row / column l % 16; lane group

@@ -119,9 +119,9 @@ __device__ __forceinline__ void row_sum(float (&v)[A], float *lds, int &flip) {
 constexpr int block_of(int tpr) { return tpr < 256 ? 256 : tpr; }
 
 // Bound by HBM: x is read and y written once, gamma and beta stay in the
-// registers of a block that walks over rows.  16384 x 4096 bf16: 49 us,
-// 5.5 TB/s (a large copy reaches 5.1); one row of 4096: 2.8 us, the launch and
-// two joins of the block's sums.
+// registers of a block that walks over rows.  16384 x 4096: bf16 49 us, 5.4 TB/s,
+// fp32 104 us, 5.1 TB/s (a large copy reaches 5.1); one row of 4096: 2.5 us, the
+// launch and two joins of the block's sums.
 template <typename T, int TPR, int C, bool EVEN>
 __global__ void __launch_bounds__(block_of(TPR))
     ln_fwd_kernel(const T *__restrict__ x, int64_t ldx, const float *__restrict__ gamma,
@@ -210,7 +210,7 @@ __device__ void column_sums(const T *dy, int64_t lddy, const T *x, int64_t ldx, 
 }
 
 // The gradient, bound by HBM as well: x and dy are read and dx written once
-// (16384 x 4096 bf16: 88 us + 7 us for the finish, 4.3 TB/s in all);
+// (16384 x 4096 bf16: 80 us + 7 us for the finish, 4.6 TB/s in all);
 // gamma and the block's column sums stay in registers.  A block takes every
 // gridDim.x-th group of rows and leaves its sums in row blockIdx.x of `part`
 // (2 x N: dgamma, then dbeta); rows of one block's waves (TPR = 64) are joined
@@ -325,6 +325,8 @@ __global__ void __launch_bounds__(block_of(TPR))
 
 // Rows too long for registers: one block per row, the row read again from
 // the caches for each pass; the gradient's column sums are kept in `part`.
+// 2048 x 20000 bf16: forward 97 us (1.7 TB/s of x and y), gradient 342 + 14 us:
+// element by element, three dependent passes with a block's join between them.
 constexpr int kLongThreads = 1024;
 
 template <typename T>
@@ -438,7 +440,6 @@ Shape shape_of(int64_t N) {
   return {0, 0};
 }
 
-
 template <typename T, bool EVEN>
 void fwd(const void *xv, int64_t ldx, const float *gamma, const float *beta, void *yv, int64_t ldy,
          float *mean, float *rstd, int64_t M, int64_t N, float eps, hipStream_t s) {
@@ -462,8 +463,8 @@ void fwd(const void *xv, int64_t ldx, const float *gamma, const float *beta, voi
 
 // Up to 64 rows for each wave of a block (and no longer rows than a block
 // holds) the column sums are taken straight from the inputs, in the same
-// launch: 256 x 4096 bf16 7.2 us against 13.4, 1024 x 16384 37 against 54;
-// beyond that the partial rows win (1024 x 4096: 21 us against 49).
+// launch: 256 x 4096 bf16 7.7 us against 13.2, 1024 x 16384 37 against 55;
+// beyond that the partial rows win (1024 x 4096: 20 us against 49).
 bool direct_sums(int64_t M, int64_t N) {
   const Shape sh = shape_of(N);
   return sh.tpr != 0 && M <= block_of(sh.tpr);

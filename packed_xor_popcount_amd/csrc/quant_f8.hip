@@ -7,8 +7,9 @@
 // NaN and do not enter a.
 //
 // Both forms are bound by HBM: one read of the source, one byte written per
-// element.  4096 x 4096 bf16: rows 11.8 us (4.3 TB/s), transposed 13.9 us; 11008 x
-// 4096 fp32: rows 34 us (6.7 TB/s), transposed 36 us.
+// element.  4096 x 4096 bf16 (inputs that fit the Infinity Cache): rows 11.7 us
+// (4.3 TB/s), transposed 13.8 us; 11008 x 4096 fp32: rows 39 us (5.8 TB/s),
+// transposed 47 us (4.8 TB/s; its writes are pieces of 32 bytes).
 #include "bnn_internal.h"
 #include "f8.h"
 

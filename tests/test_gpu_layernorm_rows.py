@@ -43,3 +43,23 @@ def test_rows_past_2_27_columns():
         assert ((dg[part].double() - (d * xh).sum(0)).abs() <= gam(M + 20) * (d * xh).abs().sum(0)).all()
         assert ((db[part].double() - d.sum(0)).abs() <= gam(M + 16) * d.abs().sum(0)).all()
         assert dx[:, part].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N", [70, 4096, 20001])
+def test_past_the_range_of_fp32(N, dtype):
+    """A row whose squares overflow gives r = 0 and y = beta, one whose sum
+    overflows an infinite mean and y = NaN; the rows beside them are as they are alone."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(N)
+    x = torch.randn(5, N, generator=g, device=DEV).to(DT[dtype])
+    beta = torch.randn(N, generator=g, device=DEV)
+    ref, _, r = bnn.layernorm_fwd(x, None, beta)
+    low = torch.finfo(torch.bfloat16).min
+    x[1, N // 2] = low
+    x[3, 1] = x[3, N - 1] = low
+    y, mu2, r2 = bnn.layernorm_fwd(x, None, beta)
+    keep = [0, 2, 4]
+    assert torch.equal(y[keep], ref[keep]) and torch.equal(r2[keep], r[keep])
+    assert r2[1] == 0 and torch.equal(y[1], beta.to(DT[dtype]))
+    assert mu2[3].isinf() and y[3].isnan().all()
