@@ -6,8 +6,9 @@
 // 128 b .. 128 b + 127.  The power of two is the smallest that brings the
 // block's largest magnitude to at most 448, the largest e4m3 value.  A power
 // of two costs an 8-bit FLOAT no precision (its relative step does not depend
-// on the exponent), and the matrix cores apply it themselves, so a product
-// needs no arithmetic on its sums between blocks.
+// on the exponent), and both the widening to bf16 and the 8-bit matrix
+// instructions apply it themselves, so a product needs no arithmetic on its
+// sums between blocks.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -55,14 +55,14 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 // Under scale byte 247 (2^120) and larger ones a value can decode to 2^128, past
-// bf16's range (the quantiser makes it of magnitudes from 1.9375 * 2^127 on).  The kernels
-// note the largest scale byte that a wave meets, and a wave that met such a
-// one computes its sums again here, with operands in two parts: twice the half
-// of such a block's values, once those of other blocks and then zeros.  Rare,
-// so nothing is staged, and one copy of the arithmetic keeps the registers of the
-// ordinary path: 4096 x 11008 x 4096 with 2^128 in one row of x 2.4 ms, in every
-// row 4.4 ms (0.29 ms without).  The 8-bit instructions need none of this: they
-// apply the scales past bf16's range.
+// bf16's range (the quantiser makes it of magnitudes from 1.9375 * 2^127 on).
+// The kernels note the largest scale byte that a wave meets, and a wave that met
+// such a one computes its sums again here, with operands in two parts: twice the
+// half of such a block's values, once those of other blocks and then zeros.
+// Rare, so nothing is staged, and one copy of the arithmetic keeps the registers
+// of the ordinary path: 4096 x 11008 x 4096 with 2^128 in one row of x 2.4 ms, in
+// every row 4.4 ms (0.3 ms without).  The 8-bit instructions need none of this:
+// they apply the scales past bf16's range.
 constexpr uint32_t kF8Split = 247;
 
 // Sums of 16 x 16 outputs over blocks b0, b0 + step, ...: xr, wr the lane's
