@@ -37,7 +37,7 @@
  * library allocates nothing, frees nothing, keeps no state between calls
  * and never synchronizes: each call enqueues its kernels on `stream` (a
  * hipStream_t; NULL means the default stream) and returns.  Inputs and
- * outputs must not overlap.
+ * outputs must not overlap, but where a call says that they may.
  *
  * Pad bits.  Outputs that are packed (bnn_pack_signs, bnn_gemm_sign_repack)
  * have every pad bit 0 (+1).  Packed INPUTS may hold anything in their pad
@@ -77,7 +77,8 @@ typedef enum bnn_status {
 
 typedef enum bnn_dtype {
   BNN_FP32 = 0, /* IEEE binary32 */
-  BNN_BF16 = 1  /* bfloat16, the upper 16 bits of a binary32 */
+  BNN_BF16 = 1, /* bfloat16, the upper 16 bits of a binary32 */
+  BNN_F8 = 2    /* the block-scaled 8-bit form (bnn_quant_f8); taken only where a call says so */
 } bnn_dtype;
 
 /* Output stage of a product (see bnn_gemm_ex). */
@@ -472,6 +473,170 @@ bnn_status bnn_gemm_signw_grouped(const void *x, int64_t ldx, int64_t xrows, con
                                   const int32_t *offsets, const uint64_t *wp, const float *alpha,
                                   const float *row_scale, void *y, int dtype, int64_t R, int64_t E,
                                   int64_t N, int64_t K, int algo, void *stream);
+
+/*
+ * bnn_route_fwd -- the router ahead of bnn_gemm_signw_grouped: each of T tokens
+ * is sent to its k best of E experts.  An expert is open to a token that is
+ * valid where its logit is above -inf; NaN is never chosen.  Per token, with
+ * m the largest logit, S = sum exp(z - m) and p = exp(z - m) / S:
+ *   choices  the k largest open logits, largest first, equal ones in the order
+ *            of their index;
+ *   weights  p at the choices or, with normalise = 1, exp(z - m) over its sum
+ *            over the token's choices.
+ * The T k slots (t, j) are sorted by expert, slots of one expert in the order of
+ * t k + j, slots without an expert last.  With Tv the number of tokens that have
+ * an expert, f_e = counts[e] / (k Tv) and P_e = sum_t p_te / Tv:
+ *   loss = E sum_e f_e P_e   (1 for an even router),   slope[e] = E f_e / Tv,
+ * both 0 without such tokens.  Sums are fp32, in an order that goes by the sizes.
+ *
+ *   z        T rows of E logits of type dtype, row stride ldz >= E, element-aligned.
+ *   valid    T bytes (0: the token is not routed), or NULL.
+ *   experts  T x k int32, -1 where no expert is left.  weights  T x k fp32, 0 there.
+ *   place    T x k int32: the slot's row, or -2 - row without an expert.
+ *   rows     T k int32: each row's token; -1 behind the last group.
+ *   offsets  E + 1 int32, counts  E int32.
+ *   stats    T x 2 fp32: m and 1 / S (0, 0 for a token without an expert).
+ *   slope, loss  E and 1 fp32; both NULL: not computed.
+ *   workspace    at least bnn_route_fwd_workspace(T, E, k) bytes, 16-byte aligned,
+ *            used on `stream` until the call's kernels have run; may be NULL when
+ *            that is 0.
+ * A valid token with a NaN or +inf among its logits has the weights NaN, and the
+ * loss is NaN.  1 <= k <= E, k <= 32, E <= 1024, T k < 2^30.  T = 0 writes offsets,
+ * counts, slope and loss.  Errors: BNN_E_DTYPE, BNN_E_ARG (normalise not 0 or
+ * 1), BNN_E_SHAPE, BNN_E_NULL, BNN_E_ALIGN, BNN_E_LAUNCH.
+ */
+int64_t bnn_route_fwd_workspace(int64_t T, int64_t E, int64_t k);
+bnn_status bnn_route_fwd(const void *z, int dtype, int64_t ldz, const uint8_t *valid,
+                         int32_t *experts, float *weights, int32_t *place, int32_t *rows,
+                         int32_t *offsets, int32_t *counts, float *stats, float *slope,
+                         float *loss, void *workspace, int64_t ws_bytes, int64_t T, int64_t E,
+                         int64_t k, int normalise, void *stream);
+
+/*
+ * bnn_route_bwd -- the gradient of bnn_route_fwd by its logits, the choices (and
+ * with them counts and slope) held fixed:
+ *   g_e = dloss slope[e]  (+ dweights at the choices, normalise = 0)
+ *   dz_e = p_e (g_e - sum_i p_i g_i)
+ *          (+ w_j (dweights_j - sum_i w_i dweights_i) at the choices, normalise = 1)
+ * Zero for a token without an expert.
+ *
+ *   experts, weights, stats, slope   from the forward pass, of the same z.
+ *   dweights  T x k fp32 or NULL (0).  dloss  1 fp32; slope and dloss both
+ *             NULL: no loss.
+ *   dz        T rows of E values of type dtype, row stride lddz >= E.
+ * Sizes and errors as bnn_route_fwd; T = 0 launches nothing.
+ */
+bnn_status bnn_route_bwd(const void *z, int dtype, int64_t ldz, const int32_t *experts,
+                         const float *weights, const float *stats, const float *slope,
+                         const float *dweights, const float *dloss, void *dz, int64_t lddz,
+                         int64_t T, int64_t E, int64_t k, int normalise, void *stream);
+
+/*
+ * bnn_combine_fwd -- the sum of the experts' outputs at each token, behind
+ * bnn_gemm_signw_grouped:
+ *   out[t] = residual[t] + sum_j weights[t][j] y[place[t][j]]
+ * in fp32, slots in the order of j, rounded once.  A slot whose place is negative
+ * (or >= R) has no expert and adds nothing.
+ *
+ *   y         R rows of N values of type ydtype (BNN_FP32 / BNN_BF16), row stride
+ *             ldy >= N, element-aligned.
+ *   place     T x k int32 (bnn_route_fwd).  weights  T x k fp32, or NULL (1).
+ *   residual  T rows of type dtype, row stride ldr >= N, or NULL (0).
+ *   out       T rows of type dtype (BNN_FP32 / BNN_BF16), row stride ldo >= N;
+ *             it may be the residual itself (same pointer and stride).
+ * k >= 1, T k < 2^30.  T = 0 or N = 0 launches nothing.  Errors: BNN_E_DTYPE,
+ * BNN_E_SHAPE, BNN_E_NULL, BNN_E_ALIGN, BNN_E_LAUNCH.
+ */
+bnn_status bnn_combine_fwd(const void *y, int ydtype, int64_t ldy, int64_t R,
+                           const int32_t *place, const float *weights, const void *residual,
+                           int64_t ldr, void *out, int dtype, int64_t ldo, int64_t T, int64_t N,
+                           int64_t k, void *stream);
+
+/*
+ * bnn_combine_bwd -- the gradient of bnn_combine_fwd:
+ *   dy[place[t][j]] = weights[t][j] dout[t],   dweights[t][j] = <dout[t], y[place[t][j]]>.
+ * A slot with place = -2 - r writes zeros to row r of dy; slots without an
+ * expert have dweights 0.  Each row of dy belongs to one slot at most (as
+ * bnn_route_fwd places them): a row that two slots name holds the gradient of
+ * one of them, in part or whole; rows that none names are not written.
+ *
+ *   dout     T rows of N values of type dtype, row stride lddo >= N.
+ *   y, ys    what the forward pass summed, of type ydtype: BNN_FP32 or BNN_BF16
+ *            with row stride ldy >= N, or BNN_F8, its block-scaled 8-bit form
+ *            (bnn_quant_f8; ys the scale bytes, ldy not used).  Not read, and
+ *            may be NULL, without dweights.
+ *   dy       R rows of type dydtype, row stride lddy >= N, or NULL.
+ *   dweights T x k fp32, or NULL.  Sums are fp32, in an order that goes by the
+ *            sizes and types.
+ * Errors: as bnn_combine_fwd.
+ */
+bnn_status bnn_combine_bwd(const void *dout, int dtype, int64_t lddo, const void *y,
+                           const uint8_t *ys, int ydtype, int64_t ldy, int64_t R,
+                           const int32_t *place, const float *weights, void *dy, int dydtype,
+                           int64_t lddy, float *dweights, int64_t T, int64_t N, int64_t k,
+                           void *stream);
+
+/*
+ * bnn_adapter_fwd -- low-rank adapters of many requests beside a shared
+ * projection.  Row t of x uses adapter l = ids[t], with factors A_l (rank x K) and
+ * B_l (rank x N):
+ *   u[t] = A_l x[t],   out[t] = base[t] + scale[l] sum_j u[t][j] B_l[j].
+ * Rows whose id lies outside [0, L) have no adapter: u = 0, out = base.  The ids
+ * may come in any order; rows of one adapter that follow one another are
+ * faster.  Products are exact and sums fp32 (within the bound of fp32 sums of K
+ * and of rank terms); out is rounded once.
+ *
+ *   x      T rows of K bf16 values, row stride ldx >= K, 2-byte aligned.
+ *   ids    T int32.
+ *   a, b   L x rank x K and L x rank x N bf16, contiguous: the rank is the slow
+ *          dimension of both.  scale  L fp32, or NULL (1).
+ *   base   T rows of N values of type dtype (the projection's output), row
+ *          stride ldb >= N, or NULL (0).
+ *   out    T rows of type dtype (BNN_FP32 / BNN_BF16), row stride ldo >= N.  It may
+ *          be the base (same pointer and stride): rows without an adapter are then
+ *          left as they are.
+ *   u      T x rank fp32, what bnn_adapter_bwd takes.
+ *   workspace  at least bnn_adapter_fwd_workspace(T, K, rank) bytes, 16-byte
+ *          aligned, used on `stream` until the call's kernels have run.
+ * 1 <= rank <= 128, T < 2^27, L < 2^20.  T = 0 launches nothing.  Errors:
+ * BNN_E_DTYPE, BNN_E_SHAPE, BNN_E_NULL, BNN_E_ALIGN, BNN_E_LAUNCH.
+ */
+int64_t bnn_adapter_fwd_workspace(int64_t T, int64_t K, int64_t rank);
+bnn_status bnn_adapter_fwd(const void *x, int64_t ldx, const int32_t *ids, const void *a,
+                           const void *b, const float *scale, const void *base, int64_t ldb,
+                           void *out, int64_t ldo, int dtype, float *u, void *workspace,
+                           int64_t ws_bytes, int64_t T, int64_t K, int64_t N, int64_t rank,
+                           int64_t L, void *stream);
+
+/*
+ * bnn_adapter_bwd -- the gradient of bnn_adapter_fwd.  With v[t] = B_l dy[t]:
+ *   dx[t] = base[t] + scale[l] sum_j v[t][j] A_l[j]
+ *   da[l] = scale[l] sum_t v[t] x[t]',   db[l] = scale[l] sum_t u[t] dy[t]'
+ * over the rows t of adapter l.  Products are exact and sums fp32, in a fixed
+ * order: equal inputs give equal bits.
+ *
+ *   dy     T rows of N bf16 values, row stride lddy >= N.
+ *   x, xs  the forward pass's input, of type xdtype: BNN_BF16 with row stride
+ *          ldx >= K, or BNN_F8, its block-scaled 8-bit form (bnn_quant_f8; xs the
+ *          scale bytes, ldx not used).
+ *   u      T x rank fp32 from the forward pass.  ids, a, b, scale  as there.
+ *   base   T rows of K values of type dtype (the gradient that reaches x by the
+ *          projection), row stride ldb >= K, or NULL (0).
+ *   dx     T rows of K values of type dtype, row stride lddx >= K (it may be the
+ *          base: same pointer and stride), or NULL (not computed; a is not read).
+ *   da, db L x rank x K and L x rank x N fp32, overwritten (zeros for an adapter
+ *          without rows); both NULL: not computed (x and u are not read).
+ *   workspace  at least bnn_adapter_bwd_workspace(T, K, N, rank, L) bytes, 16-byte
+ *          aligned, used on `stream` until the call's kernels have run.
+ * Sizes as bnn_adapter_fwd, but L <= 1024.  Errors: as bnn_adapter_fwd.
+ */
+int64_t bnn_adapter_bwd_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t L);
+bnn_status bnn_adapter_bwd(const void *dy, int64_t lddy, const void *x, const uint8_t *xs,
+                           int xdtype, int64_t ldx, const float *u, const int32_t *ids,
+                           const void *a, const void *b, const float *scale, const void *base,
+                           int64_t ldb, void *dx, int64_t lddx, int dtype, float *da, float *db,
+                           void *workspace, int64_t ws_bytes, int64_t T, int64_t K, int64_t N,
+                           int64_t rank, int64_t L, void *stream);
 
 #ifdef __cplusplus
 }

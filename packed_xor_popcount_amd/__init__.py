@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -30,13 +31,14 @@ __all__ = [
     "gemm_sign_repack", "gemm_sign_repack_thr", "flip_words", "gemm_signw_bf16", "chain3",
     "gemm_ex", "gemv_act", "version", "layernorm_fwd", "layernorm_bwd",
     "f8_row_bytes", "f8_scale_bytes", "quant_f8", "gemm_f8",
-    "gemm_signw_grouped",
+    "gemm_signw_grouped", "Routing", "route_fwd", "route_bwd", "combine_fwd", "combine_bwd",
+    "adapter_fwd", "adapter_bwd",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libbnn.so")
 
-BNN_FP32, BNN_BF16 = 0, 1
+BNN_FP32, BNN_BF16, BNN_F8 = 0, 1, 2
 EPI_I32, EPI_SCALED, EPI_REPACK = 0, 1, 2
 ALGO_AUTO, ALGO_GEMV, ALGO_TILED, ALGO_MFMA = 0, 1, 2, 3
 
@@ -45,7 +47,9 @@ EXPORTED = ("bnn_words", "bnn_status_str", "bnn_version", "bnn_pack_signs", "bnn
             "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16", "bnn_chain3",
             "bnn_layernorm_fwd", "bnn_layernorm_bwd_workspace", "bnn_layernorm_bwd",
             "bnn_f8_row_bytes", "bnn_f8_scale_bytes", "bnn_quant_f8", "bnn_gemm_f8",
-            "bnn_gemm_f8_fast", "bnn_gemm_signw_grouped")
+            "bnn_gemm_f8_fast", "bnn_gemm_signw_grouped", "bnn_route_fwd_workspace", "bnn_route_fwd",
+            "bnn_route_bwd", "bnn_combine_fwd", "bnn_combine_bwd", "bnn_adapter_fwd_workspace",
+            "bnn_adapter_fwd", "bnn_adapter_bwd_workspace", "bnn_adapter_bwd")
 
 
 class BnnError(RuntimeError):
@@ -93,6 +97,19 @@ def library():
     lib.bnn_gemm_f8.argtypes = [P, P, P, P, P, I, I64, I64, I64, P]
     lib.bnn_gemm_f8_fast.argtypes = [P, P, P, P, P, I64, I64, I64, P]
     lib.bnn_gemm_signw_grouped.argtypes = [P, I64, I64, P, P, P, P, P, P, I, I64, I64, I64, I64, I, P]
+    lib.bnn_route_fwd.argtypes = [P, I, I64] + [P] * 11 + [I64] * 4 + [I, P]
+    lib.bnn_route_bwd.argtypes = [P, I, I64] + [P] * 7 + [I64] * 4 + [I, P]
+    lib.bnn_combine_fwd.argtypes = [P, I, I64, I64, P, P, P, I64, P, I, I64, I64, I64, I64, P]
+    lib.bnn_combine_bwd.argtypes = [P, I, I64, P, P, I, I64, I64, P, P, P, I, I64, P, I64, I64, I64, P]
+    lib.bnn_adapter_fwd.argtypes = [P, I64, P, P, P, P, P, I64, P, I64, I, P, P] + [I64] * 6 + [P]
+    lib.bnn_adapter_bwd.argtypes = ([P, I64, P, P, I, I64] + [P] * 6 + [I64, P, I64, I, P, P, P] + [I64] * 6
+                                    + [P])
+    for name, n in (("bnn_route_fwd_workspace", 3), ("bnn_adapter_fwd_workspace", 3),
+                    ("bnn_adapter_bwd_workspace", 5)):
+        getattr(lib, name).argtypes, getattr(lib, name).restype = [I64] * n, I64
+    for name in ("bnn_route_fwd", "bnn_route_bwd", "bnn_combine_fwd", "bnn_combine_bwd", "bnn_adapter_fwd",
+                 "bnn_adapter_bwd"):
+        getattr(lib, name).restype = I
     for name in ("bnn_pack_signs", "bnn_gemm_u64", "bnn_gemm_u64_scaled", "bnn_gemm_sign_repack",
                  "bnn_gemm_ex", "bnn_gemv_act", "bnn_gemm_sign_repack_thr", "bnn_gemm_signw_bf16",
                  "bnn_chain3", "bnn_layernorm_fwd", "bnn_layernorm_bwd", "bnn_quant_f8",
@@ -592,3 +609,288 @@ def gemm_signw_grouped(x, wp, offsets, K=None, alpha=None, rows=None, row_scale=
                                           int(algo), _stream(x))
     _check(st, "bnn_gemm_signw_grouped")
     return out
+
+
+def _call(name: str, t: torch.Tensor, *args) -> None:
+    """One C call on the current stream of t's device, with that device current."""
+    fn = getattr(library(), name)
+    if torch.cuda.current_device() == t.device.index:
+        st = fn(*args, _stream(t))
+    else:
+        with torch.cuda.device(t.device):
+            st = fn(*args, _stream(t))
+    _check(st, name)
+
+
+def _matrix(name: str, t, shape, dtype, device) -> None:
+    _need_cuda(name, t)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _workspace(need: int, device):
+    return torch.empty((need,), dtype=torch.uint8, device=device) if need > 0 else None
+
+
+class Routing(NamedTuple):
+    """What route_fwd makes of T tokens' logits (bnn_route_fwd)."""
+    experts: torch.Tensor  # int32 (T, k): the choices, largest logit first; -1 without an expert
+    weights: torch.Tensor  # float32 (T, k)
+    place: torch.Tensor    # int32 (T, k): each choice's row in the experts' order; -2 - row without an expert
+    rows: torch.Tensor     # int32 (T k,): each row's token; -1 behind the last group
+    offsets: torch.Tensor  # int32 (E + 1,): each expert's range of rows
+    counts: torch.Tensor   # int32 (E,)
+    stats: torch.Tensor    # float32 (T, 2): the row's maximum, 1 / sum exp(z - maximum)
+    slope: torch.Tensor | None  # float32 (E,): derivative of the loss by a token's probability
+    loss: torch.Tensor | None   # float32 (1,): the balance loss
+
+
+def route_fwd(logits, k, valid=None, normalise=True, loss=True) -> Routing:
+    """Top-``k`` router of a mixture of experts (bnn_route_fwd): choices,
+    weights, rows in the experts' order (``rows`` and ``offsets`` are what
+    gemm_signw_grouped takes, ``place`` and ``weights`` what combine_fwd takes),
+    counts and, with ``loss``, the balance loss.  ``logits``: 2-D fp32 or bf16
+    CUDA tensor (T, E), rows may be strided, E <= 1024; -inf switches an expert
+    off for a token.  ``valid``: None or a contiguous bool or uint8 tensor (T,);
+    a token that is not valid is not routed.  ``normalise``: the weights of a
+    token's choices add up to 1."""
+    dt, T, E, ldz = _real_rows("logits", logits)
+    dev = logits.device
+    k = int(k)
+    if valid is not None:
+        _need_cuda("valid", valid)
+        if (valid.dtype not in (torch.bool, torch.uint8) or tuple(valid.shape) != (T,)
+                or not valid.is_contiguous() or valid.device != dev):
+            raise ValueError(f"valid must be a contiguous bool or uint8 tensor of shape ({T},) on {dev}")
+    if not (1 <= k <= E <= 1024 and k <= 32):
+        raise BnnError(2, "bnn_route_fwd")
+    experts, place = torch.empty((2, T, k), dtype=torch.int32, device=dev).unbind(0)
+    rows, offsets, counts = torch.empty((T * k + 2 * E + 1,), dtype=torch.int32, device=dev).split((T * k, E + 1, E))
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    stats = torch.empty((T, 2), dtype=torch.float32, device=dev)
+    slope = total = None
+    if loss:
+        slope, total = torch.empty((E + 1,), dtype=torch.float32, device=dev).split((E, 1))
+    need = library().bnn_route_fwd_workspace(T, E, k)
+    ws = _workspace(need, dev)
+    _call("bnn_route_fwd", logits, _ptr(logits), dt, ldz, _ptr(valid), _ptr(experts), _ptr(weights), _ptr(place),
+          _ptr(rows), _ptr(offsets), _ptr(counts), _ptr(stats), _ptr(slope), _ptr(total), _ptr(ws), need, T, E, k,
+          int(bool(normalise)))
+    return Routing(experts, weights, place, rows, offsets, counts, stats, slope, total)
+
+
+def route_bwd(logits, experts, weights, stats, slope=None, dweights=None, dloss=None, normalise=True):
+    """Gradient of route_fwd by its logits (their shape and type)
+    (bnn_route_bwd), from its ``experts``, ``weights``, ``stats`` and ``slope``:
+    ``dweights`` (T, k) is the weights' gradient or None, ``dloss`` (a float32
+    tensor of one element) the balance loss's or None.  Every tensor but the
+    logits is contiguous; ``normalise`` as in the forward pass."""
+    dt, T, E, ldz = _real_rows("logits", logits)
+    dev = logits.device
+    _need_cuda("experts", experts)
+    k = experts.shape[1] if experts.dim() == 2 else -1
+    _matrix("experts", experts, (T, k), torch.int32, dev)
+    _matrix("weights", weights, (T, k), torch.float32, dev)
+    _matrix("stats", stats, (T, 2), torch.float32, dev)
+    if dweights is not None:
+        _matrix("dweights", dweights, (T, k), torch.float32, dev)
+    if dloss is not None:
+        _vector("slope", slope, E, dev)
+        _need_cuda("dloss", dloss)
+        if dloss.dtype != torch.float32 or dloss.numel() != 1 or dloss.device != dev:
+            raise ValueError(f"dloss must be a float32 tensor of one element on {dev}")
+    dz = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    _call("bnn_route_bwd", logits, _ptr(logits), dt, ldz, _ptr(experts), _ptr(weights), _ptr(stats),
+          None if dloss is None else _ptr(slope), _ptr(dweights), _ptr(dloss), _ptr(dz), max(E, 1), T, E, k,
+          int(bool(normalise)))
+    return dz
+
+
+def combine_fwd(y, place, weights=None, residual=None, dtype=None, out=None):
+    """``out[t] = residual[t] + sum_j weights[t, j] * y[place[t, j]]``, the sum of
+    the experts' outputs at each token (bnn_combine_fwd).  ``y``: 2-D fp32 or
+    bf16 CUDA tensor (R, N), rows may be strided; ``place``: contiguous int32
+    (T, k) as route_fwd makes it (negative: no expert); ``weights`` None (1)
+    or contiguous float32 (T, k); ``residual`` None or (T, N) of the output's
+    type.  ``dtype`` of the output: float32 or bfloat16, the residual's or y's
+    by default; ``out`` may be the residual itself."""
+    dty, R, N, ldy = _real_rows("y", y)
+    dev = y.device
+    _need_cuda("place", place)
+    if place.dim() != 2:
+        raise ValueError("place must be 2-D")
+    T, k = place.shape
+    _matrix("place", place, (T, k), torch.int32, dev)
+    if weights is not None:
+        _matrix("weights", weights, (T, k), torch.float32, dev)
+    if dtype is None:
+        dtype = out.dtype if out is not None else residual.dtype if residual is not None else y.dtype
+    out, dt, ldo = _rows_out("out", out, T, N, dtype, dev)
+    ldr = 0
+    if residual is not None:
+        ldr = _same_rows("residual", residual, T, N, dt, dev)
+    _call("bnn_combine_fwd", y, _ptr(y), dty, ldy, R, _ptr(place), _ptr(weights), _ptr(residual), ldr, _ptr(out), dt,
+          ldo, T, N, k)
+    return out
+
+
+def combine_bwd(dout, place, weights=None, y=None, rows=None, dtype=None):
+    """Gradient of combine_fwd: ``(dy, dweights)`` (bnn_combine_bwd).  ``dout``:
+    2-D fp32 or bf16 CUDA tensor (T, N).  ``y`` is what the forward pass summed,
+    or its block-scaled 8-bit form ``(q, s)`` (quant_f8); without it only ``dy``
+    is computed (None for dweights) and ``rows`` says how many rows that has.
+    ``dy`` has the type ``dtype``: y's by default, dout's where y is in 8 bits
+    or missing.  Every row of dy is written if ``place`` names each row once,
+    as route_fwd's does (rows without an expert: zeros); others are left
+    undefined.  The residual's gradient is dout itself."""
+    dt, T, N, lddo = _real_rows("dout", dout)
+    dev = dout.device
+    _need_cuda("place", place)
+    k = place.shape[1] if place.dim() == 2 else -1
+    _matrix("place", place, (T, k), torch.int32, dev)
+    if weights is not None:
+        _matrix("weights", weights, (T, k), torch.float32, dev)
+    data = ys = None
+    dty, ldy = BNN_BF16, N
+    if y is None:
+        R = T * k if rows is None else int(rows)
+    elif isinstance(y, (tuple, list)):
+        data, ys = y
+        R = _quantised("y", data, ys, N)
+        dty = BNN_F8
+    else:
+        data = y
+        dty, R, Ny, ldy = _real_rows("y", y)
+        if Ny != N:
+            raise ValueError(f"y has {Ny} columns, dout {N}")
+        dtype = y.dtype if dtype is None else dtype
+    if data is not None and data.device != dev:
+        raise ValueError(f"y must be on {dev}")
+    dy, dtd = _real_out(R, N, dout.dtype if dtype is None else dtype, dev, None)
+    dw = None if y is None else torch.empty((T, k), dtype=torch.float32, device=dev)
+    _call("bnn_combine_bwd", dout, _ptr(dout), dt, lddo, _ptr(data), _ptr(ys), dty, ldy, R, _ptr(place), _ptr(weights),
+          _ptr(dy), dtd, max(N, 1), _ptr(dw), T, N, k)
+    return dy, dw
+
+
+def _rows_out(name: str, out, M: int, N: int, dtype, device):
+    """(tensor, dtype code, row stride) of an output whose rows may be strided."""
+    if out is None:
+        out, dt = _real_out(M, N, dtype, device, None)
+        return out, dt, max(N, 1)
+    dt, Mo, No, ld = _real_rows(name, out)
+    if (Mo, No) != (M, N) or out.dtype != dtype or out.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape ({M}, {N}) on {device}")
+    return out, dt, ld
+
+
+def _same_rows(name: str, t, M: int, N: int, dt: int, device) -> int:
+    """Row stride of an input of the output's shape and type."""
+    d, Mt, Nt, ld = _real_rows(name, t)
+    if (d, Mt, Nt) != (dt, M, N) or t.device != device:
+        raise ValueError(f"{name} must have the output's shape ({M}, {N}), type and device")
+    return ld
+
+
+def _factors(ids, a, b, scale, T: int, K: int, N: int, device):
+    """(adapters, rank) of checked adapter factors."""
+    _vector("ids", ids, T, device, torch.int32)
+    _need_cuda("a", a)
+    if a.dim() != 3:
+        raise ValueError("a must be 3-D: (adapters, rank, K)")
+    L, r = a.shape[0], a.shape[1]
+    _matrix("a", a, (L, r, K), torch.bfloat16, device)
+    _matrix("b", b, (L, r, N), torch.bfloat16, device)
+    if scale is not None:
+        _vector("scale", scale, L, device)
+    return L, r
+
+
+def adapter_fwd(x, ids, a, b, scale=None, base=None, dtype=None, out=None):
+    """Low-rank adapters of many requests beside a shared projection
+    (bnn_adapter_fwd): ``(out, u)`` with ``u[t] = a[ids[t]] @ x[t]`` (float32
+    (T, r)) and ``out[t] = base[t] + scale[ids[t]] * (u[t] @ b[ids[t]])``.  ``x``:
+    2-D bf16 CUDA tensor (T, K), rows may be strided; ``ids``: contiguous int32
+    (T,), an id outside [0, L) has no adapter; ``a`` and ``b``: contiguous
+    bfloat16 (L, r, K) and (L, r, N), r <= 128; ``scale`` None (1) or contiguous
+    float32 (L,); ``base`` None (0) or (T, N), the projection's output, of type
+    ``dtype`` (float32 or bfloat16; the base's by default, else float32).
+    ``out`` may be the base itself: rows without an adapter stay as they are."""
+    dtx, T, K, ldx = _real_rows("x", x)
+    if dtx != BNN_BF16:
+        raise TypeError("x must be bfloat16")
+    dev = x.device
+    _need_cuda("b", b)
+    N = b.shape[2] if b.dim() == 3 else -1
+    L, r = _factors(ids, a, b, scale, T, K, N, dev)
+    if dtype is None:
+        dtype = out.dtype if out is not None else base.dtype if base is not None else torch.float32
+    out, dt, ldo = _rows_out("out", out, T, N, dtype, dev)
+    ldb = _same_rows("base", base, T, N, dt, dev) if base is not None else 0
+    u = torch.empty((T, r), dtype=torch.float32, device=dev)
+    need = library().bnn_adapter_fwd_workspace(T, K, r)
+    ws = _workspace(need, dev)
+    _call("bnn_adapter_fwd", x, _ptr(x), ldx, _ptr(ids), _ptr(a), _ptr(b), _ptr(scale), _ptr(base), ldb, _ptr(out),
+          ldo, dt, _ptr(u), _ptr(ws), need, T, K, N, r, L)
+    return out, u
+
+
+def adapter_bwd(dy, x, u, ids, a, b, scale=None, base=None, dtype=None, dx=True, params=True):
+    """Gradient of adapter_fwd: ``(dx, da, db)`` (bnn_adapter_bwd) from the
+    output's gradient ``dy`` (2-D bf16 CUDA tensor (T, N)), the forward pass's
+    ``x`` (bf16, or its block-scaled 8-bit form ``(q, s)``, quant_f8) and ``u``:
+    with ``v[t] = b[ids[t]] @ dy[t]``
+    ``dx[t] = base[t] + scale * (v[t] @ a[ids[t]])``,
+    ``da[l] = scale[l] * sum_t outer(v[t], x[t])`` and
+    ``db[l] = scale[l] * sum_t outer(u[t], dy[t])`` over l's rows (float32).
+    ``base`` None (0) or (T, K): the gradient that reaches x by the shared
+    projection, of type ``dtype`` (the base's by default, else float32).
+    ``dx=False`` and ``params=False`` leave those out (None).  With ``params``
+    at most 1024 adapters."""
+    dtd, T, N, lddy = _real_rows("dy", dy)
+    if dtd != BNN_BF16:
+        raise TypeError("dy must be bfloat16")
+    dev = dy.device
+    _need_cuda("a", a)
+    K = a.shape[2] if a.dim() == 3 else -1
+    L, r = _factors(ids, a, b, scale, T, K, N, dev)
+    data = xs = None
+    dtx, ldx = BNN_BF16, max(K, 1)
+    if params:
+        _matrix("u", u, (T, r), torch.float32, dev)
+        if isinstance(x, (tuple, list)):
+            data, xs = x
+            if _quantised("x", data, xs, K) != T:
+                raise ValueError(f"x must have {T} rows")
+            dtx = BNN_F8
+        else:
+            data = x
+            dtx, Tx, Kx, ldx = _real_rows("x", x)
+            if dtx != BNN_BF16:
+                raise TypeError("x must be bfloat16")
+            if (Tx, Kx) != (T, K):
+                raise ValueError(f"x must have shape ({T}, {K})")
+        if data.device != dev:
+            raise ValueError(f"x must be on {dev}")
+    out, dt, ldo, ldb = None, BNN_FP32, max(K, 1), 0
+    if dx:
+        if dtype is None:
+            dtype = base.dtype if base is not None else torch.float32
+        out, dt, ldo = _rows_out("dx", None, T, K, dtype, dev)
+        if base is not None:
+            ldb = _same_rows("base", base, T, K, dt, dev)
+    else:
+        base = None
+    da = db = None
+    need = 0
+    ws = None
+    if dx or params:
+        need = library().bnn_adapter_bwd_workspace(T, K, N, r, L)
+        ws = _workspace(need, dev)
+    if params:
+        da = torch.empty((L, r, K), dtype=torch.float32, device=dev)
+        db = torch.empty((L, r, N), dtype=torch.float32, device=dev)
+    _call("bnn_adapter_bwd", dy, _ptr(dy), lddy, _ptr(data), _ptr(xs), dtx, ldx, _ptr(u) if params else None,
+          _ptr(ids), _ptr(a), _ptr(b), _ptr(scale), _ptr(base), ldb, _ptr(out), ldo, dt, _ptr(da), _ptr(db), _ptr(ws),
+          need, T, K, N, r, L)
+    return out, da, db

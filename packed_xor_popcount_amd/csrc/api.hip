@@ -5,6 +5,7 @@
 #include "../../include/bnn.h"
 #include "bnn_internal.h"
 #include "f8.h"
+#include "operators.h"
 
 #include <float.h>
 
@@ -74,6 +75,20 @@ bnn_status run_gemm_f8(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, 
   if (M == 0 || N == 0) return BNN_OK;
   return launch_status(bnn::launch_gemm_f8(xq, xs, wq, ws, y, dtype, fast, M, N, K,
                                            static_cast<hipStream_t>(stream)));
+}
+
+// Sizes of the router, of the sum behind the experts and of the adapters.
+bool route_sizes_ok(int64_t T, int64_t E, int64_t k) {
+  return T >= 0 && T < kMaxDim && E >= 1 && E <= bnn::kRouteMaxExperts && k >= 1 && k <= E &&
+         k <= bnn::kRouteMaxK && T * k < kMaxDim;
+}
+bool combine_sizes_ok(int64_t R, int64_t T, int64_t N, int64_t k) {
+  return R >= 0 && R < kMaxDim && T >= 0 && T < kMaxDim && N >= 0 && N < kMaxDim && k >= 1 &&
+         k < kMaxDim && T * k < kMaxDim;
+}
+bool adapter_sizes_ok(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t L) {
+  return T >= 0 && T < bnn::kAdapterMaxRows && K >= 0 && K < kMaxDim && N >= 0 && N < kMaxDim &&
+         rank >= 1 && rank <= bnn::kAdapterMaxRank && L >= 0 && L < kMaxGroups;
 }
 
 }  // namespace
@@ -287,6 +302,189 @@ bnn_status bnn_gemm_signw_grouped(const void *x, int64_t ldx, int64_t xrows, con
   return launch_status(bnn::launch_signw_grouped(static_cast<const uint16_t *>(x), ldx, xrows, rows,
                                                  offsets, wp, alpha, row_scale, y, dtype, R, E, N,
                                                  K, algo, static_cast<hipStream_t>(stream)));
+}
+
+int64_t bnn_route_fwd_workspace(int64_t T, int64_t E, int64_t k) {
+  if (T <= 0 || T >= kMaxDim || E <= 0 || E > bnn::kRouteMaxExperts || k <= 0) return 0;
+  return bnn::route_fwd_workspace(T, E, k);
+}
+
+bnn_status bnn_route_fwd(const void *z, int dtype, int64_t ldz, const uint8_t *valid,
+                         int32_t *experts, float *weights, int32_t *place, int32_t *rows,
+                         int32_t *offsets, int32_t *counts, float *stats, float *slope,
+                         float *loss, void *workspace, int64_t ws_bytes, int64_t T, int64_t E,
+                         int64_t k, int normalise, void *stream) {
+  if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
+  if (normalise != 0 && normalise != 1) return BNN_E_ARG;
+  if (!route_sizes_ok(T, E, k) || ldz < E || ldz >= kMaxDim) return BNN_E_SHAPE;
+  if (T > 0 && (!z || !experts || !weights || !place || !rows || !stats)) return BNN_E_NULL;
+  if (!offsets || !counts || !slope != !loss) return BNN_E_NULL;
+  const int64_t need = bnn_route_fwd_workspace(T, E, k);
+  if (need > 0 && !workspace) return BNN_E_NULL;
+  if (ws_bytes < need) return BNN_E_SHAPE;
+  if (misaligned(z, dtype == BNN_FP32 ? 4 : 2) || misaligned(experts, 4) ||
+      misaligned(weights, 4) || misaligned(place, 4) || misaligned(rows, 4) ||
+      misaligned(offsets, 4) || misaligned(counts, 4) || misaligned(stats, 4) ||
+      misaligned(slope, 4) || misaligned(loss, 4) || misaligned(workspace, 16))
+    return BNN_E_ALIGN;
+  const bnn::RouteOut out = {experts, weights, place, rows, offsets, counts, stats, slope, loss};
+  return launch_status(bnn::launch_route_fwd(z, dtype, ldz, valid, out, workspace, T, (int)E,
+                                             (int)k, normalise != 0,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+bnn_status bnn_route_bwd(const void *z, int dtype, int64_t ldz, const int32_t *experts,
+                         const float *weights, const float *stats, const float *slope,
+                         const float *dweights, const float *dloss, void *dz, int64_t lddz,
+                         int64_t T, int64_t E, int64_t k, int normalise, void *stream) {
+  if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
+  if (normalise != 0 && normalise != 1) return BNN_E_ARG;
+  if (!route_sizes_ok(T, E, k) || ldz < E || ldz >= kMaxDim || lddz < E || lddz >= kMaxDim)
+    return BNN_E_SHAPE;
+  if (T > 0 && (!z || !stats || !dz || (dweights && (!experts || !weights)))) return BNN_E_NULL;
+  if (!slope != !dloss) return BNN_E_NULL;
+  const uintptr_t es = dtype == BNN_FP32 ? 4 : 2;
+  if (misaligned(z, es) || misaligned(dz, es) || misaligned(experts, 4) ||
+      misaligned(weights, 4) || misaligned(stats, 4) || misaligned(slope, 4) ||
+      misaligned(dweights, 4) || misaligned(dloss, 4))
+    return BNN_E_ALIGN;
+  if (T == 0) return BNN_OK;
+  return launch_status(bnn::launch_route_bwd(z, dtype, ldz, experts, weights, stats, slope,
+                                             dweights, dloss, dz, lddz, T, (int)E, (int)k,
+                                             normalise != 0, static_cast<hipStream_t>(stream)));
+}
+
+bnn_status bnn_combine_fwd(const void *y, int ydtype, int64_t ldy, int64_t R,
+                           const int32_t *place, const float *weights, const void *residual,
+                           int64_t ldr, void *out, int dtype, int64_t ldo, int64_t T, int64_t N,
+                           int64_t k, void *stream) {
+  if ((dtype != BNN_FP32 && dtype != BNN_BF16) || (ydtype != BNN_FP32 && ydtype != BNN_BF16))
+    return BNN_E_DTYPE;
+  if (!combine_sizes_ok(R, T, N, k) || ldy < N || ldy >= kMaxDim || ldo < N || ldo >= kMaxDim ||
+      (residual && (ldr < N || ldr >= kMaxDim)))
+    return BNN_E_SHAPE;
+  if (T > 0 && N > 0 && (!place || !out || (R > 0 && !y))) return BNN_E_NULL;
+  const uintptr_t es = dtype == BNN_FP32 ? 4 : 2;
+  if (misaligned(y, ydtype == BNN_FP32 ? 4 : 2) || misaligned(out, es) ||
+      misaligned(residual, es) || misaligned(place, 4) || misaligned(weights, 4))
+    return BNN_E_ALIGN;
+  if (T == 0 || N == 0) return BNN_OK;
+  return launch_status(bnn::launch_combine_fwd(y, ydtype, ldy, R, place, weights, residual, ldr,
+                                               out, dtype, ldo, T, N, (int)k,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+bnn_status bnn_combine_bwd(const void *dout, int dtype, int64_t lddo, const void *y,
+                           const uint8_t *ys, int ydtype, int64_t ldy, int64_t R,
+                           const int32_t *place, const float *weights, void *dy, int dydtype,
+                           int64_t lddy, float *dweights, int64_t T, int64_t N, int64_t k,
+                           void *stream) {
+  if ((dtype != BNN_FP32 && dtype != BNN_BF16) || (dydtype != BNN_FP32 && dydtype != BNN_BF16) ||
+      (ydtype != BNN_FP32 && ydtype != BNN_BF16 && ydtype != BNN_F8))
+    return BNN_E_DTYPE;
+  if (!combine_sizes_ok(R, T, N, k) || lddo < N || lddo >= kMaxDim ||
+      (dy && (lddy < N || lddy >= kMaxDim)) ||
+      (y && ydtype != BNN_F8 && (ldy < N || ldy >= kMaxDim)))
+    return BNN_E_SHAPE;
+  if (T > 0 && !place) return BNN_E_NULL;
+  if (T > 0 && N > 0 && !dout) return BNN_E_NULL;
+  if (dweights && R > 0 && N > 0 && (!y || (ydtype == BNN_F8 && !ys))) return BNN_E_NULL;
+  if (misaligned(dout, dtype == BNN_FP32 ? 4 : 2) || misaligned(dy, dydtype == BNN_FP32 ? 4 : 2) ||
+      misaligned(y, ydtype == BNN_F8 ? 16 : ydtype == BNN_FP32 ? 4 : 2) || misaligned(ys, 4) ||
+      misaligned(place, 4) || misaligned(weights, 4) || misaligned(dweights, 4))
+    return BNN_E_ALIGN;
+  if (T == 0 || (!dy && !dweights) || (N == 0 && !dweights)) return BNN_OK;
+  return launch_status(bnn::launch_combine_bwd(dout, dtype, lddo, y, ys, ydtype, ldy, R, place,
+                                               weights, dy, dydtype, lddy, dweights, T, N, (int)k,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int64_t bnn_adapter_fwd_workspace(int64_t T, int64_t K, int64_t rank) {
+  if (!adapter_sizes_ok(T, K, 0, rank, 0) || T == 0) return 0;
+  return bnn::adapter_fwd_workspace(T, K, rank);
+}
+
+bnn_status bnn_adapter_fwd(const void *x, int64_t ldx, const int32_t *ids, const void *a,
+                           const void *b, const float *scale, const void *base, int64_t ldb,
+                           void *out, int64_t ldo, int dtype, float *u, void *workspace,
+                           int64_t ws_bytes, int64_t T, int64_t K, int64_t N, int64_t rank,
+                           int64_t L, void *stream) {
+  if (dtype != BNN_FP32 && dtype != BNN_BF16) return BNN_E_DTYPE;
+  if (!adapter_sizes_ok(T, K, N, rank, L) || ldx < K || ldx >= kMaxDim || ldo < N ||
+      ldo >= kMaxDim || (base && (ldb < N || ldb >= kMaxDim)) || (base == out && base && ldb != ldo))
+    return BNN_E_SHAPE;
+  if (T > 0 && (!ids || !u || (K > 0 && !x) || (N > 0 && !out))) return BNN_E_NULL;
+  if (T > 0 && L > 0 && ((K > 0 && !a) || (N > 0 && !b))) return BNN_E_NULL;
+  const int64_t need = bnn_adapter_fwd_workspace(T, K, rank);
+  if (need > 0 && !workspace) return BNN_E_NULL;
+  if (ws_bytes < need) return BNN_E_SHAPE;
+  const uintptr_t es = dtype == BNN_FP32 ? 4 : 2;
+  if (misaligned(x, 2) || misaligned(a, 2) || misaligned(b, 2) || misaligned(ids, 4) ||
+      misaligned(scale, 4) || misaligned(base, es) || misaligned(out, es) || misaligned(u, 4) ||
+      misaligned(workspace, 16))
+    return BNN_E_ALIGN;
+  if (T == 0) return BNN_OK;
+  return launch_status(bnn::launch_adapter_fwd(
+      static_cast<const uint16_t *>(x), ldx, ids, static_cast<const uint16_t *>(a),
+      static_cast<const uint16_t *>(b), scale, base, ldb, out, ldo, dtype, u, workspace, T, K, N,
+      (int)rank, (int)L, static_cast<hipStream_t>(stream)));
+}
+
+int64_t bnn_adapter_bwd_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t L) {
+  if (!adapter_sizes_ok(T, K, N, rank, L) || L > bnn::kRouteMaxExperts) return 0;
+  return bnn::adapter_bwd_workspace(T, K, N, rank, L);
+}
+
+bnn_status bnn_adapter_bwd(const void *dy, int64_t lddy, const void *x, const uint8_t *xs,
+                           int xdtype, int64_t ldx, const float *u, const int32_t *ids,
+                           const void *a, const void *b, const float *scale, const void *base,
+                           int64_t ldb, void *dx, int64_t lddx, int dtype, float *da, float *db,
+                           void *workspace, int64_t ws_bytes, int64_t T, int64_t K, int64_t N,
+                           int64_t rank, int64_t L, void *stream) {
+  if ((dtype != BNN_FP32 && dtype != BNN_BF16) || (xdtype != BNN_BF16 && xdtype != BNN_F8))
+    return BNN_E_DTYPE;
+  if (!adapter_sizes_ok(T, K, N, rank, L) || L > bnn::kRouteMaxExperts || lddy < N ||
+      lddy >= kMaxDim || ((da || db) && xdtype == BNN_BF16 && (ldx < K || ldx >= kMaxDim)) ||
+      (dx && (lddx < K || lddx >= kMaxDim)) || (dx && base && (ldb < K || ldb >= kMaxDim)) ||
+      (dx && base == dx && ldb != lddx))
+    return BNN_E_SHAPE;
+  const bool params = da || db;
+  if (params && L > 0 && ((K > 0 && !da) || (N > 0 && !db))) return BNN_E_NULL;
+  if (T > 0 && (!ids || (N > 0 && !dy))) return BNN_E_NULL;
+  if (T > 0 && L > 0 && ((dx && K > 0 && !a) || (N > 0 && !b))) return BNN_E_NULL;
+  if (params && T > 0 && (!u || (K > 0 && (!x || (xdtype == BNN_F8 && !xs))))) return BNN_E_NULL;
+  const int64_t need = bnn_adapter_bwd_workspace(T, K, N, rank, L);
+  if (need > 0 && !workspace) return BNN_E_NULL;
+  if (ws_bytes < need) return BNN_E_SHAPE;
+  const uintptr_t es = dtype == BNN_FP32 ? 4 : 2;
+  if (misaligned(dy, 2) || misaligned(x, xdtype == BNN_F8 ? 16 : 2) || misaligned(xs, 4) ||
+      misaligned(u, 4) || misaligned(ids, 4) || misaligned(a, 2) || misaligned(b, 2) ||
+      misaligned(scale, 4) || misaligned(base, es) || misaligned(dx, es) || misaligned(da, 4) ||
+      misaligned(db, 4) || misaligned(workspace, 16))
+    return BNN_E_ALIGN;
+  if (K == 0) dx = nullptr;
+  const bool sums = params && L > 0 && K + N > 0;
+  if (!sums && (!dx || T == 0)) return BNN_OK;
+  const bnn::AdapterGrad g = {static_cast<const uint16_t *>(dy),
+                              lddy,
+                              x,
+                              xdtype == BNN_F8 ? xs : nullptr,
+                              ldx,
+                              u,
+                              ids,
+                              static_cast<const uint16_t *>(a),
+                              static_cast<const uint16_t *>(b),
+                              scale,
+                              base,
+                              ldb,
+                              dx,
+                              lddx,
+                              dtype,
+                              sums,
+                              da,
+                              db};
+  return launch_status(bnn::launch_adapter_bwd(g, workspace, T, K, N, (int)rank, (int)L,
+                                               static_cast<hipStream_t>(stream)));
 }
 
 bnn_status bnn_gemm_u64(const uint64_t *xp, const uint64_t *wp, int32_t *y, int64_t M, int64_t N,
