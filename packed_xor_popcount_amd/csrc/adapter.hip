@@ -21,6 +21,8 @@
 #include "f8.h"
 #include "operators.h"
 
+#include <type_traits>
+
 namespace bnn {
 namespace {
 
@@ -100,60 +102,102 @@ __device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&f)[8]) {
   }
 }
 
-// The adapters met among the 16 rows of a tile: lane l < 16 is told row l's id
-// (-1: none, -2: no such row); the s-th distinct one, in the order of its first
-// row.  False past the last.
-__device__ __forceinline__ uint64_t leaders_of(int id) {
-  const int lane = threadIdx.x & 63;
-  bool first = lane < 16 && id > -2;
-#pragma unroll
-  for (int i = 0; i < 15; ++i) {
-    const int other = __builtin_amdgcn_readlane(id, i);
-    first = first && !(i < lane && other == id);
-  }
-  return __ballot(first);
-}
-__device__ __forceinline__ int nth_bit(uint64_t m, int s) {  // -1 past the last
-  for (; s > 0 && m; --s) m &= m - 1;
-  return m ? __ffsll((unsigned long long)m) - 1 : -1;
-}
+// ---------------------------------------------------------------------------
+// The rows of a chunk in tiles of one adapter each.  A block puts up to kChunk
+// neighbouring rows in the order of their ids, where these change often (a rank
+// by comparison, in LDS), and cuts that order at every change and every 16th
+// place.  So rows of one adapter share its factors wherever they stand in the
+// chunk, and nothing has to be sorted or looked up by the caller.
 
-__device__ __forceinline__ int tile_id(const int32_t *ids, int64_t t0, int64_t T, int L) {
-  const int64_t t = t0 + (threadIdx.x & 15);
-  if (t >= T) return -2;
-  const int id = ids[t];
-  return id >= 0 && id < L ? id : -1;
+constexpr int kChunk = 256;
+
+struct Plan {
+  int key[kChunk];        // the row's id; L: none
+  uint16_t order[kChunk]; // rows of the chunk by tile
+  uint16_t start[kChunk + 1];
+  int waves[kChunk / 64];
+  int tiles;
+};
+
+// By at least kChunk threads, all of the block's.
+__device__ __forceinline__ void make_plan(Plan &p, const int32_t *ids, int64_t t0, int64_t T,
+                                          int L) {
+  const int i = threadIdx.x;
+  const int n = T - t0 < kChunk ? (int)(T - t0) : kChunk;
+  int key = 0x7FFFFFFF;
+  if (i < n) {
+    key = ids[t0 + i];
+    if (key < 0 || key >= L) key = L;
+  }
+  if (i < kChunk) p.key[i] = key;
+  __syncthreads();
+  const int changes = __syncthreads_count(i > 0 && i < n && key != p.key[i - 1]);
+  int at = i;
+  if (changes > 8) {
+    at = 0;
+    if (i < n) {
+      for (int j = 0; j < n; j += 4) {  // places past n hold the largest key
+        const int4 k = *reinterpret_cast<const int4 *>(p.key + j);
+        at += (k.x < key || (k.x == key && j < i)) + (k.y < key || (k.y == key && j + 1 < i)) +
+              (k.z < key || (k.z == key && j + 2 < i)) + (k.w < key || (k.w == key && j + 3 < i));
+      }
+    }
+  }
+  if (i < n) p.order[at] = (uint16_t)i;
+  __syncthreads();
+  const bool begin = i < n && ((i & 15) == 0 || p.key[p.order[i]] != p.key[p.order[i - 1]]);
+  const uint64_t all = __ballot(begin);
+  if ((i & 63) == 0 && i < kChunk) p.waves[i >> 6] = __popcll(all);
+  __syncthreads();
+  if (i < kChunk) {
+    int before = __popcll(all & ((uint64_t(1) << (i & 63)) - 1)), total = 0;
+    for (int w = 0; w < kChunk / 64; ++w) {
+      if (w < (i >> 6)) before += p.waves[w];
+      total += p.waves[w];
+    }
+    if (begin) p.start[before] = (uint16_t)i;
+    if (i == 0) {
+      p.start[total] = (uint16_t)n;
+      p.tiles = total;
+    }
+  }
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
 // shrink: part[s][t][j] = sum over split s of the columns of x_t[c] w_id,j[c].
-// A block has 16 rows; its four waves take every fourth step of 128 columns
-// (a lane: 32 neighbours, 64 bytes) of the block's split and join their sums in
-// LDS.  blockIdx.z and gridDim.z deal out the tile's adapters.
+// The eight waves of a block take every eighth step of 128 columns (a lane: 32
+// neighbours, 64 bytes) of the block's split of a tile and join their sums in
+// LDS.  blockIdx: chunk, split, share of the chunk's tiles.
+
+constexpr int kShrinkWaves = 8;
 
 template <int RT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(64 * kShrinkWaves)
     adapter_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx,
                           const int32_t *__restrict__ ids, const uint16_t *__restrict__ w,
                           float *__restrict__ part, int64_t T, int64_t C, int r, int L) {
-  __shared__ v4f join[4][RT][64];
+  constexpr int JT = RT < 4 ? RT : 4;  // rank tiles joined at a time
+  __shared__ Plan plan;
+  __shared__ v4f join[kShrinkWaves][JT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * 16;
-  const int id = tile_id(ids, t0, T, L);
-  const uint64_t leaders = leaders_of(id);
-  const int64_t t = t0 + (lane & 15);
-  const uint16_t *xr = x + (t < T ? t : T - 1) * ldx;
-  float *out = part + ((int64_t)blockIdx.y * T + t) * r;
+  const int64_t t0 = (int64_t)blockIdx.x * kChunk;
+  make_plan(plan, ids, t0, T, L);
+  const int lo = (int)((int64_t)plan.tiles * blockIdx.z / gridDim.z);
+  const int hi = (int)((int64_t)plan.tiles * (blockIdx.z + 1) / gridDim.z);
   const int64_t steps = (C + 127) / 128, whole = C / 128;
-  const int units = 4 * gridDim.y, unit = 4 * blockIdx.y + wave;
-  for (int z = blockIdx.z;; z += gridDim.z) {
-    const int lead = nth_bit(leaders, z);
-    if (lead < 0) return;
-    const int l = __builtin_amdgcn_readlane(id, lead);
+  const int units = kShrinkWaves * gridDim.y, unit = kShrinkWaves * blockIdx.y + wave;
+  for (int i = lo; i < hi; ++i) {
+    const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
+    const int l = plan.key[plan.order[s0]];
+    const bool mine = (lane & 15) < len;
+    const int64_t t = t0 + plan.order[s0 + (mine ? lane & 15 : len - 1)];
+    const uint16_t *xr = x + t * ldx;
+    float *out = part + ((int64_t)blockIdx.y * T + t) * r;
     v4f acc[RT];
 #pragma unroll
     for (int q = 0; q < RT; ++q) acc[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    if (l >= 0) {
+    if (l < L) {
       const uint16_t *wr[RT];
 #pragma unroll
       for (int q = 0; q < RT; ++q) {
@@ -161,40 +205,51 @@ __global__ void __launch_bounds__(256)
         wr[q] = w + ((int64_t)l * r + (j < r ? j : r - 1)) * C;
       }
       int64_t st = unit;
-      for (; st < whole; st += units) {
-        const int64_t c = st * 128 + 32 * g;
-        uint4 xv[4], wv[RT][4];
-        __builtin_memcpy(xv, xr + c, 64);
+      auto several = [&](auto n) {  // n steps, all their loads in flight
+        uint4 xv[n][4], wv[n][RT][4];
 #pragma unroll
-        for (int q = 0; q < RT; ++q) __builtin_memcpy(wv[q], wr[q] + c, 64);
+        for (int m = 0; m < n; ++m) {
+          const int64_t c = (st + m * units) * 128 + 32 * g;
+          __builtin_memcpy(xv[m], xr + c, 64);
 #pragma unroll
-        for (int q = 0; q < RT; ++q)
+          for (int q = 0; q < RT; ++q) __builtin_memcpy(wv[m][q], wr[q] + c, 64);
+        }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[q] = mfma(wv[q][i], xv[i], acc[q]);
-      }
+        for (int m = 0; m < n; ++m)
+#pragma unroll
+          for (int q = 0; q < RT; ++q)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[q] = mfma(wv[m][q][k], xv[m][k], acc[q]);
+        st += n * units;
+      };
+      constexpr int kSteps = RT <= 2 ? 2 : 1;
+      while (st + (kSteps - 1) * units < whole) several(std::integral_constant<int, kSteps>());
+      if (kSteps > 1 && st < whole) several(std::integral_constant<int, 1>());
       if (st < steps) {  // the last columns
         const int64_t c = st * 128 + 32 * g;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 xv = load8(xr, c + 8 * i, C);
+        for (int k = 0; k < 4; ++k) {
+          const uint4 xv = load8(xr, c + 8 * k, C);
 #pragma unroll
-          for (int q = 0; q < RT; ++q) acc[q] = mfma(load8(wr[q], c + 8 * i, C), xv, acc[q]);
+          for (int q = 0; q < RT; ++q) acc[q] = mfma(load8(wr[q], c + 8 * k, C), xv, acc[q]);
         }
       }
     }
-    __syncthreads();  // the sums of the adapter before have been read
 #pragma unroll
-    for (int q = 0; q < RT; ++q) join[wave][q][lane] = acc[q];
-    __syncthreads();
-    const bool mine = t < T && id == l;
-    for (int q = wave; q < RT; q += 4) {
-      v4f s = join[0][q][lane];
+    for (int q0 = 0; q0 < RT; q0 += JT) {
+      __syncthreads();  // the sums before have been read
 #pragma unroll
-      for (int i = 1; i < 4; ++i) s += join[i][q][lane];
+      for (int q = 0; q < JT; ++q) join[wave][q][lane] = acc[q0 + q];
+      __syncthreads();
+      if (wave < JT) {
+        v4f s = join[0][wave][lane];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int j = 16 * q + 4 * g + v;
-        if (mine && j < r) out[j] = s[v];
+        for (int k = 1; k < kShrinkWaves; ++k) s += join[k][wave][lane];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int j = 16 * (q0 + wave) + 4 * g + v;
+          if (mine && j < r) out[j] = s[v];
+        }
       }
     }
   }
@@ -204,107 +259,126 @@ __global__ void __launch_bounds__(256)
 // expand: out_t[c] = base_t[c] + s sum_j u_t[j] w_id,j[c], u_t the sum of S parts.
 // A wave has 128 columns; the operand of its adapter's factor stays in registers
 // while the adapter does not change.  A lane ends up with eight neighbouring
-// columns of four rows.
+// columns of four rows.  The next tile's u and base are on their way while a tile
+// is computed.  blockIdx: 512 columns, chunk, share of the chunk's tiles.
 
-template <typename O, int RQ>
+template <typename O, int RQ, int S>
 __global__ void __launch_bounds__(256)
-    adapter_expand_kernel(const float *__restrict__ part, int S, const int32_t *__restrict__ ids,
+    adapter_expand_kernel(const float *__restrict__ part, const int32_t *__restrict__ ids,
                           const uint16_t *__restrict__ w, const float *__restrict__ scale,
                           const O *base, int64_t ldb, O *out, int64_t ldo, float *__restrict__ u,
-                          int64_t T, int64_t C, int r, int L, int tiles) {
+                          int64_t T, int64_t C, int r, int L) {
+  __shared__ Plan plan;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+  const int64_t t0 = (int64_t)blockIdx.y * kChunk;
+  make_plan(plan, ids, t0, T, L);
+  const int lo = (int)((int64_t)plan.tiles * blockIdx.z / gridDim.z);
+  const int hi = (int)((int64_t)plan.tiles * (blockIdx.z + 1) / gridDim.z);
   const int64_t c0 = ((int64_t)blockIdx.x * 4 + wave) * 128;
-  const bool store_u = u && c0 == 0;
-  if (c0 >= C) return;
+  if (c0 >= C || lo >= hi) return;
   const int64_t c = c0 + 8 * (lane & 15);
-  int now = -1;  // the adapter whose factor is in f
-  uint4 f[RQ][8];
+
+  struct Fetch {
+    int len, l;
+    int64_t tu;  // of row lane % 16
+    float u[RQ][8][S];
+    Chunk<O> b[4];
+  };
+  auto row_of = [&](int s0, int len, int i) {
+    return t0 + plan.order[s0 + (i < len ? i : len - 1)];
+  };
+  auto fetch = [&](int i, Fetch &f) {
+    const int s0 = plan.start[i];
+    f.len = plan.start[i + 1] - s0;
+    f.l = plan.key[plan.order[s0]];
+    f.tu = row_of(s0, f.len, lane & 15);
+#pragma unroll
+    for (int q = 0; q < RQ; ++q)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = 32 * q + 8 * g + k;
+#pragma unroll
+        for (int p = 0; p < S; ++p)
+          f.u[q][k][p] = part[((int64_t)p * T + f.tu) * r + (j < r ? j : r - 1)];
+      }
+    if (base) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        f.b[v] = load_chunk(base + row_of(s0, f.len, 4 * g + v) * ldb, (int)c, (int)C);
+    }
+  };
+
+  int now = -1;  // the adapter whose factor is in wf
+  uint4 wf[RQ][8];
   float s = 0.0f;
-  for (int i = 0; i < tiles; ++i) {
-    const int64_t t0 = ((int64_t)blockIdx.y * tiles + i) * 16;
-    if (t0 >= T) return;
-    const int id = tile_id(ids, t0, T, L);
-    const uint64_t leaders = leaders_of(id);
-    const int64_t tu = t0 + (lane & 15);
-    for (int z = blockIdx.z;; z += gridDim.z) {
-      const int lead = nth_bit(leaders, z);
-      if (lead < 0) break;
-      const int l = __builtin_amdgcn_readlane(id, lead);
-      if (l < 0) {  // rows without an adapter
-        if (store_u && id == -1)
-          for (int j = g; j < r; j += 4) u[tu * r + j] = 0.0f;
-        if (base == out) continue;  // in place (the strides are the same then)
+  Fetch cur, next;
+  fetch(lo, cur);
+  for (int i = lo; i < hi; ++i) {
+    const int s0 = plan.start[i], len = cur.len;
+    const bool has = cur.l < L;
+    if (has && cur.l != now) {
+      now = cur.l;
+      s = scale ? scale[now] : 1.0f;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int64_t t = t0 + 4 * g + v;
-          if (__shfl(id, 4 * g + v, 64) != -1) continue;
-          float val[8];
+      for (int q = 0; q < RQ; ++q) {
+        uint4 rows[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) val[j] = 0.0f;
-          if (base) {
-            const Chunk<O> b = load_chunk(base + t * ldb, (int)c, (int)C);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) val[j] = chunk_value(b, j);
-          }
-          store_chunk(out + t * ldo, (int)c, (int)C, val);
+        for (int k = 0; k < 8; ++k) {
+          const int j = 32 * q + 8 * g + k;
+          rows[k] = load8(w + ((int64_t)now * r + (j < r ? j : r - 1)) * C, c, C);
         }
-        continue;
-      }
-      if (l != now) {
-        now = l;
-        s = scale ? scale[l] : 1.0f;
+        if (32 * q + 32 > r) {
 #pragma unroll
-        for (int q = 0; q < RQ; ++q) {
-          uint4 rows[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int j = 32 * q + 8 * g + k;
-            rows[k] = make_uint4(0, 0, 0, 0);
-            if (j < r) rows[k] = load8(w + ((int64_t)l * r + j) * C, c, C);
-          }
-          transpose8(rows, f[q]);
+          for (int k = 0; k < 8; ++k)
+            if (32 * q + 8 * g + k >= r) rows[k] = make_uint4(0, 0, 0, 0);
         }
+        transpose8(rows, wf[q]);
       }
-      bool on[4];
-      Chunk<O> b[4];
+    }
+    fetch(i + 1 < hi ? i + 1 : i, next);
+    __builtin_amdgcn_sched_barrier(0);
+    v4f acc[8];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        on[v] = __shfl(id, 4 * g + v, 64) == l;
-        if (base && on[v]) b[v] = load_chunk(base + (t0 + 4 * g + v) * ldb, (int)c, (int)C);
-      }
-      v4f acc[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      const bool mine = id == l;  // of row lane % 16
+    for (int j = 0; j < 8; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const bool mine = (lane & 15) < len;
+    if (has || (u && c0 == 0)) {
 #pragma unroll
       for (int q = 0; q < RQ; ++q) {
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int j = 32 * q + 8 * g + k;
-          v[k] = 0.0f;
-          if (mine && j < r) {
-            for (int p = 0; p < S; ++p) v[k] += part[((int64_t)p * T + tu) * r + j];
-            if (store_u) u[tu * r + j] = v[k];
-          }
+          v[k] = cur.u[q][k][0];
+#pragma unroll
+          for (int p = 1; p < S; ++p) v[k] += cur.u[q][k][p];
+          if (!(mine && j < r && has)) v[k] = 0.0f;
+          if (S > 1 && u && c0 == 0 && mine && j < r) u[cur.tu * r + j] = v[k];
           v[k] *= s;
         }
-        uint4 o[3];
-        split8(v, o);
+        if (has) {
+          uint4 o[3];
+          split8(v, o);
 #pragma unroll
-        for (int p = 2; p >= 0; --p)
+          for (int p = 2; p >= 0; --p)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] = mfma(o[p], f[q][j], acc[j]);
-      }
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (!on[v]) continue;
-        float val[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) val[j] = base ? chunk_value(b[v], j) + acc[j][v] : acc[j][v];
-        store_chunk(out + (t0 + 4 * g + v) * ldo, (int)c, (int)C, val);
+            for (int j = 0; j < 8; ++j) acc[j] = mfma(o[p], wf[q][j], acc[j]);
+        }
       }
     }
+    if (has || base != out) {  // in place, rows without an adapter stay as they are
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (4 * g + v >= len) continue;
+        float val[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          val[j] = acc[j][v];
+          if (base) val[j] = has ? chunk_value(cur.b[v], j) + val[j] : chunk_value(cur.b[v], j);
+        }
+        store_chunk(out + row_of(s0, len, 4 * g + v) * ldo, (int)c, (int)C, val);
+      }
+    }
+    cur = next;
   }
 }
 
@@ -380,56 +454,104 @@ __device__ __forceinline__ bf16x2 widen2(uint32_t v, float scale, bool high) {
 // two goes to w, so that no value leaves bf16's range on either side.
 __device__ __forceinline__ int held_scale(int s) { return s < 27 ? 27 : s > 245 ? 245 : s; }
 
+// Rows, values of y and of w for 32 rows of a tile, as they are in memory.
+template <int RT, bool F8>
+struct Step {
+  uint4 y[8];  // 8 bits: x, y the bytes, z the scale byte
+  float w[RT][8];
+};
+
 template <int RT, bool F8>
 __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, const Tile &tile,
                                            float s, int64_t c0, int j0, int r, float *out) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int64_t c = c0 + 8 * (lane & 15), C = sd.C;
+  const int last = rows[tile.r1 - 1];
+  struct Rows {
+    int t[8];
+  };
+  // the buffer behind rows allows reading past the tile's end
+  auto rows_of = [&](int i0) {
+    Rows q;
+    __builtin_memcpy(q.t, rows + i0 + 8 * g, 32);
+    return q;
+  };
+  auto fetch = [&](int i0, const Rows &q, Step<RT, F8> &st) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t t = i0 + 8 * g + k < tile.r1 ? q.t[k] : last;
+      if (F8) {
+        uint2 v;
+        const int64_t at = c < C ? c : 0;  // columns past C are not stored
+        __builtin_memcpy(&v, static_cast<const uint8_t *>(sd.y) + t * f8_row_bytes(C) + at, 8);
+        st.y[k].x = v.x;
+        st.y[k].y = v.y;
+        st.y[k].z = sd.ys[t * f8_scale_bytes(C) + c0 / kF8Block];
+      } else {
+        st.y[k] = load8(static_cast<const uint16_t *>(sd.y) + t * sd.ldy, c, C);
+      }
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+        const int j = j0 + 16 * q + (lane & 15);
+        st.w[q][k] = sd.w[t * r + (j < r ? j : r - 1)];
+      }
+    }
+  };
   v4f acc[RT][8];
 #pragma unroll
   for (int q = 0; q < RT; ++q)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[q][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  Step<RT, F8> cur, next;
+  Rows ahead = rows_of(tile.r0);
+  fetch(tile.r0, ahead, cur);
+  if (tile.r0 + 32 < tile.r1) ahead = rows_of(tile.r0 + 32);
   for (int i0 = tile.r0; i0 < tile.r1; i0 += 32) {
-    uint4 y[8], f[8], o[RT][3];
-    float w[RT][8];
+    if (i0 + 32 < tile.r1) {
+      fetch(i0 + 32, ahead, next);
+      if (i0 + 64 < tile.r1) ahead = rows_of(i0 + 64);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    uint4 y[8], f[8];
+    float rest[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int i = i0 + 8 * g + k;
-      const bool in = i < tile.r1;
-      const int64_t t = rows[in ? i : tile.r1 - 1];
-      float rest = 1.0f;
-      y[k] = make_uint4(0, 0, 0, 0);
+      y[k] = cur.y[k];
+      rest[k] = 1.0f;
       if (F8) {
-        if (in && c < C) {
-          uint2 q;
-          __builtin_memcpy(&q, static_cast<const uint8_t *>(sd.y) + t * f8_row_bytes(C) + c, 8);
-          const int e = sd.ys[t * f8_scale_bytes(C) + c0 / kF8Block], h = held_scale(e);
-          const float p = __uint_as_float((uint32_t)h << 23);
-          rest = __uint_as_float((uint32_t)(127 + e - h) << 23);
-          y[k].x = __builtin_bit_cast(uint32_t, widen2(q.x, p, false));
-          y[k].y = __builtin_bit_cast(uint32_t, widen2(q.x, p, true));
-          y[k].z = __builtin_bit_cast(uint32_t, widen2(q.y, p, false));
-          y[k].w = __builtin_bit_cast(uint32_t, widen2(q.y, p, true));
-        }
-      } else if (in) {
-        y[k] = load8(static_cast<const uint16_t *>(sd.y) + t * sd.ldy, c, C);
+        const int e = (int)cur.y[k].z, h = held_scale(e);
+        const float p = __uint_as_float((uint32_t)h << 23);
+        rest[k] = __uint_as_float((uint32_t)(127 + e - h) << 23);
+        y[k].x = __builtin_bit_cast(uint32_t, widen2(cur.y[k].x, p, false));
+        y[k].y = __builtin_bit_cast(uint32_t, widen2(cur.y[k].x, p, true));
+        y[k].z = __builtin_bit_cast(uint32_t, widen2(cur.y[k].y, p, false));
+        y[k].w = __builtin_bit_cast(uint32_t, widen2(cur.y[k].y, p, true));
       }
+    }
+    if (i0 + 32 > tile.r1) {  // rows past the tile's end: zeros on both sides
 #pragma unroll
-      for (int q = 0; q < RT; ++q) {
-        const int j = j0 + 16 * q + (lane & 15);
-        w[q][k] = in && j < r ? sd.w[t * r + j] * rest : 0.0f;
-      }
+      for (int k = 0; k < 8; ++k)
+        if (i0 + 8 * g + k >= tile.r1) {
+          y[k] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int q = 0; q < RT; ++q) cur.w[q][k] = 0.0f;
+        }
     }
     transpose8(y, f);
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
-      split8(w[q], o[q]);
+      const bool in = j0 + 16 * q + (lane & 15) < r;
+      float w[8];
+      uint4 o[3];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = in ? (F8 ? cur.w[q][k] * rest[k] : cur.w[q][k]) : 0.0f;
+      split8(w, o);
 #pragma unroll
       for (int p = 2; p >= 0; --p)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[q][j] = mfma(o[q][p], f[j], acc[q][j]);
+        for (int j = 0; j < 8; ++j) acc[q][j] = mfma(o[p], f[j], acc[q][j]);
     }
+    cur = next;
   }
 #pragma unroll
   for (int q = 0; q < RT; ++q)
@@ -494,25 +616,25 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------------------
 
-int64_t shrink_splits(int64_t T, int64_t C) {
-  // at least a step of 128 columns for each wave, and no more waves than fill
-  // the chip twice
-  const int64_t tiles = T > 0 ? (T + 15) / 16 : 1, steps = (C + 127) / 128;
-  int64_t s = 512 / tiles;
-  if (s > (steps + 3) / 4) s = (steps + 3) / 4;
-  return s < 1 ? 1 : s > 16 ? 16 : s;
+// Splits of the columns: few rows of a long side are spread over more blocks.
+int64_t shrink_splits(int64_t T, int64_t C, int64_t r) {
+  return T <= 1024 && C >= 2048 && r <= 32 ? 4 : 1;
 }
 
-// Few rows: a tile's adapters go to blocks of their own.
-unsigned adapter_slots(int64_t T, int L) {
-  return T <= 512 ? (unsigned)(L < 15 ? L + 1 : 16) : 1;
+// Shares of a chunk's tiles: `want` blocks in all, no more than tiles there can be.
+unsigned tile_shares(int64_t T, int L, int64_t blocks, int64_t want) {
+  const int64_t n = T < kChunk ? T : kChunk;
+  const int64_t most = n / 16 + 1 + (L + 1 < n ? L + 1 : n);
+  int64_t z = (want + blocks - 1) / blocks;
+  return (unsigned)(z < 1 ? 1 : z > most ? most : z);
 }
 
 hipError_t shrink(const uint16_t *x, int64_t ldx, const int32_t *ids, const uint16_t *w,
                   float *part, int64_t T, int64_t C, int r, int L, int64_t S, hipStream_t s) {
-  const dim3 grid((unsigned)((T + 15) / 16), (unsigned)S, adapter_slots(T, L));
-#define BNN_SHRINK(RT) \
-  adapter_shrink_kernel<RT><<<grid, 256, 0, s>>>(x, ldx, ids, w, part, T, C, r, L)
+  const int64_t chunks = (T + kChunk - 1) / kChunk;
+  const dim3 grid((unsigned)chunks, (unsigned)S, tile_shares(T, L, chunks * S, 512));
+#define BNN_SHRINK(RT)                                                                            \
+  adapter_shrink_kernel<RT><<<grid, 64 * kShrinkWaves, 0, s>>>(x, ldx, ids, w, part, T, C, r, L)
   if (r <= 16) BNN_SHRINK(1);
   else if (r <= 32) BNN_SHRINK(2);
   else if (r <= 64) BNN_SHRINK(4);
@@ -521,25 +643,35 @@ hipError_t shrink(const uint16_t *x, int64_t ldx, const int32_t *ids, const uint
   return hipGetLastError();
 }
 
+constexpr int64_t kMostChunks = 65535;  // of a launch
+
 template <typename O>
 hipError_t expand(const float *part, int64_t S, const int32_t *ids, const uint16_t *w,
                   const float *scale, const void *base, int64_t ldb, void *out, int64_t ldo,
                   float *u, int64_t T, int64_t C, int r, int L, hipStream_t s) {
-  const int64_t all = (T + 15) / 16, cols = (C + 511) / 512;
-  int64_t tiles = all * cols / 2048;
-  tiles = tiles < 1 ? 1 : tiles > 8 ? 8 : tiles;
-  while ((all + tiles - 1) / tiles > 65535) tiles *= 2;
-  const dim3 grid((unsigned)cols, (unsigned)((all + tiles - 1) / tiles), adapter_slots(T, L));
-#define BNN_EXPAND(RQ)                                                                           \
-  adapter_expand_kernel<O, RQ><<<grid, 256, 0, s>>>(part, (int)S, ids, w, scale,                 \
-                                                    static_cast<const O *>(base), ldb,           \
-                                                    static_cast<O *>(out), ldo, u, T, C, r, L,   \
-                                                    (int)tiles)
-  if (r <= 32) BNN_EXPAND(1);
-  else if (r <= 64) BNN_EXPAND(2);
-  else BNN_EXPAND(4);
+  const int64_t all = (T + kChunk - 1) / kChunk, cols = (C + 511) / 512;
+  const O *bt = static_cast<const O *>(base);
+  O *ot = static_cast<O *>(out);
+  for (int64_t k = 0; k < all; k += kMostChunks) {  // S > 1: one launch (few rows)
+    const int64_t chunks = all - k < kMostChunks ? all - k : kMostChunks, t = k * kChunk;
+    const int64_t n = T - t < chunks * kChunk ? T - t : chunks * kChunk;
+    const dim3 grid((unsigned)cols, (unsigned)chunks, tile_shares(n, L, cols * chunks, 1024));
+#define BNN_EXPAND(RQ, S)                                                                        \
+  adapter_expand_kernel<O, RQ, S><<<grid, 256, 0, s>>>(part + t * r, ids + t, w, scale,          \
+                                                       bt ? bt + t * ldb : nullptr, ldb,         \
+                                                       ot + t * ldo, ldo, u, n, C, r, L)
+    if (S == 1) {
+      if (r <= 32) BNN_EXPAND(1, 1);
+      else if (r <= 64) BNN_EXPAND(2, 1);
+      else BNN_EXPAND(4, 1);
+    } else {
+      BNN_EXPAND(1, 4);  // r <= 32
+    }
 #undef BNN_EXPAND
-  return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t expand_as(int dtype, const float *part, int64_t S, const int32_t *ids,
@@ -565,13 +697,13 @@ struct BwdLayout {
 
 BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
   BwdLayout b;
-  const int64_t S = shrink_splits(T, N);
+  const int64_t S = shrink_splits(T, N, r);
   b.chunk = outer_chunk(T);
   const int64_t slots = T <= b.chunk ? 0 : 2 * (T / b.chunk);
   b.v = 0;
   b.part = b.v + align16(T * r * 4);
   b.rows = b.part + (S > 1 ? align16(S * T * r * 4) : 0);
-  b.off = b.rows + align16(T * 4);
+  b.off = b.rows + align16(T * 4 + 256);  // read a step past a tile's end
   b.group = b.off + align16((L + 1) * 4);
   b.slot_a = b.group + align16(group_rows_workspace(T, L));
   b.slot_b = b.slot_a + align16(slots * r * K * 4);
@@ -582,7 +714,7 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
 }  // namespace
 
 int64_t adapter_fwd_workspace(int64_t T, int64_t K, int64_t r) {
-  const int64_t S = shrink_splits(T, K);
+  const int64_t S = shrink_splits(T, K, r);
   return S > 1 ? S * T * r * 4 : 0;
 }
 
@@ -591,7 +723,7 @@ hipError_t launch_adapter_fwd(const uint16_t *x, int64_t ldx, const int32_t *ids
                               const void *base, int64_t ldb, void *out, int64_t ldo, int dtype,
                               float *u, void *workspace, int64_t T, int64_t K, int64_t N, int r,
                               int L, hipStream_t s) {
-  const int64_t S = N > 0 ? shrink_splits(T, K) : 1;
+  const int64_t S = N > 0 ? shrink_splits(T, K, r) : 1;
   float *part = S > 1 ? static_cast<float *>(workspace) : u;
   const hipError_t e = shrink(x, ldx, ids, a, part, T, K, r, L, S, s);
   if (e != hipSuccess) return e;
@@ -614,7 +746,7 @@ hipError_t launch_adapter_bwd(const AdapterGrad &q, void *workspace, int64_t T, 
   hipError_t e = hipSuccess;
   if (T > 0) {
     // without dx nothing sums the parts of v: one split
-    const int64_t S = q.dx ? shrink_splits(T, N) : 1;
+    const int64_t S = q.dx ? shrink_splits(T, N, r) : 1;
     float *part = S > 1 ? reinterpret_cast<float *>(ws + b.part) : v;
     e = shrink(q.dy, q.lddy, q.ids, q.b, part, T, N, r, L, S, s);
     if (e != hipSuccess) return e;
