@@ -36,22 +36,18 @@ __device__ __forceinline__ v4f mfma(const uint4 &a, const uint4 &b, v4f c) {
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Eight bf16 values of a row of n from element c on; zero past n.
-__device__ __forceinline__ uint4 load8(const uint16_t *row, int64_t c, int64_t n) {
-  uint4 v = {0, 0, 0, 0};
-  if (c + 8 <= n) {
-    __builtin_memcpy(&v, row + c, 16);
-    return v;
-  }
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 7; ++j)
-    if (c + j < n) w[j / 2] |= (uint32_t)row[c + j] << (16 * (j & 1));
-  v.x = w[0];
-  v.y = w[1];
-  v.z = w[2];
-  v.w = w[3];
-  return v;
+__device__ __forceinline__ uint4 words(const Chunk<bf16_t> &c) {
+  return make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+}
+// Eight elements of a row of C; LONG: C >= 8, so that no choice comes between the
+// loads of a kernel.
+template <bool LONG, typename T>
+__device__ __forceinline__ Chunk<T> raw8(const T *row, int64_t c, int64_t C) {
+  return LONG ? raw_chunk_long(row, (int)c, (int)C) : raw_chunk(row, (int)c, (int)C);
+}
+template <bool LONG>
+__device__ __forceinline__ Chunk<bf16_t> raw8(const uint16_t *row, int64_t c, int64_t C) {
+  return raw8<LONG>(reinterpret_cast<const bf16_t *>(row), c, C);
 }
 
 // Three bf16 parts whose sum is v exactly (bits below 2^-133 aside); an
@@ -112,11 +108,17 @@ __device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&f)[8]) {
 constexpr int kChunk = 256;
 
 struct Plan {
-  int key[kChunk];        // the row's id; L: none
-  uint16_t order[kChunk]; // rows of the chunk by tile
+  int row[kChunk];              // 256 id + place in the chunk (id L: none); by tile in `sorted`
+  int sorted[kChunk];
   uint16_t start[kChunk + 1];
   int waves[kChunk / 64];
   int tiles;
+
+  // row `i` of tile `at`'s `len` ones (the last again past them), and the id
+  __device__ __forceinline__ int place(int at, int len, int i) const {
+    return sorted[at + (i < len ? i : len - 1)] & (kChunk - 1);
+  }
+  __device__ __forceinline__ int id(int at) const { return sorted[at] / kChunk; }
 };
 
 // By at least kChunk threads, all of the block's.
@@ -124,28 +126,32 @@ __device__ __forceinline__ void make_plan(Plan &p, const int32_t *ids, int64_t t
                                           int L) {
   const int i = threadIdx.x;
   const int n = T - t0 < kChunk ? (int)(T - t0) : kChunk;
-  int key = 0x7FFFFFFF;
+  int mine = 0x7FFFFFFF;
   if (i < n) {
-    key = ids[t0 + i];
-    if (key < 0 || key >= L) key = L;
+    int id = ids[t0 + i];
+    if (id < 0 || id >= L) id = L;
+    mine = id * kChunk + i;
   }
-  if (i < kChunk) p.key[i] = key;
+  if (i < kChunk) p.row[i] = mine;
   __syncthreads();
-  const int changes = __syncthreads_count(i > 0 && i < n && key != p.key[i - 1]);
+  const bool change = i > 0 && i < n && mine / kChunk != p.row[i - 1] / kChunk;
   int at = i;
-  if (changes > 8) {
+  if (__syncthreads_count(change) > 8) {
     at = 0;
     if (i < n) {
-      for (int j = 0; j < n; j += 4) {  // places past n hold the largest key
-        const int4 k = *reinterpret_cast<const int4 *>(p.key + j);
-        at += (k.x < key || (k.x == key && j < i)) + (k.y < key || (k.y == key && j + 1 < i)) +
-              (k.z < key || (k.z == key && j + 2 < i)) + (k.w < key || (k.w == key && j + 3 < i));
+#pragma unroll 4
+      for (int j = 0; j < n; j += 4) {  // places past n hold the largest value
+        const int4 k = *reinterpret_cast<const int4 *>(p.row + j);
+        at += k.x < mine;
+        at += k.y < mine;
+        at += k.z < mine;
+        at += k.w < mine;
       }
     }
   }
-  if (i < n) p.order[at] = (uint16_t)i;
+  if (i < n) p.sorted[at] = mine;
   __syncthreads();
-  const bool begin = i < n && ((i & 15) == 0 || p.key[p.order[i]] != p.key[p.order[i - 1]]);
+  const bool begin = i < n && ((i & 15) == 0 || p.id(i) != p.id(i - 1));
   const uint64_t all = __ballot(begin);
   if ((i & 63) == 0 && i < kChunk) p.waves[i >> 6] = __popcll(all);
   __syncthreads();
@@ -165,35 +171,38 @@ __device__ __forceinline__ void make_plan(Plan &p, const int32_t *ids, int64_t t
 }
 
 // ---------------------------------------------------------------------------
-// shrink: part[s][t][j] = sum over split s of the columns of x_t[c] w_id,j[c].
-// The eight waves of a block take every eighth step of 128 columns (a lane: 32
-// neighbours, 64 bytes) of the block's split of a tile and join their sums in
-// LDS.  blockIdx: chunk, split, share of the chunk's tiles.
+// shrink: u_t[j] = sum_c x_t[c] w_id,j[c], and the parts of s u_t for expand.
+// The eight waves of a block take every eighth step of 128 columns of a tile and
+// join their sums in LDS.  blockIdx: chunk, share of the chunk's tiles.
+//
+// A row's parts are 16 RP bf16 values a part: for ranks up to 16 (RP = 1) four of
+// them -- high, middle, low, zeros -- so that two neighbouring ones make one operand
+// of 32; for larger ranks (RP even) three.
 
 constexpr int kShrinkWaves = 8;
+constexpr int parts_kept(int rp) { return rp == 1 ? 4 : 3; }
 
-template <int RT>
+template <int RT, bool LONG>
 __global__ void __launch_bounds__(64 * kShrinkWaves)
     adapter_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx,
                           const int32_t *__restrict__ ids, const uint16_t *__restrict__ w,
-                          float *__restrict__ part, int64_t T, int64_t C, int r, int L) {
+                          const float *__restrict__ scale, float *__restrict__ u,
+                          uint16_t *__restrict__ parts, int64_t T, int64_t C, int r, int L) {
   constexpr int JT = RT < 4 ? RT : 4;  // rank tiles joined at a time
   __shared__ Plan plan;
   __shared__ v4f join[kShrinkWaves][JT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
   const int64_t t0 = (int64_t)blockIdx.x * kChunk;
   make_plan(plan, ids, t0, T, L);
-  const int lo = (int)((int64_t)plan.tiles * blockIdx.z / gridDim.z);
-  const int hi = (int)((int64_t)plan.tiles * (blockIdx.z + 1) / gridDim.z);
+  const int lo = (int)((int64_t)plan.tiles * blockIdx.y / gridDim.y);
+  const int hi = (int)((int64_t)plan.tiles * (blockIdx.y + 1) / gridDim.y);
   const int64_t steps = (C + 127) / 128, whole = C / 128;
-  const int units = kShrinkWaves * gridDim.y, unit = kShrinkWaves * blockIdx.y + wave;
   for (int i = lo; i < hi; ++i) {
     const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
-    const int l = plan.key[plan.order[s0]];
+    const int l = plan.id(s0);
     const bool mine = (lane & 15) < len;
-    const int64_t t = t0 + plan.order[s0 + (mine ? lane & 15 : len - 1)];
+    const int64_t t = t0 + plan.place(s0, len, lane & 15);
     const uint16_t *xr = x + t * ldx;
-    float *out = part + ((int64_t)blockIdx.y * T + t) * r;
     v4f acc[RT];
 #pragma unroll
     for (int q = 0; q < RT; ++q) acc[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -204,15 +213,18 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
         const int j = 16 * q + (lane & 15);
         wr[q] = w + ((int64_t)l * r + (j < r ? j : r - 1)) * C;
       }
-      int64_t st = unit;
+      int64_t st = wave;
       auto several = [&](auto n) {  // n steps, all their loads in flight
         uint4 xv[n][4], wv[n][RT][4];
 #pragma unroll
         for (int m = 0; m < n; ++m) {
-          const int64_t c = (st + m * units) * 128 + 32 * g;
-          __builtin_memcpy(xv[m], xr + c, 64);
+          const int64_t c = (st + m * kShrinkWaves) * 128 + 8 * g;
 #pragma unroll
-          for (int q = 0; q < RT; ++q) __builtin_memcpy(wv[m][q], wr[q] + c, 64);
+          for (int k = 0; k < 4; ++k) {
+            __builtin_memcpy(&xv[m][k], xr + c + 32 * k, 16);
+#pragma unroll
+            for (int q = 0; q < RT; ++q) __builtin_memcpy(&wv[m][q][k], wr[q] + c + 32 * k, 16);
+          }
         }
 #pragma unroll
         for (int m = 0; m < n; ++m)
@@ -220,21 +232,33 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
           for (int q = 0; q < RT; ++q)
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[q] = mfma(wv[m][q][k], xv[m][k], acc[q]);
-        st += n * units;
+        st += n * kShrinkWaves;
       };
       constexpr int kSteps = RT <= 2 ? 2 : 1;
-      while (st + (kSteps - 1) * units < whole) several(std::integral_constant<int, kSteps>());
+      while (st + (kSteps - 1) * kShrinkWaves < whole)
+        several(std::integral_constant<int, kSteps>());
       if (kSteps > 1 && st < whole) several(std::integral_constant<int, 1>());
       if (st < steps) {  // the last columns
-        const int64_t c = st * 128 + 32 * g;
+        const int c = (int)(st * 128) + 8 * g;
+        Chunk<bf16_t> xv[4], wv[RT][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint4 xv = load8(xr, c + 8 * k, C);
+          xv[k] = raw8<LONG>(xr, c + 32 * k, C);
 #pragma unroll
-          for (int q = 0; q < RT; ++q) acc[q] = mfma(load8(wr[q], c + 8 * k, C), xv, acc[q]);
+          for (int q = 0; q < RT; ++q) wv[q][k] = raw8<LONG>(wr[q], c + 32 * k, C);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          settle_chunk(xv[k], c + 32 * k, (int)C);
+#pragma unroll
+          for (int q = 0; q < RT; ++q) {
+            settle_chunk(wv[q][k], c + 32 * k, (int)C);
+            acc[q] = mfma(words(wv[q][k]), words(xv[k]), acc[q]);
+          }
         }
       }
     }
+    const float s = l < L && scale ? scale[l] : 1.0f;
 #pragma unroll
     for (int q0 = 0; q0 < RT; q0 += JT) {
       __syncthreads();  // the sums before have been read
@@ -242,32 +266,50 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
       for (int q = 0; q < JT; ++q) join[wave][q][lane] = acc[q0 + q];
       __syncthreads();
       if (wave < JT) {
-        v4f s = join[0][wave][lane];
+        v4f sum = join[0][wave][lane];
 #pragma unroll
-        for (int k = 1; k < kShrinkWaves; ++k) s += join[k][wave][lane];
+        for (int k = 1; k < kShrinkWaves; ++k) sum += join[k][wave][lane];
+        const int j = 16 * (q0 + wave) + 4 * g;
+        if (!mine) continue;
+        uint2 p[3];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const int j = 16 * (q0 + wave) + 4 * g + v;
-          if (mine && j < r) out[j] = s[v];
+          if (j + v >= r) sum[v] = 0.0f;  // computed from rank r - 1 again
+          else u[t * r + j + v] = sum[v];
         }
+        const Parts a = parts_of(sum[0] * s), b = parts_of(sum[1] * s);
+        const Parts c = parts_of(sum[2] * s), d = parts_of(sum[3] * s);
+        p[0] = make_uint2(__builtin_amdgcn_perm(b.hi, a.hi, 0x07060302u),
+                          __builtin_amdgcn_perm(d.hi, c.hi, 0x07060302u));
+        p[1] = make_uint2(__builtin_amdgcn_perm(b.mid, a.mid, 0x07060302u),
+                          __builtin_amdgcn_perm(d.mid, c.mid, 0x07060302u));
+        p[2] = make_uint2(__builtin_amdgcn_perm(b.lo, a.lo, 0x07060302u),
+                          __builtin_amdgcn_perm(d.lo, c.lo, 0x07060302u));
+        if (!parts) continue;
+        uint16_t *row = parts + t * (parts_kept(RT) * 16 * RT) + j;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2 *>(row + k * 16 * RT) = p[k];
+        if (RT == 1) *reinterpret_cast<uint2 *>(row + 48) = make_uint2(0, 0);
       }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// expand: out_t[c] = base_t[c] + s sum_j u_t[j] w_id,j[c], u_t the sum of S parts.
-// A wave has 128 columns; the operand of its adapter's factor stays in registers
-// while the adapter does not change.  A lane ends up with eight neighbouring
-// columns of four rows.  The next tile's u and base are on their way while a tile
-// is computed.  blockIdx: 512 columns, chunk, share of the chunk's tiles.
+// expand: out_t[c] = base_t[c] + sum_j (s u_t[j]) w_id,j[c], the bracket from the
+// parts that shrink left.  A wave has 128 columns; the operand of its adapter's
+// factor stays in registers while the adapter does not change.  A lane ends up
+// with eight neighbouring columns of four rows.  The next tile's operands and
+// base are on their way while a tile is computed.  blockIdx: 512 columns, chunk,
+// share of the chunk's tiles.
 
-template <typename O, int RQ, int S>
+template <typename O, int RP, bool LONG>
 __global__ void __launch_bounds__(256)
-    adapter_expand_kernel(const float *__restrict__ part, const int32_t *__restrict__ ids,
-                          const uint16_t *__restrict__ w, const float *__restrict__ scale,
-                          const O *base, int64_t ldb, O *out, int64_t ldo, float *__restrict__ u,
-                          int64_t T, int64_t C, int r, int L) {
+    adapter_expand_kernel(const uint16_t *__restrict__ parts, const int32_t *__restrict__ ids,
+                          const uint16_t *__restrict__ w, const O *base, int64_t ldb, O *out,
+                          int64_t ldo, int64_t T, int64_t C, int r, int L) {
+  constexpr int Q = (RP + 1) / 2;           // operands of 32 ranks
+  constexpr int P = RP == 1 ? 2 : 3;        // and the parts of each
   __shared__ Plan plan;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
   const int64_t t0 = (int64_t)blockIdx.y * kChunk;
@@ -277,108 +319,94 @@ __global__ void __launch_bounds__(256)
   const int64_t c0 = ((int64_t)blockIdx.x * 4 + wave) * 128;
   if (c0 >= C || lo >= hi) return;
   const int64_t c = c0 + 8 * (lane & 15);
+  const bool edge = c0 + 128 > C;
 
   struct Fetch {
-    int len, l;
-    int64_t tu;  // of row lane % 16
-    float u[RQ][8][S];
+    uint4 u[Q][P];
     Chunk<O> b[4];
   };
-  auto row_of = [&](int s0, int len, int i) {
-    return t0 + plan.order[s0 + (i < len ? i : len - 1)];
-  };
   auto fetch = [&](int i, Fetch &f) {
-    const int s0 = plan.start[i];
-    f.len = plan.start[i + 1] - s0;
-    f.l = plan.key[plan.order[s0]];
-    f.tu = row_of(s0, f.len, lane & 15);
+    i = i < hi ? i : hi - 1;  // past the last: again, unused
+    const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
+    const uint16_t *row = parts + (t0 + plan.place(s0, len, lane & 15)) *
+                                      (parts_kept(RP) * 16 * RP) + 8 * g;
 #pragma unroll
-    for (int q = 0; q < RQ; ++q)
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int j = 32 * q + 8 * g + k;
-#pragma unroll
-        for (int p = 0; p < S; ++p)
-          f.u[q][k][p] = part[((int64_t)p * T + f.tu) * r + (j < r ? j : r - 1)];
-      }
+      for (int p = 0; p < P; ++p)
+        f.u[q][p] = *reinterpret_cast<const uint4 *>(row + 32 * q + p * (RP == 1 ? 32 : 16 * RP));
     if (base) {
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        f.b[v] = load_chunk(base + row_of(s0, f.len, 4 * g + v) * ldb, (int)c, (int)C);
+        f.b[v] = raw8<LONG>(base + (t0 + plan.place(s0, len, 4 * g + v)) * ldb, c, C);
     }
   };
 
   int now = -1;  // the adapter whose factor is in wf
-  uint4 wf[RQ][8];
-  float s = 0.0f;
-  Fetch cur, next;
-  fetch(lo, cur);
-  for (int i = lo; i < hi; ++i) {
-    const int s0 = plan.start[i], len = cur.len;
-    const bool has = cur.l < L;
-    if (has && cur.l != now) {
-      now = cur.l;
-      s = scale ? scale[now] : 1.0f;
+  uint4 wf[Q][8];
+  auto tile = [&](int i, Fetch &f) {
+    const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
+    const int l = plan.id(s0);
+    const bool has = l < L;
+    if (!has && base == out) return;  // in place, rows without an adapter stay as they are
+    if (has && l != now) {
+      now = l;
 #pragma unroll
-      for (int q = 0; q < RQ; ++q) {
+      for (int q = 0; q < Q; ++q) {
         uint4 rows[8];
+        Chunk<bf16_t> raw[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int j = 32 * q + 8 * g + k;
-          rows[k] = load8(w + ((int64_t)now * r + (j < r ? j : r - 1)) * C, c, C);
+          const int j = (RP == 1 ? 8 * (g & 1) : 32 * q + 8 * g) + k;
+          raw[k] = raw8<LONG>(w + ((int64_t)l * r + (j < r ? j : r - 1)) * C, c, C);
         }
-        if (32 * q + 32 > r) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (edge) settle_chunk(raw[k], (int)c, (int)C);
+          rows[k] = words(raw[k]);
+        }
+        if (r < 16 * RP) {  // ranks past r: no value, not even an infinite one
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (32 * q + 8 * g + k >= r) rows[k] = make_uint4(0, 0, 0, 0);
+            if ((RP == 1 ? 8 * (g & 1) : 32 * q + 8 * g) + k >= r) rows[k] = make_uint4(0, 0, 0, 0);
         }
         transpose8(rows, wf[q]);
       }
     }
-    fetch(i + 1 < hi ? i + 1 : i, next);
-    __builtin_amdgcn_sched_barrier(0);
     v4f acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    const bool mine = (lane & 15) < len;
-    if (has || (u && c0 == 0)) {
+    if (has) {
 #pragma unroll
-      for (int q = 0; q < RQ; ++q) {
-        float v[8];
+      for (int p = P - 1; p >= 0; --p)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int j = 32 * q + 8 * g + k;
-          v[k] = cur.u[q][k][0];
+        for (int q = 0; q < Q; ++q)
 #pragma unroll
-          for (int p = 1; p < S; ++p) v[k] += cur.u[q][k][p];
-          if (!(mine && j < r && has)) v[k] = 0.0f;
-          if (S > 1 && u && c0 == 0 && mine && j < r) u[cur.tu * r + j] = v[k];
-          v[k] *= s;
-        }
-        if (has) {
-          uint4 o[3];
-          split8(v, o);
-#pragma unroll
-          for (int p = 2; p >= 0; --p)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = mfma(o[p], wf[q][j], acc[j]);
-        }
-      }
+          for (int j = 0; j < 8; ++j) acc[j] = mfma(f.u[q][p], wf[q][j], acc[j]);
     }
-    if (has || base != out) {  // in place, rows without an adapter stay as they are
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (4 * g + v >= len) continue;
-        float val[8];
+    for (int v = 0; v < 4; ++v) {
+      if (4 * g + v >= len) continue;
+      if (edge && base) settle_chunk(f.b[v], (int)c, (int)C);
+      float val[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          val[j] = acc[j][v];
-          if (base) val[j] = has ? chunk_value(cur.b[v], j) + val[j] : chunk_value(cur.b[v], j);
-        }
-        store_chunk(out + row_of(s0, len, 4 * g + v) * ldo, (int)c, (int)C, val);
+      for (int j = 0; j < 8; ++j) {
+        val[j] = acc[j][v];
+        if (base) val[j] = has ? chunk_value(f.b[v], j) + val[j] : chunk_value(f.b[v], j);
       }
+      store_chunk(out + (t0 + plan.place(s0, len, 4 * g + v)) * ldo, (int)c, (int)C, val);
     }
-    cur = next;
+  };
+  Fetch one, two;
+  fetch(lo, one);
+  for (int i = lo; i < hi; i += 2) {
+    fetch(i + 1, two);
+    __builtin_amdgcn_sched_barrier(0);
+    tile(i, one);
+    if (i + 1 >= hi) return;
+    fetch(i + 2, one);
+    __builtin_amdgcn_sched_barrier(0);
+    tile(i + 1, two);
   }
 }
 
@@ -461,11 +489,12 @@ struct Step {
   float w[RT][8];
 };
 
-template <int RT, bool F8>
+template <int RT, bool F8, bool LONG>
 __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, const Tile &tile,
                                            float s, int64_t c0, int j0, int r, float *out) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int64_t c = c0 + 8 * (lane & 15), C = sd.C;
+  const bool edge = c0 + 128 > C;
   const int last = rows[tile.r1 - 1];
   struct Rows {
     int t[8];
@@ -488,7 +517,7 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
         st.y[k].y = v.y;
         st.y[k].z = sd.ys[t * f8_scale_bytes(C) + c0 / kF8Block];
       } else {
-        st.y[k] = load8(static_cast<const uint16_t *>(sd.y) + t * sd.ldy, c, C);
+        st.y[k] = words(raw8<LONG>(static_cast<const uint16_t *>(sd.y) + t * sd.ldy, c, C));
       }
 #pragma unroll
       for (int q = 0; q < RT; ++q) {
@@ -526,6 +555,10 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
         y[k].y = __builtin_bit_cast(uint32_t, widen2(cur.y[k].x, p, true));
         y[k].z = __builtin_bit_cast(uint32_t, widen2(cur.y[k].y, p, false));
         y[k].w = __builtin_bit_cast(uint32_t, widen2(cur.y[k].y, p, true));
+      } else if (edge) {
+        Chunk<bf16_t> h = {{y[k].x, y[k].y, y[k].z, y[k].w}};
+        settle_chunk(h, (int)c, (int)C);
+        y[k] = words(h);
       }
     }
     if (i0 + 32 > tile.r1) {  // rows past the tile's end: zeros on both sides
@@ -568,7 +601,7 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
 
 // blockIdx.x: 512 columns of the first or (from `split` on) the second side;
 // blockIdx.y: a tile; blockIdx.z: RT x 16 of the ranks.
-template <int RT, bool F8>
+template <int RT, bool F8, bool LONG>
 __global__ void __launch_bounds__(256)
     adapter_outer_kernel(Side first, Side second, int split, const int32_t *__restrict__ rows,
                          const int32_t *__restrict__ off, const float *__restrict__ scale, int r,
@@ -585,8 +618,8 @@ __global__ void __launch_bounds__(256)
     const float s = scale ? scale[t.l] : 1.0f;
     float *out = whole ? sd.d + (int64_t)t.l * r * sd.C : sd.slot + (int64_t)t.slot * r * sd.C;
     const int j0 = blockIdx.z * RT * 16;
-    if (two || !F8) outer_tile<RT, false>(sd, rows, t, s, c0, j0, r, out);
-    else outer_tile<RT, F8>(sd, rows, t, s, c0, j0, r, out);
+    if (two || !F8) outer_tile<RT, false, LONG>(sd, rows, t, s, c0, j0, r, out);
+    else outer_tile<RT, F8, LONG>(sd, rows, t, s, c0, j0, r, out);
   }
 }
 
@@ -616,9 +649,14 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------------------
 
-// Splits of the columns: few rows of a long side are spread over more blocks.
-int64_t shrink_splits(int64_t T, int64_t C, int64_t r) {
-  return T <= 1024 && C >= 2048 && r <= 32 ? 4 : 1;
+// Ranks in tiles of 16, as the kernels are made for them.
+int rank_tiles(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8; }
+
+int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
+
+int64_t parts_bytes(int64_t T, int64_t r) {
+  const int rp = rank_tiles(r);
+  return T * parts_kept(rp) * 32 * rp;
 }
 
 // Shares of a chunk's tiles: `want` blocks in all, no more than tiles there can be.
@@ -630,60 +668,73 @@ unsigned tile_shares(int64_t T, int L, int64_t blocks, int64_t want) {
 }
 
 hipError_t shrink(const uint16_t *x, int64_t ldx, const int32_t *ids, const uint16_t *w,
-                  float *part, int64_t T, int64_t C, int r, int L, int64_t S, hipStream_t s) {
+                  const float *scale, float *u, uint16_t *parts, int64_t T, int64_t C, int r,
+                  int L, hipStream_t s) {
   const int64_t chunks = (T + kChunk - 1) / kChunk;
-  const dim3 grid((unsigned)chunks, (unsigned)S, tile_shares(T, L, chunks * S, 512));
-#define BNN_SHRINK(RT)                                                                            \
-  adapter_shrink_kernel<RT><<<grid, 64 * kShrinkWaves, 0, s>>>(x, ldx, ids, w, part, T, C, r, L)
-  if (r <= 16) BNN_SHRINK(1);
-  else if (r <= 32) BNN_SHRINK(2);
-  else if (r <= 64) BNN_SHRINK(4);
-  else BNN_SHRINK(8);
+  const dim3 grid((unsigned)chunks, tile_shares(T, L, chunks, 512));
+#define BNN_SHRINK_AS(RT, LONG)                                                                 \
+  adapter_shrink_kernel<RT, LONG><<<grid, 64 * kShrinkWaves, 0, s>>>(x, ldx, ids, w, scale, u,  \
+                                                                     parts, T, C, r, L)
+#define BNN_SHRINK(RT)                    \
+  do {                                    \
+    if (C >= 8) BNN_SHRINK_AS(RT, true);  \
+    else BNN_SHRINK_AS(RT, false);        \
+  } while (0)
+  switch (rank_tiles(r)) {
+    case 1: BNN_SHRINK(1); break;
+    case 2: BNN_SHRINK(2); break;
+    case 4: BNN_SHRINK(4); break;
+    default: BNN_SHRINK(8);
+  }
 #undef BNN_SHRINK
+#undef BNN_SHRINK_AS
   return hipGetLastError();
 }
 
 constexpr int64_t kMostChunks = 65535;  // of a launch
 
 template <typename O>
-hipError_t expand(const float *part, int64_t S, const int32_t *ids, const uint16_t *w,
-                  const float *scale, const void *base, int64_t ldb, void *out, int64_t ldo,
-                  float *u, int64_t T, int64_t C, int r, int L, hipStream_t s) {
+hipError_t expand(const uint16_t *parts, const int32_t *ids, const uint16_t *w, const void *base,
+                  int64_t ldb, void *out, int64_t ldo, int64_t T, int64_t C, int r, int L,
+                  hipStream_t s) {
   const int64_t all = (T + kChunk - 1) / kChunk, cols = (C + 511) / 512;
   const O *bt = static_cast<const O *>(base);
   O *ot = static_cast<O *>(out);
-  for (int64_t k = 0; k < all; k += kMostChunks) {  // S > 1: one launch (few rows)
+  for (int64_t k = 0; k < all; k += kMostChunks) {
     const int64_t chunks = all - k < kMostChunks ? all - k : kMostChunks, t = k * kChunk;
     const int64_t n = T - t < chunks * kChunk ? T - t : chunks * kChunk;
     const dim3 grid((unsigned)cols, (unsigned)chunks, tile_shares(n, L, cols * chunks, 1024));
-#define BNN_EXPAND(RQ, S)                                                                        \
-  adapter_expand_kernel<O, RQ, S><<<grid, 256, 0, s>>>(part + t * r, ids + t, w, scale,          \
-                                                       bt ? bt + t * ldb : nullptr, ldb,         \
-                                                       ot + t * ldo, ldo, u, n, C, r, L)
-    if (S == 1) {
-      if (r <= 32) BNN_EXPAND(1, 1);
-      else if (r <= 64) BNN_EXPAND(2, 1);
-      else BNN_EXPAND(4, 1);
-    } else {
-      BNN_EXPAND(1, 4);  // r <= 32
+    const uint16_t *pt = parts + parts_bytes(t, r) / 2;
+#define BNN_EXPAND_AS(RP, LONG)                                                                  \
+  adapter_expand_kernel<O, RP, LONG><<<grid, 256, 0, s>>>(pt, ids + t, w,                        \
+                                                          bt ? bt + t * ldb : nullptr, ldb,      \
+                                                          ot + t * ldo, ldo, n, C, r, L)
+#define BNN_EXPAND(RP)                    \
+  do {                                    \
+    if (C >= 8) BNN_EXPAND_AS(RP, true);  \
+    else BNN_EXPAND_AS(RP, false);        \
+  } while (0)
+    switch (rank_tiles(r)) {
+      case 1: BNN_EXPAND(1); break;
+      case 2: BNN_EXPAND(2); break;
+      case 4: BNN_EXPAND(4); break;
+      default: BNN_EXPAND(8);
     }
 #undef BNN_EXPAND
+#undef BNN_EXPAND_AS
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-hipError_t expand_as(int dtype, const float *part, int64_t S, const int32_t *ids,
-                     const uint16_t *w, const float *scale, const void *base, int64_t ldb,
-                     void *out, int64_t ldo, float *u, int64_t T, int64_t C, int r, int L,
-                     hipStream_t s) {
+hipError_t expand_as(int dtype, const uint16_t *parts, const int32_t *ids, const uint16_t *w,
+                     const void *base, int64_t ldb, void *out, int64_t ldo, int64_t T, int64_t C,
+                     int r, int L, hipStream_t s) {
   if (dtype == BNN_FP32)
-    return expand<float>(part, S, ids, w, scale, base, ldb, out, ldo, u, T, C, r, L, s);
-  return expand<bf16_t>(part, S, ids, w, scale, base, ldb, out, ldo, u, T, C, r, L, s);
+    return expand<float>(parts, ids, w, base, ldb, out, ldo, T, C, r, L, s);
+  return expand<bf16_t>(parts, ids, w, base, ldb, out, ldo, T, C, r, L, s);
 }
-
-int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
 
 // Rows of a tile of the outer sums: few enough tiles that the slots stay small.
 int64_t outer_chunk(int64_t T) {
@@ -692,17 +743,16 @@ int64_t outer_chunk(int64_t T) {
 }
 
 struct BwdLayout {
-  int64_t v, part, rows, off, group, slot_a, slot_b, bytes, chunk;
+  int64_t v, parts, rows, off, group, slot_a, slot_b, bytes, chunk;
 };
 
 BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
   BwdLayout b;
-  const int64_t S = shrink_splits(T, N, r);
   b.chunk = outer_chunk(T);
   const int64_t slots = T <= b.chunk ? 0 : 2 * (T / b.chunk);
   b.v = 0;
-  b.part = b.v + align16(T * r * 4);
-  b.rows = b.part + (S > 1 ? align16(S * T * r * 4) : 0);
+  b.parts = b.v + align16(T * r * 4);
+  b.rows = b.parts + parts_bytes(T, r);
   b.off = b.rows + align16(T * 4 + 256);  // read a step past a tile's end
   b.group = b.off + align16((L + 1) * 4);
   b.slot_a = b.group + align16(group_rows_workspace(T, L));
@@ -713,23 +763,17 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
 
 }  // namespace
 
-int64_t adapter_fwd_workspace(int64_t T, int64_t K, int64_t r) {
-  const int64_t S = shrink_splits(T, K, r);
-  return S > 1 ? S * T * r * 4 : 0;
-}
+int64_t adapter_fwd_workspace(int64_t T, int64_t r) { return parts_bytes(T, r); }
 
 hipError_t launch_adapter_fwd(const uint16_t *x, int64_t ldx, const int32_t *ids,
                               const uint16_t *a, const uint16_t *b, const float *scale,
                               const void *base, int64_t ldb, void *out, int64_t ldo, int dtype,
                               float *u, void *workspace, int64_t T, int64_t K, int64_t N, int r,
                               int L, hipStream_t s) {
-  const int64_t S = N > 0 ? shrink_splits(T, K, r) : 1;
-  float *part = S > 1 ? static_cast<float *>(workspace) : u;
-  const hipError_t e = shrink(x, ldx, ids, a, part, T, K, r, L, S, s);
-  if (e != hipSuccess) return e;
-  if (N == 0) return hipSuccess;
-  return expand_as(dtype, part, S, ids, b, scale, base, ldb, out, ldo, S > 1 ? u : nullptr, T, N,
-                   r, L, s);
+  uint16_t *parts = static_cast<uint16_t *>(workspace);
+  const hipError_t e = shrink(x, ldx, ids, a, scale, u, N > 0 ? parts : nullptr, T, K, r, L, s);
+  if (e != hipSuccess || N == 0) return e;
+  return expand_as(dtype, parts, ids, b, base, ldb, out, ldo, T, N, r, L, s);
 }
 
 int64_t adapter_bwd_workspace(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
@@ -743,16 +787,13 @@ hipError_t launch_adapter_bwd(const AdapterGrad &q, void *workspace, int64_t T, 
   float *v = reinterpret_cast<float *>(ws + b.v);
   int32_t *rows = reinterpret_cast<int32_t *>(ws + b.rows);
   int32_t *off = reinterpret_cast<int32_t *>(ws + b.off);
+  uint16_t *parts = reinterpret_cast<uint16_t *>(ws + b.parts);
   hipError_t e = hipSuccess;
   if (T > 0) {
-    // without dx nothing sums the parts of v: one split
-    const int64_t S = q.dx ? shrink_splits(T, N, r) : 1;
-    float *part = S > 1 ? reinterpret_cast<float *>(ws + b.part) : v;
-    e = shrink(q.dy, q.lddy, q.ids, q.b, part, T, N, r, L, S, s);
+    e = shrink(q.dy, q.lddy, q.ids, q.b, q.scale, v, q.dx ? parts : nullptr, T, N, r, L, s);
     if (e != hipSuccess) return e;
     if (q.dx) {
-      e = expand_as(q.dtype, part, S, q.ids, q.a, q.scale, q.base, q.ldb, q.dx, q.lddx,
-                    S > 1 ? v : nullptr, T, K, r, L, s);
+      e = expand_as(q.dtype, parts, q.ids, q.a, q.base, q.ldb, q.dx, q.lddx, T, K, r, L, s);
       if (e != hipSuccess) return e;
     }
   }
@@ -765,18 +806,23 @@ hipError_t launch_adapter_bwd(const AdapterGrad &q, void *workspace, int64_t T, 
   const int64_t most = (T < L ? T : L) + T / b.chunk;
   if (most > 0) {
     const unsigned ty = (unsigned)(most < 65535 ? most : 65535);
-#define BNN_OUTER(RT)                                                                            \
-  if (q.xs)                                                                                      \
-    adapter_outer_kernel<RT, true><<<dim3(cols, ty, (r + RT * 16 - 1) / (RT * 16)), 256, 0, s>>>( \
-        sa, sb, split, rows, off, q.scale, r, L, (int)b.chunk);                                  \
-  else                                                                                           \
-    adapter_outer_kernel<RT, false><<<dim3(cols, ty, (r + RT * 16 - 1) / (RT * 16)), 256, 0, s>>>( \
-        sa, sb, split, rows, off, q.scale, r, L, (int)b.chunk);
-    if (r <= 16) {
-      BNN_OUTER(1)
-    } else {
-      BNN_OUTER(2)
-    }
+#define BNN_OUTER(RT, F8, LONG)                                                                  \
+  adapter_outer_kernel<RT, F8, LONG>                                                             \
+      <<<dim3(cols, ty, (r + RT * 16 - 1) / (RT * 16)), 256, 0, s>>>(sa, sb, split, rows, off,   \
+                                                                     q.scale, r, L, (int)b.chunk)
+#define BNN_OUTER_AS(RT)                                             \
+  do {                                                               \
+    if ((K < 8 && K > 0) || (N < 8 && N > 0)) {                      \
+      if (q.xs) BNN_OUTER(RT, true, false);                          \
+      else BNN_OUTER(RT, false, false);                              \
+    } else {                                                         \
+      if (q.xs) BNN_OUTER(RT, true, true);                           \
+      else BNN_OUTER(RT, false, true);                               \
+    }                                                                \
+  } while (0)
+    if (r <= 16) BNN_OUTER_AS(1);
+    else BNN_OUTER_AS(2);
+#undef BNN_OUTER_AS
 #undef BNN_OUTER
     e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -401,7 +401,7 @@ bnn_status bnn_combine_bwd(const void *dout, int dtype, int64_t lddo, const void
 
 int64_t bnn_adapter_fwd_workspace(int64_t T, int64_t K, int64_t rank) {
   if (!adapter_sizes_ok(T, K, 0, rank, 0) || T == 0) return 0;
-  return bnn::adapter_fwd_workspace(T, K, rank);
+  return bnn::adapter_fwd_workspace(T, rank);
 }
 
 bnn_status bnn_adapter_fwd(const void *x, int64_t ldx, const int32_t *ids, const void *a,

