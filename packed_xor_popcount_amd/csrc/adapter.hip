@@ -182,6 +182,30 @@ __device__ __forceinline__ void make_plan(Plan &p, const int32_t *ids, int64_t t
 constexpr int kShrinkWaves = 8;
 constexpr int parts_kept(int rp) { return rp == 1 ? 4 : 3; }
 
+// A step's 16 rows of 128 columns are loaded 256 bytes a row (16 lanes each) and
+// change to the operands' lanes through the wave's own 4 KiB of LDS, the 16-byte
+// pieces swapped by row so that neither side meets a bank twice.  Loaded as
+// operands at once, four neighbouring lanes read four rows, and a CU took in 16
+// bytes a cycle instead of 64 (8192 rows of 4096, rank 32: 37 us).
+typedef uint4 StepRows[16][16];
+
+__device__ __forceinline__ void fence_wave() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// In: v[m] is piece lane % 16 of row 4 m + lane / 16.  Out: piece 4 k + lane / 16 of
+// row lane % 16 in v[k].
+__device__ __forceinline__ void to_operands(StepRows &buf, uint4 (&v)[4]) {
+  const int lane = threadIdx.x & 63, low = lane & 15, g = lane >> 4;
+  fence_wave();
+#pragma unroll
+  for (int m = 0; m < 4; ++m) buf[4 * m + g][low ^ (4 * m + g)] = v[m];
+  fence_wave();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = buf[low][(4 * k + g) ^ low];
+}
+
 template <int RT, bool LONG>
 __global__ void __launch_bounds__(64 * kShrinkWaves)
     adapter_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx,
@@ -190,7 +214,10 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
                           uint16_t *__restrict__ parts, int64_t T, int64_t C, int r, int L) {
   constexpr int JT = RT < 4 ? RT : 4;  // rank tiles joined at a time
   __shared__ Plan plan;
-  __shared__ v4f join[kShrinkWaves][JT][64];
+  __shared__ union {
+    StepRows rows[kShrinkWaves];
+    v4f join[kShrinkWaves][JT][64];
+  } lds;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
   const int64_t t0 = (int64_t)blockIdx.x * kChunk;
   make_plan(plan, ids, t0, T, L);
@@ -202,73 +229,90 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
     const int l = plan.id(s0);
     const bool mine = (lane & 15) < len;
     const int64_t t = t0 + plan.place(s0, len, lane & 15);
-    const uint16_t *xr = x + t * ldx;
     v4f acc[RT];
 #pragma unroll
     for (int q = 0; q < RT; ++q) acc[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     if (l < L) {
-      const uint16_t *wr[RT];
+      const uint16_t *xr[4], *wr[RT][4];
 #pragma unroll
-      for (int q = 0; q < RT; ++q) {
-        const int j = 16 * q + (lane & 15);
-        wr[q] = w + ((int64_t)l * r + (j < r ? j : r - 1)) * C;
+      for (int m = 0; m < 4; ++m) {
+        xr[m] = x + (t0 + plan.place(s0, len, 4 * m + g)) * ldx;
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+          const int j = 16 * q + 4 * m + g;
+          wr[q][m] = w + ((int64_t)l * r + (j < r ? j : r - 1)) * C;
+        }
       }
       int64_t st = wave;
       auto several = [&](auto n) {  // n steps, all their loads in flight
         uint4 xv[n][4], wv[n][RT][4];
 #pragma unroll
-        for (int m = 0; m < n; ++m) {
-          const int64_t c = (st + m * kShrinkWaves) * 128 + 8 * g;
+        for (int k = 0; k < n; ++k) {
+          const int64_t c = (st + k * kShrinkWaves) * 128 + 8 * (lane & 15);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            __builtin_memcpy(&xv[m][k], xr + c + 32 * k, 16);
+          for (int m = 0; m < 4; ++m) {
+            __builtin_memcpy(&xv[k][m], xr[m] + c, 16);
 #pragma unroll
-            for (int q = 0; q < RT; ++q) __builtin_memcpy(&wv[m][q][k], wr[q] + c + 32 * k, 16);
+            for (int q = 0; q < RT; ++q) __builtin_memcpy(&wv[k][q][m], wr[q][m] + c, 16);
           }
         }
 #pragma unroll
-        for (int m = 0; m < n; ++m)
-#pragma unroll
-          for (int q = 0; q < RT; ++q)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[q] = mfma(wv[m][q][k], xv[m][k], acc[q]);
-        st += n * kShrinkWaves;
-      };
-      constexpr int kSteps = RT <= 2 ? 2 : 1;
-      while (st + (kSteps - 1) * kShrinkWaves < whole)
-        several(std::integral_constant<int, kSteps>());
-      if (kSteps > 1 && st < whole) several(std::integral_constant<int, 1>());
-      if (st < steps) {  // the last columns
-        const int c = (int)(st * 128) + 8 * g;
-        Chunk<bf16_t> xv[4], wv[RT][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          xv[k] = raw8<LONG>(xr, c + 32 * k, C);
-#pragma unroll
-          for (int q = 0; q < RT; ++q) wv[q][k] = raw8<LONG>(wr[q], c + 32 * k, C);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          settle_chunk(xv[k], c + 32 * k, (int)C);
+        for (int k = 0; k < n; ++k) {
+          to_operands(lds.rows[wave], xv[k]);
 #pragma unroll
           for (int q = 0; q < RT; ++q) {
-            settle_chunk(wv[q][k], c + 32 * k, (int)C);
-            acc[q] = mfma(words(wv[q][k]), words(xv[k]), acc[q]);
+            to_operands(lds.rows[wave], wv[k][q]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) acc[q] = mfma(wv[k][q][m], xv[k][m], acc[q]);
           }
+        }
+        st += n * kShrinkWaves;
+      };
+      constexpr int kSteps = RT == 1 ? 4 : RT == 2 ? 2 : 1;
+      while (st + (kSteps - 1) * kShrinkWaves < whole)
+        several(std::integral_constant<int, kSteps>());
+      if (kSteps > 1)
+        while (st < whole) several(std::integral_constant<int, 1>());
+      if (st < steps) {  // the last columns
+        const int c = (int)(st * 128) + 8 * (lane & 15);
+        Chunk<bf16_t> xc[4], wc[RT][4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          xc[m] = raw8<LONG>(xr[m], c, C);
+#pragma unroll
+          for (int q = 0; q < RT; ++q) wc[q][m] = raw8<LONG>(wr[q][m], c, C);
+        }
+        uint4 xv[4], wv[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          settle_chunk(xc[m], c, (int)C);
+          xv[m] = words(xc[m]);
+        }
+        to_operands(lds.rows[wave], xv);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            settle_chunk(wc[q][m], c, (int)C);
+            wv[m] = words(wc[q][m]);
+          }
+          to_operands(lds.rows[wave], wv);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) acc[q] = mfma(wv[m], xv[m], acc[q]);
         }
       }
     }
     const float s = l < L && scale ? scale[l] : 1.0f;
 #pragma unroll
     for (int q0 = 0; q0 < RT; q0 += JT) {
-      __syncthreads();  // the sums before have been read
+      __syncthreads();  // rows and sums before have been read
 #pragma unroll
-      for (int q = 0; q < JT; ++q) join[wave][q][lane] = acc[q0 + q];
+      for (int q = 0; q < JT; ++q) lds.join[wave][q][lane] = acc[q0 + q];
       __syncthreads();
       if (wave < JT) {
-        v4f sum = join[0][wave][lane];
+        v4f sum = lds.join[0][wave][lane];
 #pragma unroll
-        for (int k = 1; k < kShrinkWaves; ++k) sum += join[k][wave][lane];
+        for (int k = 1; k < kShrinkWaves; ++k) sum += lds.join[k][wave][lane];
         const int j = 16 * (q0 + wave) + 4 * g;
         if (!mine) continue;
         uint2 p[3];
@@ -292,6 +336,7 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
         if (RT == 1) *reinterpret_cast<uint2 *>(row + 48) = make_uint2(0, 0);
       }
     }
+    __syncthreads();  // the sums have been read
   }
 }
 
