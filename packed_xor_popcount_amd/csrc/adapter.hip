@@ -716,7 +716,7 @@ hipError_t shrink(const uint16_t *x, int64_t ldx, const int32_t *ids, const uint
                   const float *scale, float *u, uint16_t *parts, int64_t T, int64_t C, int r,
                   int L, hipStream_t s) {
   const int64_t chunks = (T + kChunk - 1) / kChunk;
-  const dim3 grid((unsigned)chunks, tile_shares(T, L, chunks, 512));
+  const dim3 grid((unsigned)chunks, tile_shares(T, L, chunks, 256));
 #define BNN_SHRINK_AS(RT, LONG)                                                                 \
   adapter_shrink_kernel<RT, LONG><<<grid, 64 * kShrinkWaves, 0, s>>>(x, ldx, ids, w, scale, u,  \
                                                                      parts, T, C, r, L)
@@ -748,7 +748,7 @@ hipError_t expand(const uint16_t *parts, const int32_t *ids, const uint16_t *w, 
   for (int64_t k = 0; k < all; k += kMostChunks) {
     const int64_t chunks = all - k < kMostChunks ? all - k : kMostChunks, t = k * kChunk;
     const int64_t n = T - t < chunks * kChunk ? T - t : chunks * kChunk;
-    const dim3 grid((unsigned)cols, (unsigned)chunks, tile_shares(n, L, cols * chunks, 1024));
+    const dim3 grid((unsigned)cols, (unsigned)chunks, tile_shares(n, L, cols * chunks, 384));
     const uint16_t *pt = parts + parts_bytes(t, r) / 2;
 #define BNN_EXPAND_AS(RP, LONG)                                                                  \
   adapter_expand_kernel<O, RP, LONG><<<grid, 256, 0, s>>>(pt, ids + t, w,                        \
