@@ -596,12 +596,13 @@ bnn_status bnn_combine_bwd(const void *dout, int dtype, int64_t lddo, const void
  *          be the base (same pointer and stride): rows without an adapter are then
  *          left as they are.
  *   u      T x rank fp32, what bnn_adapter_bwd takes.
- *   workspace  at least bnn_adapter_fwd_workspace(T, K, rank) bytes, 16-byte
- *          aligned, used on `stream` until the call's kernels have run.
+ *   workspace  at least bnn_adapter_fwd_workspace(T, K, N, rank, L) bytes, 16-byte
+ *          aligned, used on `stream` until the call's kernels have run; may be
+ *          NULL when that is 0 (few rows).
  * 1 <= rank <= 128, T < 2^27, L < 2^20.  T = 0 launches nothing.  Errors:
  * BNN_E_DTYPE, BNN_E_SHAPE, BNN_E_NULL, BNN_E_ALIGN, BNN_E_LAUNCH.
  */
-int64_t bnn_adapter_fwd_workspace(int64_t T, int64_t K, int64_t rank);
+int64_t bnn_adapter_fwd_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t L);
 bnn_status bnn_adapter_fwd(const void *x, int64_t ldx, const int32_t *ids, const void *a,
                            const void *b, const float *scale, const void *base, int64_t ldb,
                            void *out, int64_t ldo, int dtype, float *u, void *workspace,

@@ -104,7 +104,7 @@ def library():
     lib.bnn_adapter_fwd.argtypes = [P, I64, P, P, P, P, P, I64, P, I64, I, P, P] + [I64] * 6 + [P]
     lib.bnn_adapter_bwd.argtypes = ([P, I64, P, P, I, I64] + [P] * 6 + [I64, P, I64, I, P, P, P] + [I64] * 6
                                     + [P])
-    for name, n in (("bnn_route_fwd_workspace", 3), ("bnn_adapter_fwd_workspace", 3),
+    for name, n in (("bnn_route_fwd_workspace", 3), ("bnn_adapter_fwd_workspace", 5),
                     ("bnn_adapter_bwd_workspace", 5)):
         getattr(lib, name).argtypes, getattr(lib, name).restype = [I64] * n, I64
     for name in ("bnn_route_fwd", "bnn_route_bwd", "bnn_combine_fwd", "bnn_combine_bwd", "bnn_adapter_fwd",
@@ -828,7 +828,7 @@ def adapter_fwd(x, ids, a, b, scale=None, base=None, dtype=None, out=None):
     out, dt, ldo = _rows_out("out", out, T, N, dtype, dev)
     ldb = _same_rows("base", base, T, N, dt, dev) if base is not None else 0
     u = torch.empty((T, r), dtype=torch.float32, device=dev)
-    need = library().bnn_adapter_fwd_workspace(T, K, r)
+    need = library().bnn_adapter_fwd_workspace(T, K, N, r, L)
     ws = _workspace(need, dev)
     _call("bnn_adapter_fwd", x, _ptr(x), ldx, _ptr(ids), _ptr(a), _ptr(b), _ptr(scale), _ptr(base), ldb, _ptr(out),
           ldo, dt, _ptr(u), _ptr(ws), need, T, K, N, r, L)

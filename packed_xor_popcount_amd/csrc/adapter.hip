@@ -206,138 +206,163 @@ __device__ __forceinline__ void to_operands(StepRows &buf, uint4 (&v)[4]) {
   for (int k = 0; k < 4; ++k) v[k] = buf[low][(4 * k + g) ^ low];
 }
 
+template <int RT>
+constexpr int kJoined = RT < 4 ? RT : 4;  // rank tiles joined at a time
+
+template <int RT>
+union ShrinkLds {
+  StepRows rows[kShrinkWaves];
+  v4f join[kShrinkWaves][kJoined<RT>][64];
+};
+
+// Sums of tile i by all eight waves.  done(j, t, s, sum) is called with the sums of
+// ranks j .. j + 3 of row t (zeros past r) by the lanes that hold them; the block is
+// synchronised afterwards.
+template <int RT, int STEPS, bool LONG, typename Done>
+__device__ __forceinline__ void contract_tile(ShrinkLds<RT> &lds, const Plan &plan, int i,
+                                              int64_t t0, const uint16_t *x, int64_t ldx,
+                                              const uint16_t *w, const float *scale, int64_t C,
+                                              int r, int L, Done done) {
+  constexpr int JT = kJoined<RT>;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+  const int64_t steps = (C + 127) / 128, whole = C / 128;
+  const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
+  const int l = plan.id(s0);
+  const bool mine = (lane & 15) < len;
+  const int64_t t = t0 + plan.place(s0, len, lane & 15);
+  v4f acc[RT];
+#pragma unroll
+  for (int q = 0; q < RT; ++q) acc[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  if (l < L) {
+    const uint16_t *xr[4], *wr[RT][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      xr[m] = x + (t0 + plan.place(s0, len, 4 * m + g)) * ldx;
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+        const int j = 16 * q + 4 * m + g;
+        wr[q][m] = w + ((int64_t)l * r + (j < r ? j : r - 1)) * C;
+      }
+    }
+    int64_t st = wave;
+    auto several = [&](auto n) {  // n steps, all their loads in flight
+      uint4 xv[n][4], wv[n][RT][4];
+#pragma unroll
+      for (int k = 0; k < n; ++k) {
+        const int64_t c = (st + k * kShrinkWaves) * 128 + 8 * (lane & 15);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          __builtin_memcpy(&xv[k][m], xr[m] + c, 16);
+#pragma unroll
+          for (int q = 0; q < RT; ++q) __builtin_memcpy(&wv[k][q][m], wr[q][m] + c, 16);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < n; ++k) {
+        to_operands(lds.rows[wave], xv[k]);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+          to_operands(lds.rows[wave], wv[k][q]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) acc[q] = mfma(wv[k][q][m], xv[k][m], acc[q]);
+        }
+      }
+      st += n * kShrinkWaves;
+    };
+    while (st + (STEPS - 1) * kShrinkWaves < whole)
+      several(std::integral_constant<int, STEPS>());
+    if (STEPS > 1)
+      while (st < whole) several(std::integral_constant<int, 1>());
+    if (st < steps) {  // the last columns
+      const int c = (int)(st * 128) + 8 * (lane & 15);
+      Chunk<bf16_t> xc[4], wc[RT][4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        xc[m] = raw8<LONG>(xr[m], c, C);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) wc[q][m] = raw8<LONG>(wr[q][m], c, C);
+      }
+      uint4 xv[4], wv[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        settle_chunk(xc[m], c, (int)C);
+        xv[m] = words(xc[m]);
+      }
+      to_operands(lds.rows[wave], xv);
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          settle_chunk(wc[q][m], c, (int)C);
+          wv[m] = words(wc[q][m]);
+        }
+        to_operands(lds.rows[wave], wv);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc[q] = mfma(wv[m], xv[m], acc[q]);
+      }
+    }
+  }
+  const float s = l < L && scale ? scale[l] : 1.0f;
+#pragma unroll
+  for (int q0 = 0; q0 < RT; q0 += JT) {
+    __syncthreads();  // rows and sums before have been read
+#pragma unroll
+    for (int q = 0; q < JT; ++q) lds.join[wave][q][lane] = acc[q0 + q];
+    __syncthreads();
+    if (wave < JT && mine) {
+      v4f sum = lds.join[0][wave][lane];
+#pragma unroll
+      for (int k = 1; k < kShrinkWaves; ++k) sum += lds.join[k][wave][lane];
+      const int j = 16 * (q0 + wave) + 4 * g;
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (j + v >= r) sum[v] = 0.0f;  // rank r - 1 again
+      done(j, t, s, sum);
+    }
+  }
+  __syncthreads();  // the sums have been read
+}
+
+// The parts of s sum in a row of parts, from rank j on.
+template <int RT>
+__device__ __forceinline__ void store_parts(uint16_t *row, int j, float s, const v4f &sum) {
+  const Parts a = parts_of(sum[0] * s), b = parts_of(sum[1] * s);
+  const Parts c = parts_of(sum[2] * s), d = parts_of(sum[3] * s);
+  *reinterpret_cast<uint2 *>(row + j) = make_uint2(
+      __builtin_amdgcn_perm(b.hi, a.hi, 0x07060302u), __builtin_amdgcn_perm(d.hi, c.hi, 0x07060302u));
+  *reinterpret_cast<uint2 *>(row + j + 16 * RT) =
+      make_uint2(__builtin_amdgcn_perm(b.mid, a.mid, 0x07060302u),
+                 __builtin_amdgcn_perm(d.mid, c.mid, 0x07060302u));
+  *reinterpret_cast<uint2 *>(row + j + 32 * RT) = make_uint2(
+      __builtin_amdgcn_perm(b.lo, a.lo, 0x07060302u), __builtin_amdgcn_perm(d.lo, c.lo, 0x07060302u));
+  if (RT == 1) *reinterpret_cast<uint2 *>(row + j + 48) = make_uint2(0, 0);
+}
+
+__device__ __forceinline__ void store_sums(float *u, int j, int r, const v4f &sum) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (j + v < r) u[j + v] = sum[v];
+}
+
 template <int RT, bool LONG>
 __global__ void __launch_bounds__(64 * kShrinkWaves)
     adapter_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx,
                           const int32_t *__restrict__ ids, const uint16_t *__restrict__ w,
                           const float *__restrict__ scale, float *__restrict__ u,
                           uint16_t *__restrict__ parts, int64_t T, int64_t C, int r, int L) {
-  constexpr int JT = RT < 4 ? RT : 4;  // rank tiles joined at a time
   __shared__ Plan plan;
-  __shared__ union {
-    StepRows rows[kShrinkWaves];
-    v4f join[kShrinkWaves][JT][64];
-  } lds;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+  __shared__ ShrinkLds<RT> lds;
   const int64_t t0 = (int64_t)blockIdx.x * kChunk;
   make_plan(plan, ids, t0, T, L);
   const int lo = (int)((int64_t)plan.tiles * blockIdx.y / gridDim.y);
   const int hi = (int)((int64_t)plan.tiles * (blockIdx.y + 1) / gridDim.y);
-  const int64_t steps = (C + 127) / 128, whole = C / 128;
-  for (int i = lo; i < hi; ++i) {
-    const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
-    const int l = plan.id(s0);
-    const bool mine = (lane & 15) < len;
-    const int64_t t = t0 + plan.place(s0, len, lane & 15);
-    v4f acc[RT];
-#pragma unroll
-    for (int q = 0; q < RT; ++q) acc[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    if (l < L) {
-      const uint16_t *xr[4], *wr[RT][4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        xr[m] = x + (t0 + plan.place(s0, len, 4 * m + g)) * ldx;
-#pragma unroll
-        for (int q = 0; q < RT; ++q) {
-          const int j = 16 * q + 4 * m + g;
-          wr[q][m] = w + ((int64_t)l * r + (j < r ? j : r - 1)) * C;
-        }
-      }
-      int64_t st = wave;
-      auto several = [&](auto n) {  // n steps, all their loads in flight
-        uint4 xv[n][4], wv[n][RT][4];
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-          const int64_t c = (st + k * kShrinkWaves) * 128 + 8 * (lane & 15);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            __builtin_memcpy(&xv[k][m], xr[m] + c, 16);
-#pragma unroll
-            for (int q = 0; q < RT; ++q) __builtin_memcpy(&wv[k][q][m], wr[q][m] + c, 16);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-          to_operands(lds.rows[wave], xv[k]);
-#pragma unroll
-          for (int q = 0; q < RT; ++q) {
-            to_operands(lds.rows[wave], wv[k][q]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) acc[q] = mfma(wv[k][q][m], xv[k][m], acc[q]);
-          }
-        }
-        st += n * kShrinkWaves;
-      };
-      constexpr int kSteps = RT == 1 ? 4 : RT == 2 ? 2 : 1;
-      while (st + (kSteps - 1) * kShrinkWaves < whole)
-        several(std::integral_constant<int, kSteps>());
-      if (kSteps > 1)
-        while (st < whole) several(std::integral_constant<int, 1>());
-      if (st < steps) {  // the last columns
-        const int c = (int)(st * 128) + 8 * (lane & 15);
-        Chunk<bf16_t> xc[4], wc[RT][4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          xc[m] = raw8<LONG>(xr[m], c, C);
-#pragma unroll
-          for (int q = 0; q < RT; ++q) wc[q][m] = raw8<LONG>(wr[q][m], c, C);
-        }
-        uint4 xv[4], wv[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          settle_chunk(xc[m], c, (int)C);
-          xv[m] = words(xc[m]);
-        }
-        to_operands(lds.rows[wave], xv);
-#pragma unroll
-        for (int q = 0; q < RT; ++q) {
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            settle_chunk(wc[q][m], c, (int)C);
-            wv[m] = words(wc[q][m]);
-          }
-          to_operands(lds.rows[wave], wv);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) acc[q] = mfma(wv[m], xv[m], acc[q]);
-        }
-      }
-    }
-    const float s = l < L && scale ? scale[l] : 1.0f;
-#pragma unroll
-    for (int q0 = 0; q0 < RT; q0 += JT) {
-      __syncthreads();  // rows and sums before have been read
-#pragma unroll
-      for (int q = 0; q < JT; ++q) lds.join[wave][q][lane] = acc[q0 + q];
-      __syncthreads();
-      if (wave < JT) {
-        v4f sum = lds.join[0][wave][lane];
-#pragma unroll
-        for (int k = 1; k < kShrinkWaves; ++k) sum += lds.join[k][wave][lane];
-        const int j = 16 * (q0 + wave) + 4 * g;
-        if (!mine) continue;
-        uint2 p[3];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          if (j + v >= r) sum[v] = 0.0f;  // computed from rank r - 1 again
-          else u[t * r + j + v] = sum[v];
-        }
-        const Parts a = parts_of(sum[0] * s), b = parts_of(sum[1] * s);
-        const Parts c = parts_of(sum[2] * s), d = parts_of(sum[3] * s);
-        p[0] = make_uint2(__builtin_amdgcn_perm(b.hi, a.hi, 0x07060302u),
-                          __builtin_amdgcn_perm(d.hi, c.hi, 0x07060302u));
-        p[1] = make_uint2(__builtin_amdgcn_perm(b.mid, a.mid, 0x07060302u),
-                          __builtin_amdgcn_perm(d.mid, c.mid, 0x07060302u));
-        p[2] = make_uint2(__builtin_amdgcn_perm(b.lo, a.lo, 0x07060302u),
-                          __builtin_amdgcn_perm(d.lo, c.lo, 0x07060302u));
-        if (!parts) continue;
-        uint16_t *row = parts + t * (parts_kept(RT) * 16 * RT) + j;
-#pragma unroll
-        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2 *>(row + k * 16 * RT) = p[k];
-        if (RT == 1) *reinterpret_cast<uint2 *>(row + 48) = make_uint2(0, 0);
-      }
-    }
-    __syncthreads();  // the sums have been read
-  }
+  for (int i = lo; i < hi; ++i)
+    contract_tile<RT, (RT == 1 ? 4 : RT == 2 ? 2 : 1), LONG>(
+        lds, plan, i, t0, x, ldx, w, scale, C, r, L,
+        [&](int j, int64_t t, float s, const v4f &sum) {
+          store_sums(u + t * r, j, r, sum);
+          if (parts) store_parts<RT>(parts + t * (parts_kept(RT) * 16 * RT), j, s, sum);
+        });
 }
 
 // ---------------------------------------------------------------------------
@@ -348,13 +373,93 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
 // base are on their way while a tile is computed.  blockIdx: 512 columns, chunk,
 // share of the chunk's tiles.
 
+constexpr int operands(int rp) { return (rp + 1) / 2; }     // of 32 ranks
+constexpr int parts_of_operand(int rp) { return rp == 1 ? 2 : 3; }
+
+// A row's operands, for lane group g.
+template <int RP>
+struct RowParts {
+  uint4 v[operands(RP)][parts_of_operand(RP)];
+  __device__ __forceinline__ void load(const uint16_t *row, int g) {
+#pragma unroll
+    for (int q = 0; q < operands(RP); ++q)
+#pragma unroll
+      for (int p = 0; p < parts_of_operand(RP); ++p)
+        v[q][p] = *reinterpret_cast<const uint4 *>(row + 8 * g + 32 * q +
+                                                   p * (RP == 1 ? 32 : 16 * RP));
+  }
+};
+
+// Eight columns of 32 ranks (operand q) of an adapter's factor (r x C) from column
+// c on.
+template <int RP, bool LONG>
+struct Factor {
+  Chunk<bf16_t> raw[8];
+  __device__ __forceinline__ static int rank(int q, int g, int k) {
+    return (RP == 1 ? 8 * (g & 1) : 32 * q + 8 * g) + k;
+  }
+  __device__ __forceinline__ void load(const uint16_t *w, int q, int64_t c, int64_t C, int r,
+                                       int g) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int j = rank(q, g, k);
+      raw[k] = raw8<LONG>(w + (int64_t)(j < r ? j : r - 1) * C, c, C);
+    }
+  }
+  __device__ __forceinline__ void operand(int q, int64_t c, int64_t C, int r, int g, bool edge,
+                                          uint4 (&f)[8]) {
+    uint4 rows[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (edge) settle_chunk(raw[k], (int)c, (int)C);
+      rows[k] = words(raw[k]);
+    }
+    if (r < 16 * RP) {  // ranks past r: no value, not even an infinite one
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (rank(q, g, k) >= r) rows[k] = make_uint4(0, 0, 0, 0);
+    }
+    transpose8(rows, f);
+  }
+};
+
+// base + the products of a tile: lane g holds rows 4 g .. 4 g + 3 of it, eight columns.
+template <typename O, int RP, bool LONG>
+__device__ __forceinline__ void finish_tile(const Plan &plan, int s0, int len, bool has,
+                                            const RowParts<RP> &u,
+                                            const uint4 (&f)[operands(RP)][8], Chunk<O> (&b)[4],
+                                            bool base, O *out, int64_t ldo, int64_t t0, int64_t c,
+                                            int64_t C, bool edge, int g) {
+  v4f acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  if (has) {
+#pragma unroll
+    for (int p = parts_of_operand(RP) - 1; p >= 0; --p)
+#pragma unroll
+      for (int q = 0; q < operands(RP); ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = mfma(u.v[q][p], f[q][j], acc[j]);
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (4 * g + v >= len) continue;
+    if (edge && base) settle_chunk(b[v], (int)c, (int)C);
+    float val[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      val[j] = acc[j][v];
+      if (base) val[j] = has ? chunk_value(b[v], j) + val[j] : chunk_value(b[v], j);
+    }
+    store_chunk(out + (t0 + plan.place(s0, len, 4 * g + v)) * ldo, (int)c, (int)C, val);
+  }
+}
+
 template <typename O, int RP, bool LONG>
 __global__ void __launch_bounds__(256)
     adapter_expand_kernel(const uint16_t *__restrict__ parts, const int32_t *__restrict__ ids,
                           const uint16_t *__restrict__ w, const O *base, int64_t ldb, O *out,
                           int64_t ldo, int64_t T, int64_t C, int r, int L) {
-  constexpr int Q = (RP + 1) / 2;           // operands of 32 ranks
-  constexpr int P = RP == 1 ? 2 : 3;        // and the parts of each
   __shared__ Plan plan;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
   const int64_t t0 = (int64_t)blockIdx.y * kChunk;
@@ -367,28 +472,21 @@ __global__ void __launch_bounds__(256)
   const bool edge = c0 + 128 > C;
 
   struct Fetch {
-    uint4 u[Q][P];
+    RowParts<RP> u;
     Chunk<O> b[4];
   };
   auto fetch = [&](int i, Fetch &f) {
     i = i < hi ? i : hi - 1;  // past the last: again, unused
     const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
-    const uint16_t *row = parts + (t0 + plan.place(s0, len, lane & 15)) *
-                                      (parts_kept(RP) * 16 * RP) + 8 * g;
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        f.u[q][p] = *reinterpret_cast<const uint4 *>(row + 32 * q + p * (RP == 1 ? 32 : 16 * RP));
+    f.u.load(parts + (t0 + plan.place(s0, len, lane & 15)) * (parts_kept(RP) * 16 * RP), g);
     if (base) {
 #pragma unroll
       for (int v = 0; v < 4; ++v)
         f.b[v] = raw8<LONG>(base + (t0 + plan.place(s0, len, 4 * g + v)) * ldb, c, C);
     }
   };
-
   int now = -1;  // the adapter whose factor is in wf
-  uint4 wf[Q][8];
+  uint4 wf[operands(RP)][8];
   auto tile = [&](int i, Fetch &f) {
     const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
     const int l = plan.id(s0);
@@ -397,50 +495,15 @@ __global__ void __launch_bounds__(256)
     if (has && l != now) {
       now = l;
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        uint4 rows[8];
-        Chunk<bf16_t> raw[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int j = (RP == 1 ? 8 * (g & 1) : 32 * q + 8 * g) + k;
-          raw[k] = raw8<LONG>(w + ((int64_t)l * r + (j < r ? j : r - 1)) * C, c, C);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (edge) settle_chunk(raw[k], (int)c, (int)C);
-          rows[k] = words(raw[k]);
-        }
-        if (r < 16 * RP) {  // ranks past r: no value, not even an infinite one
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if ((RP == 1 ? 8 * (g & 1) : 32 * q + 8 * g) + k >= r) rows[k] = make_uint4(0, 0, 0, 0);
-        }
-        transpose8(rows, wf[q]);
+      for (int q = 0; q < operands(RP); ++q) {
+        Factor<RP, LONG> w8;
+        w8.load(w + (int64_t)l * r * C, q, c, C, r, g);
+        w8.operand(q, c, C, r, g, edge, wf[q]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    v4f acc[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    if (has) {
-#pragma unroll
-      for (int p = P - 1; p >= 0; --p)
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] = mfma(f.u[q][p], wf[q][j], acc[j]);
-    }
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (4 * g + v >= len) continue;
-      if (edge && base) settle_chunk(f.b[v], (int)c, (int)C);
-      float val[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        val[j] = acc[j][v];
-        if (base) val[j] = has ? chunk_value(f.b[v], j) + val[j] : chunk_value(f.b[v], j);
-      }
-      store_chunk(out + (t0 + plan.place(s0, len, 4 * g + v)) * ldo, (int)c, (int)C, val);
-    }
+    finish_tile<O, RP, LONG>(plan, s0, len, has, f.u, wf, f.b, base != nullptr, out, ldo, t0, c, C,
+                             edge, g);
   };
   Fetch one, two;
   fetch(lo, one);
@@ -452,6 +515,61 @@ __global__ void __launch_bounds__(256)
     fetch(i + 2, one);
     __builtin_amdgcn_sched_barrier(0);
     tile(i + 1, two);
+  }
+}
+
+// Few rows: both products in one launch.  Every block of 1024 columns sums u
+// again for its tiles, from the caches, which costs less than a second launch
+// waiting for the first (32 rows on 24 adapters, 4096 x 4096 rank 16: FUSED us,
+// the two kernels 12.4 us and a launch's 3.5 us on the host).
+template <typename O, int RT, bool LONG>
+__global__ void __launch_bounds__(64 * kShrinkWaves)
+    adapter_small_kernel(const uint16_t *__restrict__ x, int64_t ldx,
+                         const int32_t *__restrict__ ids, const uint16_t *__restrict__ a,
+                         const uint16_t *__restrict__ b, const float *__restrict__ scale,
+                         const O *base, int64_t ldb, O *out, int64_t ldo, float *__restrict__ u,
+                         int64_t T, int64_t K, int64_t N, int r, int L) {
+  static_assert(operands(RT) == 1, "one operand of ranks");
+  constexpr int kRow = parts_kept(RT) * 16 * RT;
+  __shared__ Plan plan;
+  __shared__ ShrinkLds<RT> lds;
+  __shared__ uint16_t parts[16][kRow] __attribute__((aligned(16)));
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+  make_plan(plan, ids, 0, T, L);
+  const int lo = (int)((int64_t)plan.tiles * blockIdx.y / gridDim.y);
+  const int hi = (int)((int64_t)plan.tiles * (blockIdx.y + 1) / gridDim.y);
+  const int64_t c0 = ((int64_t)blockIdx.x * kShrinkWaves + wave) * 128;
+  const int64_t c = c0 + 8 * (lane & 15);
+  const bool edge = c0 + 128 > N;
+  for (int i = lo; i < hi; ++i) {
+    const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
+    const int l = plan.id(s0);
+    const bool has = l < L, mine = c0 < N && (has || base != out);
+    Factor<RT, LONG> w8;
+    Chunk<O> bs[4];
+    if (mine) {  // under way during the first product
+      if (has) w8.load(b + (int64_t)l * r * N, 0, c, N, r, g);
+      if (base) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          bs[v] = raw8<LONG>(base + (int64_t)plan.place(s0, len, 4 * g + v) * ldb, c, N);
+      }
+    }
+    contract_tile<RT, (RT == 1 ? 2 : 1), LONG>(lds, plan, i, 0, x, ldx, a, scale, K, r, L,
+                                               [&](int j, int64_t t, float s, const v4f &sum) {
+                                                 if (blockIdx.x == 0)
+                                                   store_sums(u + t * r, j, r, sum);
+                                                 store_parts<RT>(parts[lane & 15], j, s, sum);
+                                               });
+    if (!mine) continue;
+    RowParts<RT> rp;
+    rp.load(parts[lane & 15], g);
+    uint4 f[operands(RT)][8];
+    if (has) {
+      w8.operand(0, c, N, r, g, edge, f[0]);
+    }
+    finish_tile<O, RT, LONG>(plan, s0, len, has, rp, f, bs, base != nullptr, out, ldo, 0, c, N,
+                             edge, g);
   }
 }
 
@@ -806,15 +924,49 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
   return b;
 }
 
+bool adapter_small(int64_t T, int64_t N, int64_t r, int64_t L) {
+  return T <= kChunk && r <= 32 && (T / 16 + 1 + (L + 1 < T ? L + 1 : T)) * ((N + 1023) / 1024) <= 256;
+}
+
+// No more tiles than blocks that run at once, in one chunk.
+template <typename O>
+hipError_t small(const uint16_t *x, int64_t ldx, const int32_t *ids, const uint16_t *a,
+                 const uint16_t *b, const float *scale, const void *base, int64_t ldb, void *out,
+                 int64_t ldo, float *u, int64_t T, int64_t K, int64_t N, int r, int L,
+                 hipStream_t s) {
+  const dim3 grid((unsigned)((N + 1023) / 1024), tile_shares(T, (int)L, 1, kChunk));
+#define BNN_SMALL_AS(RT, LONG)                                                               \
+  adapter_small_kernel<O, RT, LONG><<<grid, 64 * kShrinkWaves, 0, s>>>(                      \
+      x, ldx, ids, a, b, scale, static_cast<const O *>(base), ldb, static_cast<O *>(out), ldo, \
+      u, T, K, N, r, L)
+#define BNN_SMALL(RT)                              \
+  do {                                             \
+    if (K >= 8 && N >= 8) BNN_SMALL_AS(RT, true);  \
+    else BNN_SMALL_AS(RT, false);                  \
+  } while (0)
+  if (r <= 16) BNN_SMALL(1);
+  else BNN_SMALL(2);
+#undef BNN_SMALL
+#undef BNN_SMALL_AS
+  return hipGetLastError();
+}
+
 }  // namespace
 
-int64_t adapter_fwd_workspace(int64_t T, int64_t r) { return parts_bytes(T, r); }
+int64_t adapter_fwd_workspace(int64_t T, int64_t N, int64_t r, int64_t L) {
+  return N == 0 || adapter_small(T, N, r, L) ? 0 : parts_bytes(T, r);
+}
 
 hipError_t launch_adapter_fwd(const uint16_t *x, int64_t ldx, const int32_t *ids,
                               const uint16_t *a, const uint16_t *b, const float *scale,
                               const void *base, int64_t ldb, void *out, int64_t ldo, int dtype,
                               float *u, void *workspace, int64_t T, int64_t K, int64_t N, int r,
                               int L, hipStream_t s) {
+  if (N > 0 && adapter_small(T, N, r, L)) {
+    if (dtype == BNN_FP32)
+      return small<float>(x, ldx, ids, a, b, scale, base, ldb, out, ldo, u, T, K, N, r, L, s);
+    return small<bf16_t>(x, ldx, ids, a, b, scale, base, ldb, out, ldo, u, T, K, N, r, L, s);
+  }
   uint16_t *parts = static_cast<uint16_t *>(workspace);
   const hipError_t e = shrink(x, ldx, ids, a, scale, u, N > 0 ? parts : nullptr, T, K, r, L, s);
   if (e != hipSuccess || N == 0) return e;

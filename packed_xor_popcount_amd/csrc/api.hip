@@ -399,9 +399,9 @@ bnn_status bnn_combine_bwd(const void *dout, int dtype, int64_t lddo, const void
                                                static_cast<hipStream_t>(stream)));
 }
 
-int64_t bnn_adapter_fwd_workspace(int64_t T, int64_t K, int64_t rank) {
-  if (!adapter_sizes_ok(T, K, 0, rank, 0) || T == 0) return 0;
-  return bnn::adapter_fwd_workspace(T, rank);
+int64_t bnn_adapter_fwd_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t L) {
+  if (!adapter_sizes_ok(T, K, N, rank, L) || T == 0) return 0;
+  return bnn::adapter_fwd_workspace(T, N, rank, L);
 }
 
 bnn_status bnn_adapter_fwd(const void *x, int64_t ldx, const int32_t *ids, const void *a,
@@ -415,7 +415,7 @@ bnn_status bnn_adapter_fwd(const void *x, int64_t ldx, const int32_t *ids, const
     return BNN_E_SHAPE;
   if (T > 0 && (!ids || !u || (K > 0 && !x) || (N > 0 && !out))) return BNN_E_NULL;
   if (T > 0 && L > 0 && ((K > 0 && !a) || (N > 0 && !b))) return BNN_E_NULL;
-  const int64_t need = bnn_adapter_fwd_workspace(T, K, rank);
+  const int64_t need = bnn_adapter_fwd_workspace(T, K, N, rank, L);
   if (need > 0 && !workspace) return BNN_E_NULL;
   if (ws_bytes < need) return BNN_E_SHAPE;
   const uintptr_t es = dtype == BNN_FP32 ? 4 : 2;

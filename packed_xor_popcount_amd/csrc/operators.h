@@ -49,7 +49,7 @@ hipError_t launch_combine_bwd(const void *dout, int dtype, int64_t lddo, const v
 // Low-rank adapters and their gradient.
 constexpr int64_t kAdapterMaxRank = 128;
 constexpr int64_t kAdapterMaxRows = int64_t(1) << 27;
-int64_t adapter_fwd_workspace(int64_t T, int64_t r);
+int64_t adapter_fwd_workspace(int64_t T, int64_t N, int64_t r, int64_t L);
 hipError_t launch_adapter_fwd(const uint16_t *x, int64_t ldx, const int32_t *ids,
                               const uint16_t *a, const uint16_t *b, const float *scale,
                               const void *base, int64_t ldb, void *out, int64_t ldo, int dtype,

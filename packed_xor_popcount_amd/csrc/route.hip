@@ -24,40 +24,83 @@ namespace {
 
 typedef __bf16 bf16_t;
 
-// A wave per token: lane l holds the logits l + 64 i.
-constexpr int threads_of(int vpl) { return vpl >= 16 ? 512 : 1024; }
-constexpr int64_t kRouteBlocks = 256;  // most blocks: each leaves one row of partial sums
+// LPT lanes share a token (16: a DPP row, four tokens a wave); lane l of them holds
+// the V neighbouring logits from V l on, so that ties go to the lowest lane and
+// then to the lowest place.
+constexpr int threads_of(int lpt, int v) { return lpt == 64 && v > 8 ? 512 : 1024; }
 
-// Tokens of a block: a multiple of its waves, so that there are at most
-// kRouteBlocks of them.
-inline int64_t tokens_per_block(int64_t T, int threads) {
-  const int64_t w = threads / 64;
+template <int LPT, int V>
+struct Shape {
+  static constexpr int kThreads = threads_of(LPT, V);
+  static constexpr int kWaves = kThreads / 64, kTokens = 64 / LPT;
+};
+
+template <int CTRL>
+__device__ __forceinline__ float rotated(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+// Of the token's lanes; every one receives it.  (Rotations by 8, 4, 2, 1: the
+// lanes add the same pairs, so their sums are equal bit for bit.)
+template <int LPT>
+__device__ __forceinline__ float token_max(float v) {
+  if (LPT == 64) return wave_max(v);
+  v = fmaxf(v, rotated<0x128>(v));
+  v = fmaxf(v, rotated<0x124>(v));
+  v = fmaxf(v, rotated<0x122>(v));
+  return fmaxf(v, rotated<0x121>(v));
+}
+template <int LPT>
+__device__ __forceinline__ float token_add(float v) {
+  if (LPT == 64) return wave_add(v);
+  v += rotated<0x128>(v);
+  v += rotated<0x124>(v);
+  v += rotated<0x122>(v);
+  return v + rotated<0x121>(v);
+}
+
+constexpr int64_t kRouteBlocks = 256;  // most blocks: each leaves a row of partial sums
+
+// Tokens of a block: a multiple of those that it takes at once.
+inline int64_t tokens_per_block(int64_t T, int at_once) {
   const int64_t c = (T + kRouteBlocks - 1) / kRouteBlocks;
-  const int64_t least = 4 * w;
-  return c < least ? least : (c + w - 1) / w * w;
+  return c < at_once ? at_once : (c + at_once - 1) / at_once * at_once;
 }
 
-template <typename T, int VPL>
-__device__ __forceinline__ void load_logits(const T *z, int E, float (&v)[VPL]) {
-  const int lane = threadIdx.x & 63;
+// A lane's elements of a row of E >= V; `past` behind its end.  One vector access,
+// whatever E: the last one ends with the row, and its elements move into place.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T *z, int e0, int E, float past, float (&v)[V]) {
+  T r[V];
+  const int at = e0 < E - V ? e0 : E - V;
+  __builtin_memcpy(r, z + at, sizeof(r));
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 64 * i;
-    v[i] = e < E ? (float)z[e] : -INFINITY;
+  for (int i = 0; i < V; ++i) v[i] = (float)r[i];
+  const int by = e0 - at;
+#pragma unroll
+  for (int d = V / 2; d > 0; d /= 2) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float from = i + d < V ? v[i + d] : past;
+      v[i] = (by & d) ? from : v[i];
+    }
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = by < V ? v[i] : past;
 }
 
-// The block's LDS.  `join` holds the waves' sums of p first, later the slots
-// counted by wave and expert.
+// The block's LDS.  `join` holds the tokens' choices and the waves' sums of p
+// first, later partial sums of the table or the slots counted by wave and expert.
 template <int THREADS>
 struct Shared {
-  int hist[kRouteMaxExperts + 1];    // this block's slots per expert
-  int first[kRouteMaxExperts + 1];   // row of the block's next slot per expert
+  int hist[kRouteMaxExperts + 1];   // this block's slots per expert
+  int first[kRouteMaxExperts + 1];  // row of the block's next slot per expert
   int total[kRouteMaxExperts + 1];
   union {
-    float sums[8192];                // waves x E
-    uint16_t seen[8192 + 16];        // waves x (E + 1)
-    int seg[2 * THREADS];
+    float2 slots[THREADS / 16][kRouteMaxK];  // (logit, expert) by token
+    float sums[8192];                        // waves x E
+    uint16_t seen[8192 + 16];                // waves x (E + 1)
+    int seg[8 * THREADS];
+    float fseg[4 * THREADS];
   } join;
   int wave[THREADS / 64];
   float fwave[THREADS / 64];
@@ -67,104 +110,114 @@ struct Shared {
 // Choices, weights and statistics of the block's tokens, their counts in
 // sh.hist, the number of tokens with an expert in sh.routed and the sums of p
 // in psum (E floats, or null).
-template <typename T, int VPL>
+template <typename T, int LPT, int V>
 __device__ void choose(const T *z, int64_t ldz, const uint8_t *valid, const RouteOut &o, int64_t t0,
                        int64_t t1, int E, int k, bool normalise, float *psum,
-                       Shared<threads_of(VPL)> &sh) {
-  constexpr int W = threads_of(VPL) / 64;
+                       Shared<Shape<LPT, V>::kThreads> &sh) {
+  constexpr int W = Shape<LPT, V>::kWaves, TOKENS = Shape<LPT, V>::kTokens;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int sub = lane % LPT, grp = lane / LPT, e0 = V * sub;
+  // lanes of the same token before this one
+  const uint64_t before = ((uint64_t(1) << lane) - 1) & ~((uint64_t(1) << (grp * LPT)) - 1);
   for (int e = threadIdx.x; e < E; e += 64 * W) sh.hist[e] = 0;
   if (threadIdx.x == 0) sh.routed = 0;
   __syncthreads();
-  float acc[VPL];
+  float acc[V];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
   int routed = 0;
-  for (int64_t t = t0 + wave; t < t1; t += W) {
-    float v[VPL], key[VPL], ex[VPL];
-    load_logits<T, VPL>(z + t * ldz, E, v);
-    if (valid && !valid[t]) {
+  float2 *slots = sh.join.slots[wave * TOKENS + grp];
+  for (int64_t tw = t0 + wave * TOKENS; tw < t1; tw += W * TOKENS) {
+    const int64_t t = tw + grp;
+    const bool in = t < t1;
+    float v[V], key[V], ex[V];
+    load_row<T, V>(z + (in ? t : t1 - 1) * ldz, e0, E, -INFINITY, v);
+    const bool on = in && !(valid && !valid[t]);
+    for (int j = sub; j < k; j += LPT) slots[j] = make_float2(0.0f, __int_as_float(-1));
+    float best = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) v[i] = -INFINITY;
-    }
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
+    for (int i = 0; i < V; ++i) {
+      if (!on) v[i] = -INFINITY;
       key[i] = v[i] > -INFINITY ? v[i] : -INFINITY;  // NaN is never chosen
-      m = fmaxf(m, key[i]);
+      best = fmaxf(best, key[i]);
     }
-    m = wave_max(m);
-    const float mz = m > -INFINITY ? m : 0.0f;
+    float top = token_max<LPT>(best);
+    const float mz = top > -INFINITY ? top : 0.0f;
+    routed += top > -INFINITY && sub == 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // the k largest, one after the other
+    for (int j = 0; j < k; ++j) {
+      const bool has = best == top && top > -INFINITY;
+      const uint64_t lanes = __ballot(has);
+      if (lanes == 0) break;
+      if (has && (lanes & before) == 0) {
+        bool found = false;
+        best = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (!found && key[i] == top) {
+            slots[j] = make_float2(top, __int_as_float(e0 + i));
+            key[i] = -INFINITY;
+            found = true;
+          }
+          best = fmaxf(best, key[i]);
+        }
+      }
+      top = token_max<LPT>(best);
+    }
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
+    for (int i = 0; i < V; ++i) {
       ex[i] = expf(v[i] - mz);
       sum += ex[i];
     }
-    sum = wave_add(sum);
+    sum = token_add<LPT>(sum);
     const float rsum = sum == 0.0f ? 0.0f : 1.0f / sum;  // NaN where a logit is NaN or +inf
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] = fmaf(ex[i], rsum, acc[i]);
-    routed += m > -INFINITY;
-    // the k largest, one after the other; lane j keeps choice j
-    float best = -INFINITY, top = m;
-    int chosen = -1;
-    for (int j = 0; j < k && top > -INFINITY; ++j) {
-      int at = VPL;  // this lane's lowest i that holds the largest value
+    for (int i = 0; i < V; ++i) acc[i] = fmaf(ex[i], rsum, acc[i]);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // lane `sub` finishes choices sub, sub + LPT
+    constexpr int PER = LPT == 16 ? 2 : 1;
+    float w[PER], wsum = 0.0f;
+    int e[PER];
 #pragma unroll
-      for (int i = VPL - 1; i >= 0; --i)
-        if (key[i] == top) at = i;
-      uint64_t has = __ballot(at < VPL);
-      int i0 = __builtin_amdgcn_readlane(at, __ffsll((unsigned long long)has) - 1);
-      if (VPL > 1 && (has & (has - 1))) {  // a tie: the lowest i, then the lowest lane
-        for (i0 = 0; i0 < VPL; ++i0) {
-          has = __ballot(at == i0);
-          if (has) break;
-        }
-      }
-      const int l0 = __ffsll((unsigned long long)has) - 1;
-      if (lane == j) {
-        best = top;
-        chosen = l0 + 64 * i0;
-      }
-      float next = -INFINITY;
+    for (int i = 0; i < PER; ++i) {
+      const int j = sub + LPT * i;
+      const float2 c = j < k ? slots[j] : make_float2(0.0f, __int_as_float(-1));
+      e[i] = __float_as_int(c.y);
+      w[i] = e[i] >= 0 ? expf(c.x - mz) : 0.0f;
+      wsum += w[i];
+    }
+    if (normalise) wsum = token_add<LPT>(wsum);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (lane == l0 && i == i0) key[i] = -INFINITY;
-        next = fmaxf(next, key[i]);
+    for (int i = 0; i < PER; ++i) {
+      const int j = sub + LPT * i;
+      if (e[i] >= 0)  // NaN where the statistics are
+        w[i] = normalise ? w[i] / wsum + 0.0f * rsum : w[i] * rsum;
+      if (in && j < k) {
+        o.experts[t * k + j] = e[i];
+        o.weights[t * k + j] = w[i];
+        if (e[i] >= 0) atomicAdd(&sh.hist[e[i]], 1);
       }
-      top = wave_max(next);
     }
-    float w = chosen >= 0 ? expf(best - mz) : 0.0f;
-    if (normalise) {
-      const float s = wave_add(w);
-      w = chosen >= 0 ? w / s + 0.0f * rsum : 0.0f;  // NaN where the statistics are
-    } else if (chosen >= 0) {
-      w *= rsum;
-    }
-    if (lane < k) {
-      o.experts[t * k + lane] = chosen;
-      o.weights[t * k + lane] = w;
-      if (chosen >= 0) atomicAdd(&sh.hist[chosen], 1);
-    }
-    if (lane == 0) {
+    if (in && sub == 0) {
       o.stats[2 * t] = mz;
       o.stats[2 * t + 1] = rsum;
     }
   }
-  if (lane == 0 && routed) atomicAdd(&sh.routed, routed);
-  if (psum) {
+  if (routed) atomicAdd(&sh.routed, routed);
+  __syncthreads();  // the choices have been read, the counts are complete
+  if (!psum) return;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + 64 * i < E) sh.join.sums[wave * E + lane + 64 * i] = acc[i];
+  for (int i = 0; i < V; ++i) {
+    for (int d = LPT; d < 64; d *= 2) acc[i] += __shfl_xor(acc[i], d, 64);
+    if (lane < LPT && e0 + i < E) sh.join.sums[wave * E + e0 + i] = acc[i];
   }
   __syncthreads();
-  if (psum) {
-    for (int e = threadIdx.x; e < E; e += 64 * W) {
-      float s = 0.0f;
-      for (int w = 0; w < W; ++w) s += sh.join.sums[w * E + e];
-      psum[e] = s;
-    }
+  for (int e = threadIdx.x; e < E; e += 64 * W) {
+    float s = 0.0f;
+    for (int w = 0; w < W; ++w) s += sh.join.sums[w * E + e];
+    psum[e] = s;
   }
 }
 
@@ -268,14 +321,14 @@ __device__ void finish(const RouteOut &o, const float *sums, int routed, int E, 
 }
 
 // All of it in one launch of one block.
-template <typename T, int VPL>
-__global__ void __launch_bounds__(threads_of(VPL))
+template <typename T, int LPT, int V>
+__global__ void __launch_bounds__(threads_of(LPT, V))
     route_one_kernel(const T *__restrict__ z, int64_t ldz, const uint8_t *__restrict__ valid,
                      RouteOut o, int64_t Tn, int E, int k, bool normalise) {
-  constexpr int THREADS = threads_of(VPL);
+  constexpr int THREADS = Shape<LPT, V>::kThreads;
   __shared__ Shared<THREADS> sh;
   __shared__ float sums[kRouteMaxExperts];
-  choose<T, VPL>(z, ldz, valid, o, 0, Tn, E, k, normalise, o.slope ? sums : nullptr, sh);
+  choose<T, LPT, V>(z, ldz, valid, o, 0, Tn, E, k, normalise, o.slope ? sums : nullptr, sh);
   for (int e = threadIdx.x; e < E; e += THREADS) {
     sh.total[e] = sh.hist[e];
     sh.first[e] = 0;
@@ -288,20 +341,25 @@ __global__ void __launch_bounds__(threads_of(VPL))
   place_slots<THREADS>(o, 0, Tn * k, E, k, sh);
 }
 
-// Two launches: the blocks' choices, with their counts and sums of p in the
-// workspace (a row of `table`: E counts, then the tokens with an expert) ...
-template <typename T, int VPL>
-__global__ void __launch_bounds__(threads_of(VPL))
+// Two launches: the blocks' choices, with their counts (a row of `table`: counts,
+// zeros up to a multiple of four), tokens with an expert and sums of p (`psum`,
+// rows as the table's) in the workspace ...
+__host__ __device__ inline int table_row(int E) { return (E + 3) / 4 * 4; }
+
+template <typename T, int LPT, int V>
+__global__ void __launch_bounds__(threads_of(LPT, V))
     route_choose_kernel(const T *__restrict__ z, int64_t ldz, const uint8_t *__restrict__ valid,
                         RouteOut o, int64_t Tn, int E, int k, bool normalise, int64_t C,
-                        int *__restrict__ table, float *__restrict__ psum) {
-  __shared__ Shared<threads_of(VPL)> sh;
+                        int *__restrict__ table, int *__restrict__ routed,
+                        float *__restrict__ psum) {
+  __shared__ Shared<Shape<LPT, V>::kThreads> sh;
   const int64_t t0 = (int64_t)blockIdx.x * C, t1 = t0 + C < Tn ? t0 + C : Tn;
-  choose<T, VPL>(z, ldz, valid, o, t0, t1, E, k, normalise,
-                 psum ? psum + (int64_t)blockIdx.x * E : nullptr, sh);
-  int *row = table + (int64_t)blockIdx.x * (E + 1);
-  for (int e = threadIdx.x; e < E; e += threads_of(VPL)) row[e] = sh.hist[e];
-  if (threadIdx.x == 0) row[E] = sh.routed;
+  const int row = table_row(E);
+  choose<T, LPT, V>(z, ldz, valid, o, t0, t1, E, k, normalise,
+                    psum ? psum + (int64_t)blockIdx.x * row : nullptr, sh);
+  for (int e = threadIdx.x; e < row; e += Shape<LPT, V>::kThreads)
+    table[(int64_t)blockIdx.x * row + e] = e < E ? sh.hist[e] : 0;
+  if (threadIdx.x == 0) routed[blockIdx.x] = sh.routed;
 }
 
 // ... and the rows: every block sums the whole table itself (a launch less),
@@ -309,55 +367,68 @@ __global__ void __launch_bounds__(threads_of(VPL))
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
     route_place_kernel(RouteOut o, int64_t Tn, int E, int k, int64_t C,
-                       const int *__restrict__ table, const float *__restrict__ psum) {
+                       const int *__restrict__ table, const int *__restrict__ block_routed,
+                       const float *__restrict__ psum) {
   __shared__ Shared<THREADS> sh;
   __shared__ float sums[kRouteMaxExperts];
-  const int B = gridDim.x, me = blockIdx.x;
-  // thread (segment, expert): the segment's share of the table's rows
-  int wide = 64;
-  while (wide < E) wide <<= 1;
-  const int segs = wide <= THREADS ? THREADS / wide : 1;
-  for (int e0 = 0; e0 < E; e0 += THREADS) {
-    const int e = e0 + threadIdx.x % wide, seg = threadIdx.x / wide;
-    const int per = (B + segs - 1) / segs;
-    int before = 0, total = 0;
-    if (e < E && seg < segs) {
-      const int b1 = (seg + 1) * per < B ? (seg + 1) * per : B;
-#pragma unroll 16
-      for (int b = seg * per; b < b1; ++b) {
-        const int n = table[(int64_t)b * (E + 1) + e];
-        total += n;
-        before += b < me ? n : 0;
+  const int B = gridDim.x, me = blockIdx.x, row = table_row(E);
+  // thread (segment, four experts): the segment's share of the table's rows
+  int wide = 16;
+  while (4 * wide < E) wide <<= 1;
+  const int segs = THREADS / wide, per = (B + segs - 1) / segs;
+  const int quad = threadIdx.x % wide, seg = threadIdx.x / wide;
+  const int b0 = seg * per, b1 = b0 + per < B ? b0 + per : B;
+  int4 before = {0, 0, 0, 0}, total = {0, 0, 0, 0};
+  if (4 * quad < E) {
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) {
+      const int4 n = *reinterpret_cast<const int4 *>(table + (int64_t)b * row + 4 * quad);
+      const int m = b < me ? -1 : 0;
+      total.x += n.x;
+      total.y += n.y;
+      total.z += n.z;
+      total.w += n.w;
+      before.x += n.x & m;
+      before.y += n.y & m;
+      before.z += n.z & m;
+      before.w += n.w & m;
+    }
+  }
+  reinterpret_cast<int4 *>(sh.join.seg)[threadIdx.x] = before;
+  reinterpret_cast<int4 *>(sh.join.seg)[THREADS + threadIdx.x] = total;
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += THREADS) {
+    int first = 0, all = 0;
+#pragma unroll 4
+    for (int i = 0; i < segs; ++i) {
+      first += sh.join.seg[4 * wide * i + e];
+      all += sh.join.seg[4 * THREADS + 4 * wide * i + e];
+    }
+    sh.first[e] = first;
+    sh.total[e] = all;
+  }
+  __syncthreads();
+  if (psum && me == 0) {  // the sums of p, in the same segments
+    float4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (4 * quad < E) {
+#pragma unroll 8
+      for (int b = b0; b < b1; ++b) {
+        const float4 n = *reinterpret_cast<const float4 *>(psum + (int64_t)b * row + 4 * quad);
+        p.x += n.x;
+        p.y += n.y;
+        p.z += n.z;
+        p.w += n.w;
       }
     }
-    sh.join.seg[threadIdx.x] = before;
-    sh.join.seg[THREADS + threadIdx.x] = total;
+    reinterpret_cast<float4 *>(sh.join.fseg)[threadIdx.x] = p;
     __syncthreads();
-    if (seg == 0 && e < E) {
-      for (int s = 1; s < segs; ++s) {
-        before += sh.join.seg[s * wide + threadIdx.x];
-        total += sh.join.seg[THREADS + s * wide + threadIdx.x];
-      }
-      sh.first[e] = before;
-      sh.total[e] = total;
+    for (int e = threadIdx.x; e < E; e += THREADS) {
+      float s = 0.0f;
+#pragma unroll 4
+      for (int i = 0; i < segs; ++i) s += sh.join.fseg[4 * wide * i + e];
+      sums[e] = s;
     }
     __syncthreads();
-    if (psum && me == 0) {  // the sums of p in the same segments
-      float *part = reinterpret_cast<float *>(sh.join.seg);
-      float sum = 0.0f;
-      if (e < E && seg < segs) {
-        const int b1 = (seg + 1) * per < B ? (seg + 1) * per : B;
-#pragma unroll 16
-        for (int b = seg * per; b < b1; ++b) sum += psum[(int64_t)b * E + e];
-      }
-      part[threadIdx.x] = sum;
-      __syncthreads();
-      if (seg == 0 && e < E) {
-        for (int s = 1; s < segs; ++s) sum += part[s * wide + threadIdx.x];
-        sums[e] = sum;
-      }
-      __syncthreads();
-    }
   }
   // slots of the blocks before this one that have no expert
   int mine = 0;
@@ -374,7 +445,8 @@ __global__ void __launch_bounds__(THREADS)
   if (threadIdx.x == 0) sh.first[E] = all + tail;
   if (me == 0) {
     int routed = 0;
-    for (int b = threadIdx.x; b < B; b += THREADS) routed += table[(int64_t)b * (E + 1) + E];
+    if (block_routed)
+      for (int b = threadIdx.x; b < B; b += THREADS) routed += block_routed[b];
     for (int d = 32; d > 0; d >>= 1) routed += __shfl_xor(routed, d, 64);
     if ((threadIdx.x & 63) == 0) sh.wave[threadIdx.x >> 6] = routed;
     __syncthreads();
@@ -400,118 +472,148 @@ __global__ void __launch_bounds__(THREADS)
     if (g >= 0 && g < G) atomicAdd(&hist[g], 1);
   }
   __syncthreads();
-  int *row = table + (int64_t)blockIdx.x * (G + 1);
-  for (int g = threadIdx.x; g < G; g += THREADS) row[g] = hist[g];
-  if (threadIdx.x == 0) row[G] = 0;
+  const int row = table_row(G);
+  for (int g = threadIdx.x; g < row; g += THREADS)
+    table[(int64_t)blockIdx.x * row + g] = g < G ? hist[g] : 0;
 }
 
-// dz of a token, by one wave.
-template <typename T, int VPL>
+// dz of TOKENS tokens by a wave, lanes as in the forward pass.  What the choices
+// add goes to its lanes through LDS.
+template <typename T, int LPT, int V>
 __global__ void __launch_bounds__(256)
     route_bwd_kernel(const T *__restrict__ z, int64_t ldz, const int32_t *__restrict__ experts,
                      const float *__restrict__ weights, const float *__restrict__ stats,
                      const float *__restrict__ slope, const float *__restrict__ dweights,
                      const float *__restrict__ dloss, T *__restrict__ dz, int64_t lddz, int64_t Tn,
                      int E, int k, bool normalise) {
-  const int lane = threadIdx.x & 63;
-  float gl[VPL];  // the loss's share of g
+  constexpr int TOKENS = Shape<LPT, V>::kTokens, PER = LPT == 16 ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) float adds[4][TOKENS][LPT * V];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int sub = lane % LPT, grp = lane / LPT, e0 = V * sub;
+  float *mine = adds[wave][grp];
+  float gl[V];  // the loss's share of g
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 64 * i;
-    gl[i] = slope && e < E ? dloss[0] * slope[e] : 0.0f;
+  for (int i = 0; i < V; ++i) gl[i] = 0.0f;
+  if (slope) {
+    const float dl = dloss[0];
+    load_row<float, V>(slope, e0, E, 0.0f, gl);
+#pragma unroll
+    for (int i = 0; i < V; ++i) gl[i] = e0 + i < E ? gl[i] * dl : 0.0f;
   }
-  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < Tn;
-       t += (int64_t)gridDim.x * 4) {
-    float v[VPL];
-    load_logits<T, VPL>(z + t * ldz, E, v);
+  for (int64_t tw = ((int64_t)blockIdx.x * 4 + wave) * TOKENS; tw < Tn;
+       tw += (int64_t)gridDim.x * 4 * TOKENS) {
+    const bool in = tw + grp < Tn;
+    const int64_t t = in ? tw + grp : Tn - 1;
+    float v[V];
+    load_row<T, V>(z + t * ldz, e0, E, -INFINITY, v);
     const float m = stats[2 * t], rsum = stats[2 * t + 1];
-    int mine = -1;
-    float w = 0.0f, d = 0.0f;
-    if (dweights && lane < k) {
-      mine = experts[t * k + lane];
-      w = weights[t * k + lane];
-      d = dweights[t * k + lane];
-      if (mine < 0 || mine >= E) {
-        mine = -1;
-        w = d = 0.0f;
+    int e[PER];
+    float w[PER], d[PER], inner = 0.0f;
+    if (dweights) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int j = sub + LPT * i;
+        const int64_t at = t * k + (j < k ? j : k - 1);
+        e[i] = experts[at];
+        w[i] = weights[at];
+        d[i] = dweights[at];
+        if (j >= k || e[i] < 0 || e[i] >= E) {
+          e[i] = -1;
+          w[i] = d[i] = 0.0f;
+        }
+        inner = fmaf(w[i], d[i], inner);
       }
+#pragma unroll
+      for (int i = 0; i < V; ++i) mine[e0 + i] = 0.0f;
     }
-    const float inner = wave_add(w * d);
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
+    for (int i = 0; i < V; ++i) {
       v[i] = rsum == 0.0f ? 0.0f : expf(v[i] - m) * rsum;
       s = fmaf(v[i], gl[i], s);
     }
-    s = wave_add(s);
-    if (!normalise) s += inner;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] *= gl[i] - s;
-    const float add = w * (normalise ? d - inner : d);
+    s = token_add<LPT>(s);
     if (dweights) {
-      for (int j = 0; j < k; ++j) {
-        const int e = __builtin_amdgcn_readlane(mine, j);
-        const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(add), j));
+      inner = token_add<LPT>(inner);
+      if (!normalise) s += inner;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (lane + 64 * i == e) v[i] += a;
-      }
+      for (int i = 0; i < PER; ++i)
+        if (e[i] >= 0) atomicAdd(&mine[e[i]], w[i] * (normalise ? d[i] - inner : d[i]));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + 64 * i < E) dz[t * lddz + lane + 64 * i] = (T)v[i];
+    for (int i = 0; i < V; ++i) v[i] *= gl[i] - s;
+    if (dweights) {
+      float add[V];
+      __builtin_memcpy(add, __builtin_assume_aligned(mine + e0, 4 * (V < 4 ? V : 4)), sizeof(add));
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += add[i];
+    }
+    if (!in) continue;
+    T *row = dz + t * lddz;
+    if (e0 + V <= E) {
+      T r[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) r[i] = (T)v[i];
+      __builtin_memcpy(row + e0, r, sizeof(r));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (e0 + i < E) row[e0 + i] = (T)v[i];
+    }
   }
 }
 
-template <typename T, int VPL>
+template <typename T, int LPT, int V>
 hipError_t fwd(const void *z, int64_t ldz, const uint8_t *valid, const RouteOut &o, void *ws,
                int64_t Tn, int E, int k, bool normalise, hipStream_t s) {
-  constexpr int THREADS = threads_of(VPL);
+  constexpr int THREADS = Shape<LPT, V>::kThreads;
   const T *zt = static_cast<const T *>(z);
-  const int64_t C = tokens_per_block(Tn, THREADS), B = (Tn + C - 1) / C;
+  const int64_t C = tokens_per_block(Tn, THREADS / LPT), B = (Tn + C - 1) / C;
   if (B <= 1) {
-    route_one_kernel<T, VPL><<<1, THREADS, 0, s>>>(zt, ldz, valid, o, Tn, E, k, normalise);
+    route_one_kernel<T, LPT, V><<<1, THREADS, 0, s>>>(zt, ldz, valid, o, Tn, E, k, normalise);
     return hipGetLastError();
   }
-  int *table = static_cast<int *>(ws);
-  float *psum = o.slope ? reinterpret_cast<float *>(table + B * (E + 1)) : nullptr;
-  route_choose_kernel<T, VPL><<<(unsigned)B, THREADS, 0, s>>>(zt, ldz, valid, o, Tn, E, k,
-                                                              normalise, C, table, psum);
+  int *table = static_cast<int *>(ws), *routed = table + 2 * B * table_row(E);
+  float *psum = o.slope ? reinterpret_cast<float *>(table + B * table_row(E)) : nullptr;
+  route_choose_kernel<T, LPT, V><<<(unsigned)B, THREADS, 0, s>>>(zt, ldz, valid, o, Tn, E, k,
+                                                                 normalise, C, table, routed, psum);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  route_place_kernel<THREADS><<<(unsigned)B, THREADS, 0, s>>>(o, Tn, E, k, C, table, psum);
+  route_place_kernel<THREADS><<<(unsigned)B, THREADS, 0, s>>>(o, Tn, E, k, C, table, routed, psum);
   return hipGetLastError();
 }
 
-template <typename T, int VPL>
+template <typename T, int LPT, int V>
 hipError_t bwd(const void *z, int64_t ldz, const int32_t *experts, const float *weights,
                const float *stats, const float *slope, const float *dweights, const float *dloss,
                void *dz, int64_t lddz, int64_t Tn, int E, int k, bool normalise, hipStream_t s) {
-  const int64_t need = (Tn + 3) / 4, most = 2048;
-  route_bwd_kernel<T, VPL><<<(unsigned)(need < most ? need : most), 256, 0, s>>>(
+  constexpr int64_t kAtOnce = 4 * Shape<LPT, V>::kTokens, most = 2048;
+  const int64_t need = (Tn + kAtOnce - 1) / kAtOnce;
+  route_bwd_kernel<T, LPT, V><<<(unsigned)(need < most ? need : most), 256, 0, s>>>(
       static_cast<const T *>(z), ldz, experts, weights, stats, slope, dweights, dloss,
       static_cast<T *>(dz), lddz, Tn, E, k, normalise);
   return hipGetLastError();
 }
 
-// Calls F<T, VPL> for the logits' type and number.
-#define BNN_ROUTE(F, ...)                                                             \
-  (dtype == BNN_FP32 ? (E <= 64    ? F<float, 1>(__VA_ARGS__)                         \
-                        : E <= 128 ? F<float, 2>(__VA_ARGS__)                         \
-                        : E <= 256 ? F<float, 4>(__VA_ARGS__)                         \
-                        : E <= 512 ? F<float, 8>(__VA_ARGS__)                         \
-                                   : F<float, 16>(__VA_ARGS__))                       \
-                     : (E <= 64    ? F<bf16_t, 1>(__VA_ARGS__)                        \
-                        : E <= 128 ? F<bf16_t, 2>(__VA_ARGS__)                        \
-                        : E <= 256 ? F<bf16_t, 4>(__VA_ARGS__)                        \
-                        : E <= 512 ? F<bf16_t, 8>(__VA_ARGS__)                        \
-                                   : F<bf16_t, 16>(__VA_ARGS__)))
+// Calls F<T, LPT, V> for the logits' type and number.
+#define BNN_ROUTE_AS(F, T, ...)              \
+  (E <= 16    ? F<T, 16, 1>(__VA_ARGS__)     \
+   : E <= 32  ? F<T, 16, 2>(__VA_ARGS__)     \
+   : E <= 64  ? F<T, 16, 4>(__VA_ARGS__)     \
+   : E <= 128 ? F<T, 16, 8>(__VA_ARGS__)     \
+   : E <= 256 ? F<T, 16, 16>(__VA_ARGS__)    \
+   : E <= 512 ? F<T, 64, 8>(__VA_ARGS__)     \
+              : F<T, 64, 16>(__VA_ARGS__))
+#define BNN_ROUTE(F, ...) \
+  (dtype == BNN_FP32 ? BNN_ROUTE_AS(F, float, __VA_ARGS__) : BNN_ROUTE_AS(F, bf16_t, __VA_ARGS__))
 
 }  // namespace
 
 int64_t route_fwd_workspace(int64_t T, int64_t E, int64_t k) {
-  const int64_t C = tokens_per_block(T, E > 512 ? 512 : 1024), B = (T + C - 1) / C;
-  return B <= 1 ? 0 : B * (2 * E + 1) * 4;
+  const int64_t C = tokens_per_block(T, E <= 256 ? 64 : E <= 512 ? 16 : 8), B = (T + C - 1) / C;
+  return B <= 1 ? 0 : B * (2 * table_row((int)E) + 1) * 4;
 }
 
 static int64_t group_chunk(int64_t n) {
@@ -521,7 +623,7 @@ static int64_t group_chunk(int64_t n) {
 
 int64_t group_rows_workspace(int64_t n, int64_t G) {
   const int64_t C = group_chunk(n), B = (n + C - 1) / C;
-  return (B > 0 ? B : 1) * (G + 1) * 4;
+  return (B > 0 ? B : 1) * table_row((int)G) * 4;
 }
 
 hipError_t launch_group_rows(const int32_t *ids, int32_t *rows, int32_t *offsets, void *workspace,
@@ -537,12 +639,12 @@ hipError_t launch_group_rows(const int32_t *ids, int32_t *rows, int32_t *offsets
     group_count_kernel<1024><<<B, 1024, 0, s>>>(ids, n, G, C, table);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    route_place_kernel<1024><<<B, 1024, 0, s>>>(o, n, G, 1, C, table, nullptr);
+    route_place_kernel<1024><<<B, 1024, 0, s>>>(o, n, G, 1, C, table, nullptr, nullptr);
   } else {
     group_count_kernel<512><<<B, 512, 0, s>>>(ids, n, G, C, table);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    route_place_kernel<512><<<B, 512, 0, s>>>(o, n, G, 1, C, table, nullptr);
+    route_place_kernel<512><<<B, 512, 0, s>>>(o, n, G, 1, C, table, nullptr, nullptr);
   }
   return hipGetLastError();
 }

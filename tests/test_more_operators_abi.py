@@ -91,13 +91,14 @@ def test_combine_bwd_refusals(lib):
 
 
 def test_adapter_fwd_refusals(lib):
-    need = lib.bnn_adapter_fwd_workspace(4, 4096, 16)
-    assert need > 0
-    assert all(lib.bnn_adapter_fwd_workspace(*s) == 0 for s in ((0, 4096, 16), (-1, 4096, 16), (4, -1, 16), (4, 4096, 0),
-                                                                (4, 4096, 129), (2 ** 27, 4096, 16)))
+    need = lib.bnn_adapter_fwd_workspace(400, 4096, 8, 16, 2)  # few rows need none
+    assert need > 0 and lib.bnn_adapter_fwd_workspace(4, 4096, 8, 16, 2) == 0
+    assert all(lib.bnn_adapter_fwd_workspace(*s) == 0 for s in (
+        (0, 4096, 8, 16, 2), (-1, 4096, 8, 16, 2), (400, -1, 8, 16, 2), (400, 4096, 8, 0, 2), (400, 4096, 8, 129, 2),
+        (2 ** 27, 4096, 8, 16, 2), (400, 4096, -1, 16, 2), (400, 4096, 8, 16, 2 ** 20)))
 
     def f(x=FAKE, ldx=4096, ids=FAKE, a=FAKE, b=FAKE, sc=None, base=None, ldb=0, out=FAKE, ldo=8, dt=0, u=FAKE, ws=FAKE,
-          wb=need, T=4, K=4096, N=8, r=16, L=2):
+          wb=need, T=400, K=4096, N=8, r=16, L=2):
         return lib.bnn_adapter_fwd(x, ldx, ids, a, b, sc, base, ldb, out, ldo, dt, u, ws, wb, T, K, N, r, L, None)
     assert f(dt=2) == E_DTYPE
     for kw in (dict(T=-1), dict(K=-1), dict(N=-1), dict(T=2 ** 27), dict(N=BIG, ldo=BIG), dict(r=0), dict(r=129), dict(L=-1),
