@@ -58,6 +58,18 @@ __device__ __forceinline__ float token_add(float v) {
   return v + rotated<0x121>(v);
 }
 
+template <int V>
+__device__ __forceinline__ float largest(const float (&v)[V]) {
+  float m[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) m[i] = v[i];
+#pragma unroll
+  for (int d = V / 2; d > 0; d /= 2)
+#pragma unroll
+    for (int i = 0; i < d; ++i) m[i] = fmaxf(m[i], m[i + d]);
+  return m[0];
+}
+
 constexpr int64_t kRouteBlocks = 256;  // most blocks: each leaves a row of partial sums
 
 // Tokens of a block: a multiple of those that it takes at once.
@@ -134,13 +146,12 @@ __device__ void choose(const T *z, int64_t ldz, const uint8_t *valid, const Rout
     load_row<T, V>(z + (in ? t : t1 - 1) * ldz, e0, E, -INFINITY, v);
     const bool on = in && !(valid && !valid[t]);
     for (int j = sub; j < k; j += LPT) slots[j] = make_float2(0.0f, __int_as_float(-1));
-    float best = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (!on) v[i] = -INFINITY;
       key[i] = v[i] > -INFINITY ? v[i] : -INFINITY;  // NaN is never chosen
-      best = fmaxf(best, key[i]);
     }
+    float best = largest<V>(key);
     float top = token_max<LPT>(best);
     const float mz = top > -INFINITY ? top : 0.0f;
     routed += top > -INFINITY && sub == 0;
@@ -150,19 +161,15 @@ __device__ void choose(const T *z, int64_t ldz, const uint8_t *valid, const Rout
       const bool has = best == top && top > -INFINITY;
       const uint64_t lanes = __ballot(has);
       if (lanes == 0) break;
-      if (has && (lanes & before) == 0) {
-        bool found = false;
-        best = -INFINITY;
+      const bool wins = has && (lanes & before) == 0;
+      int at = V;  // the lane's lowest place that holds its largest value
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (!found && key[i] == top) {
-            slots[j] = make_float2(top, __int_as_float(e0 + i));
-            key[i] = -INFINITY;
-            found = true;
-          }
-          best = fmaxf(best, key[i]);
-        }
-      }
+      for (int i = V - 1; i >= 0; --i) at = key[i] == best ? i : at;
+      if (wins) slots[j] = make_float2(top, __int_as_float(e0 + at));
+      at = wins ? at : -1;
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = at == i ? -INFINITY : key[i];
+      best = largest<V>(key);
       top = token_max<LPT>(best);
     }
     float sum = 0.0f;
