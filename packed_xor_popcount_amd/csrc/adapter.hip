@@ -344,18 +344,156 @@ __device__ __forceinline__ void store_sums(float *u, int j, int r, const v4f &su
     if (j + v < r) u[j + v] = sum[v];
 }
 
+// The outer sums take an adapter's rows in tiles of `chunk`; an adapter with one
+// tile is written at once, the others' tiles leave their sums in slots that
+// adapter_join_kernel adds up.
+struct Grouping {
+  int32_t *rows, *off;  // rows by adapter, their bounds; null: none wanted
+  int4 *tiles;          // (adapter, first row, end, slot or -1); adapter -1 past the last
+  int2 *sums;           // of each adapter: tiles, first slot
+  int most, chunk;      // entries of `tiles`
+};
+
+// Tiles and slots of the adapters, 64 at a time, by one wave: `at` and `m` are the
+// first row and the number of rows of adapter l (m = 0 past the last).
+struct TileMaker {
+  int tiles = 0, slots = 0;
+  __device__ __forceinline__ void add(const Grouping &gr, int l, int L, int at, int m) {
+    const int lane = threadIdx.x & 63;
+    const int n = (m + gr.chunk - 1) / gr.chunk, k = n > 1 ? n : 0;
+    int tn = n, tk = k;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int un = __shfl_up(tn, d, 64), uk = __shfl_up(tk, d, 64);
+      if (lane >= d) {
+        tn += un;
+        tk += uk;
+      }
+    }
+    const int first = tiles + tn - n, slot = slots + tk - k;
+    if (l < L) gr.sums[l] = make_int2(n, slot);
+    for (int i = 0; i < n; ++i) {
+      const int r0 = at + i * gr.chunk, r1 = r0 + gr.chunk;
+      gr.tiles[first + i] = make_int4(l, r0, r1 < at + m ? r1 : at + m, n > 1 ? slot + i : -1);
+    }
+    tiles += __shfl(tn, 63, 64);
+    slots += __shfl(tk, 63, 64);
+  }
+  __device__ __forceinline__ void finish(const Grouping &gr) {
+    for (int i = tiles + (threadIdx.x & 63); i < gr.most; i += 64)
+      gr.tiles[i] = make_int4(-1, 0, 0, -1);
+  }
+};
+
+__global__ void __launch_bounds__(64) adapter_tiles_kernel(Grouping gr, int L) {
+  TileMaker tm;
+  for (int l0 = 0; l0 < L; l0 += 64) {
+    const int l = l0 + threadIdx.x;
+    const int at = l < L ? gr.off[l] : 0;
+    tm.add(gr, l, L, at, l < L ? gr.off[l + 1] - at : 0);
+  }
+  tm.finish(gr);
+}
+
+// Rows by adapter for the outer sums (what launch_group_rows makes), by one block:
+// beside the contraction it takes next to no time of its own, where two launches
+// take 11 us.  Each wave counts and then places a stretch of the rows; `start`, its
+// next row of each id (L: none), holds kShrinkWaves x (L + 1).
+constexpr int64_t kGroupedRows = 8192;  // more would outlast the contraction
+constexpr int kGroupedMost = 1000;      // adapters
+
+__device__ __forceinline__ void group_block(const int32_t *ids, int n, int L, const Grouping &gr,
+                                            int *start) {
+  constexpr int W = kShrinkWaves;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int k = threadIdx.x; k < W * (L + 1); k += 64 * W) start[k] = 0;
+  __syncthreads();
+  int *mine = start + wave * (L + 1);
+  const int per = (n + 64 * W - 1) / (64 * W) * 64;
+  const int i0 = wave * per, i1 = i0 + per < n ? i0 + per : n;
+#pragma unroll 4
+  for (int i = i0 + lane; i < i1; i += 64) {
+    const int l = ids[i];
+    atomicAdd(&mine[l >= 0 && l < L ? l : L], 1);
+  }
+  __syncthreads();
+  if (wave == 0) {  // counts -> first rows
+    int carry = 0;
+    TileMaker tm;
+    for (int l0 = 0; l0 <= L; l0 += 64) {
+      const int l = l0 + lane <= L ? l0 + lane : L;
+      int m[W], all = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        m[w] = start[w * (L + 1) + l];
+        all += m[w];
+      }
+      int inc = l0 + lane <= L ? all : 0;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(inc, d, 64);
+        if (lane >= d) inc += up;
+      }
+      int at = carry + inc - all;
+      tm.add(gr, l0 + lane, L, at, l0 + lane < L ? all : 0);
+      if (l0 + lane <= L) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          start[w * (L + 1) + l] = at;
+          at += m[w];
+        }
+      }
+      carry += __shfl(inc, 63, 64);
+    }
+    tm.finish(gr);
+  }
+  __syncthreads();
+  int next = i0 < i1 ? ids[i0 + lane < i1 ? i0 + lane : i1 - 1] : 0;
+  for (int i = i0 + lane; i - lane < i1; i += 64) {
+    int l = i < i1 ? next : L;
+    if (l < 0 || l >= L) l = L;
+    next = ids[i + 64 < i1 ? i + 64 : i1 - 1];
+    uint64_t same = __ballot(i < i1);  // lanes with the same id
+    for (int bit = 1; bit <= L; bit <<= 1) {
+      const uint64_t set = __ballot((l & bit) != 0);
+      same &= (l & bit) ? set : ~set;
+    }
+    const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+    fence_wave();
+    const int row = mine[l] + rank;
+    fence_wave();
+    if (i < i1) {
+      if (rank == 0) mine[l] = row + __popcll(same);
+      gr.rows[row] = l < L ? i : -1;
+    }
+  }
+}
+
+// gridDim.y counts the shares of a chunk, and one more where `gr` is wanted: its
+// first block groups the rows.
 template <int RT, bool LONG>
 __global__ void __launch_bounds__(64 * kShrinkWaves)
     adapter_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx,
                           const int32_t *__restrict__ ids, const uint16_t *__restrict__ w,
                           const float *__restrict__ scale, float *__restrict__ u,
-                          uint16_t *__restrict__ parts, int64_t T, int64_t C, int r, int L) {
+                          uint16_t *__restrict__ parts, int64_t T, int64_t C, int r, int L,
+                          Grouping gr) {
   __shared__ Plan plan;
   __shared__ ShrinkLds<RT> lds;
+  int shares = gridDim.y, share = blockIdx.y;
+  if (gr.rows) {  // dispatched first, as it takes longest
+    if (share == 0) {
+      static_assert(sizeof(lds) >= 4 * kShrinkWaves * (kGroupedMost + 1), "room for the counts");
+      if (blockIdx.x == 0) group_block(ids, (int)T, L, gr, reinterpret_cast<int *>(&lds));
+      return;
+    }
+    --shares;
+    --share;
+  }
   const int64_t t0 = (int64_t)blockIdx.x * kChunk;
   make_plan(plan, ids, t0, T, L);
-  const int lo = (int)((int64_t)plan.tiles * blockIdx.y / gridDim.y);
-  const int hi = (int)((int64_t)plan.tiles * (blockIdx.y + 1) / gridDim.y);
+  const int lo = (int)((int64_t)plan.tiles * share / shares);
+  const int hi = (int)((int64_t)plan.tiles * (share + 1) / shares);
   for (int i = lo; i < hi; ++i)
     contract_tile<RT, (RT == 1 ? 4 : RT == 2 ? 2 : 1), LONG>(
         lds, plan, i, t0, x, ldx, w, scale, C, r, L,
@@ -574,57 +712,8 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
 }
 
 // ---------------------------------------------------------------------------
-// outer: d_l[j][c] = s_l sum over the rows t of adapter l of w_t[j] y_t[c].  Rows are
-// sorted by adapter and cut into tiles of `chunk`; an adapter with one tile is
-// written at once, the others' tiles leave their sums in slots that
-// adapter_join_kernel adds up.
-
-// Tile of an adapter's rows: which adapter, its rows, how many tiles it has and
-// the slot of its first one (slots count the tiles of adapters with several).
-struct Tile {
-  int l, r0, r1, tiles, slot;
-};
-
-// The idx-th tile; false past the last.  By whole waves.
-__device__ __forceinline__ bool find_tile(const int32_t *off, int L, int chunk, int64_t idx,
-                                          Tile &t) {
-  const int lane = threadIdx.x & 63;
-  int64_t before = 0;
-  int slots = 0;
-  for (int l0 = 0; l0 < L; l0 += 64) {
-    int a = 0, b = 0;
-    if (l0 + lane < L) {
-      a = off[l0 + lane];
-      b = off[l0 + lane + 1];
-    }
-    const int n = (b - a + chunk - 1) / chunk, m = n > 1 ? n : 0;
-    int sum = n, msum = m;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(sum, o, 64), k = __shfl_up(msum, o, 64);
-      if (lane >= o) {
-        sum += v;
-        msum += k;
-      }
-    }
-    const int total = __shfl(sum, 63, 64);
-    if (idx < before + total) {
-      const uint64_t past = __ballot(before + sum > idx);
-      const int at = __ffsll((unsigned long long)past) - 1;
-      const int i = (int)(idx - before) - __shfl(sum - n, at, 64);
-      t.l = l0 + at;
-      t.r0 = __shfl(a, at, 64) + i * chunk;
-      const int end = __shfl(b, at, 64);
-      t.r1 = t.r0 + chunk < end ? t.r0 + chunk : end;
-      t.tiles = __shfl(n, at, 64);
-      t.slot = slots + __shfl(msum - m, at, 64) + i;
-      return true;
-    }
-    before += total;
-    slots += __shfl(msum, 63, 64);
-  }
-  return false;
-}
+// outer: d_l[j][c] = s_l sum over the rows t of adapter l of w_t[j] y_t[c], tile by
+// tile.
 
 // One side of the gradient: d += w y'.
 struct Side {
@@ -653,12 +742,12 @@ struct Step {
 };
 
 template <int RT, bool F8, bool LONG>
-__device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, const Tile &tile,
+__device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, int r0, int r1,
                                            float s, int64_t c0, int j0, int r, float *out) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int64_t c = c0 + 8 * (lane & 15), C = sd.C;
   const bool edge = c0 + 128 > C;
-  const int last = rows[tile.r1 - 1];
+  const int last = rows[r1 - 1];
   struct Rows {
     int t[8];
   };
@@ -671,7 +760,7 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
   auto fetch = [&](int i0, const Rows &q, Step<RT, F8> &st) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int64_t t = i0 + 8 * g + k < tile.r1 ? q.t[k] : last;
+      const int64_t t = i0 + 8 * g + k < r1 ? q.t[k] : last;
       if (F8) {
         uint2 v;
         const int64_t at = c < C ? c : 0;  // columns past C are not stored
@@ -695,13 +784,13 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[q][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   Step<RT, F8> cur, next;
-  Rows ahead = rows_of(tile.r0);
-  fetch(tile.r0, ahead, cur);
-  if (tile.r0 + 32 < tile.r1) ahead = rows_of(tile.r0 + 32);
-  for (int i0 = tile.r0; i0 < tile.r1; i0 += 32) {
-    if (i0 + 32 < tile.r1) {
+  Rows ahead = rows_of(r0);
+  fetch(r0, ahead, cur);
+  if (r0 + 32 < r1) ahead = rows_of(r0 + 32);
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    if (i0 + 32 < r1) {
       fetch(i0 + 32, ahead, next);
-      if (i0 + 64 < tile.r1) ahead = rows_of(i0 + 64);
+      if (i0 + 64 < r1) ahead = rows_of(i0 + 64);
     }
     __builtin_amdgcn_sched_barrier(0);
     uint4 y[8], f[8];
@@ -724,10 +813,10 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
         y[k] = words(h);
       }
     }
-    if (i0 + 32 > tile.r1) {  // rows past the tile's end: zeros on both sides
+    if (i0 + 32 > r1) {  // rows past the tile's end: zeros on both sides
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (i0 + 8 * g + k >= tile.r1) {
+        if (i0 + 8 * g + k >= r1) {
           y[k] = make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int q = 0; q < RT; ++q) cur.w[q][k] = 0.0f;
@@ -767,46 +856,67 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
 template <int RT, bool F8, bool LONG>
 __global__ void __launch_bounds__(256)
     adapter_outer_kernel(Side first, Side second, int split, const int32_t *__restrict__ rows,
-                         const int32_t *__restrict__ off, const float *__restrict__ scale, int r,
-                         int L, int chunk) {
+                         const int4 *__restrict__ tiles, int most,
+                         const float *__restrict__ scale, int r) {
   const bool two = (int)blockIdx.x >= split;
   const int wave = threadIdx.x >> 6;
   const Side &sd = two ? second : first;
   const int64_t c0 = ((int64_t)(two ? blockIdx.x - split : blockIdx.x) * 4 + wave) * 128;
   if (c0 >= sd.C) return;
-  for (int64_t idx = blockIdx.y;; idx += gridDim.y) {
-    Tile t;
-    if (!find_tile(off, L, chunk, idx, t)) return;
-    const bool whole = t.tiles == 1;
-    const float s = scale ? scale[t.l] : 1.0f;
-    float *out = whole ? sd.d + (int64_t)t.l * r * sd.C : sd.slot + (int64_t)t.slot * r * sd.C;
+  for (int i = blockIdx.y; i < most; i += gridDim.y) {
+    const int4 t = tiles[i];
+    if (t.x < 0) return;
+    const float s = scale ? scale[t.x] : 1.0f;
+    float *out = t.w < 0 ? sd.d + (int64_t)t.x * r * sd.C : sd.slot + (int64_t)t.w * r * sd.C;
     const int j0 = blockIdx.z * RT * 16;
-    if (two || !F8) outer_tile<RT, false, LONG>(sd, rows, t, s, c0, j0, r, out);
-    else outer_tile<RT, F8, LONG>(sd, rows, t, s, c0, j0, r, out);
+    if (two || !F8) outer_tile<RT, false, LONG>(sd, rows, t.y, t.z, s, c0, j0, r, out);
+    else outer_tile<RT, F8, LONG>(sd, rows, t.y, t.z, s, c0, j0, r, out);
   }
 }
 
-// The sums of adapters with several tiles, and zeros for those without rows.
+// The sums of adapters with several tiles, and zeros for those without rows.  A
+// thread has four neighbours (the last ones end with the matrix) of eight slots at
+// a time, without a choice between the loads; blockIdx.y and gridDim.y deal out
+// the adapters.  8192 rows in 20 slots of 32 x 8192: 5.3 us (17 us with branches).
 __global__ void __launch_bounds__(256)
-    adapter_join_kernel(Side first, Side second, int split, const int32_t *__restrict__ off, int r,
-                        int L, int chunk) {
+    adapter_join_kernel(Side first, Side second, int split, const int2 *__restrict__ sums, int r,
+                        int L) {
+  constexpr int V = 4, IN_FLIGHT = 8;
   const bool two = (int)blockIdx.x >= split;
-  const Side &sd = two ? second : first;
-  const int64_t n = (int64_t)r * sd.C;
-  const int64_t i0 = (int64_t)(two ? blockIdx.x - split : blockIdx.x) * 256 + threadIdx.x;
-  const int64_t step = (int64_t)(two ? gridDim.x - split : split) * 256;
-  int slot = 0;
-  for (int l = 0; l < L; ++l) {
-    const int tiles = (off[l + 1] - off[l] + chunk - 1) / chunk;
-    if (tiles != 1 && (int)blockIdx.y == l % (int)gridDim.y) {
-      for (int64_t i = i0; i < n; i += step) {
-        float s = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < tiles; ++k) s += sd.slot[(int64_t)(slot + k) * n + i];
-        sd.d[(int64_t)l * n + i] = s;
+  const int64_t n = (int64_t)r * (two ? second.C : first.C);
+  const float *slots = two ? second.slot : first.slot;
+  float *d = two ? second.d : first.d;
+  const int64_t i0 = V * ((int64_t)((int)blockIdx.x - (two ? split : 0)) * 256 + threadIdx.x);
+  const int64_t step = (int64_t)(two ? gridDim.x - split : split) * 256 * V;
+  for (int l = blockIdx.y; l < L; l += gridDim.y) {
+    const int2 e = sums[l];
+    const int tiles = e.x;
+    if (tiles == 1) continue;
+    if (n < V) {
+      for (int64_t i = i0 / V; i < n; i += step / V) {
+        float sum = 0.0f;
+        for (int k = 0; k < tiles; ++k) sum += slots[(e.y + k) * n + i];
+        d[l * n + i] = sum;
       }
+      continue;
     }
-    if (tiles > 1) slot += tiles;
+    for (int64_t i = i0; i < n; i += step) {
+      float s[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] = 0.0f;
+      const float *at = slots + e.y * n + (i + V <= n ? i : n - V);
+      for (int k0 = 0; k0 < tiles; k0 += IN_FLIGHT) {
+        float v[IN_FLIGHT][V];
+#pragma unroll
+        for (int k = 0; k < IN_FLIGHT; ++k)
+          __builtin_memcpy(v[k], at + (k0 + k < tiles ? k0 + k : tiles - 1) * n, 4 * V);
+#pragma unroll
+        for (int k = 0; k < IN_FLIGHT; ++k)
+#pragma unroll
+          for (int j = 0; j < V; ++j) s[j] += k0 + k < tiles ? v[k][j] : 0.0f;
+      }
+      __builtin_memcpy(d + l * n + (i + V <= n ? i : n - V), s, 4 * V);
+    }
   }
 }
 
@@ -832,12 +942,12 @@ unsigned tile_shares(int64_t T, int L, int64_t blocks, int64_t want) {
 
 hipError_t shrink(const uint16_t *x, int64_t ldx, const int32_t *ids, const uint16_t *w,
                   const float *scale, float *u, uint16_t *parts, int64_t T, int64_t C, int r,
-                  int L, hipStream_t s) {
+                  int L, const Grouping &gr, hipStream_t s) {
   const int64_t chunks = (T + kChunk - 1) / kChunk;
-  const dim3 grid((unsigned)chunks, tile_shares(T, L, chunks, 256));
+  const dim3 grid((unsigned)chunks, tile_shares(T, L, chunks, 256) + (gr.rows ? 1 : 0));
 #define BNN_SHRINK_AS(RT, LONG)                                                                 \
   adapter_shrink_kernel<RT, LONG><<<grid, 64 * kShrinkWaves, 0, s>>>(x, ldx, ids, w, scale, u,  \
-                                                                     parts, T, C, r, L)
+                                                                     parts, T, C, r, L, gr)
 #define BNN_SHRINK(RT)                    \
   do {                                    \
     if (C >= 8) BNN_SHRINK_AS(RT, true);  \
@@ -899,25 +1009,32 @@ hipError_t expand_as(int dtype, const uint16_t *parts, const int32_t *ids, const
   return expand<bf16_t>(parts, ids, w, base, ldb, out, ldo, T, C, r, L, s);
 }
 
-// Rows of a tile of the outer sums: few enough tiles that the slots stay small.
+// Rows of a tile of the outer sums: about 16 tiles, which with the columns' blocks
+// fill the chip (8192 rows, rank 32, 2 x 4096 columns: 37 us of 512 each, 43 of 256;
+// 1024 rows, rank 16: 10.6 us of 128, 13.2 of 256), and at most 64.
 int64_t outer_chunk(int64_t T) {
-  const int64_t c = ((T + 63) / 64 + 31) / 32 * 32;
-  return c < 256 ? 256 : c;
+  int64_t c = (T + 15) / 16;
+  c = c < 128 ? 128 : c > 512 ? 512 : c;
+  if (c < (T + 63) / 64) c = (T + 63) / 64;
+  return (c + 31) / 32 * 32;
 }
 
 struct BwdLayout {
-  int64_t v, parts, rows, off, group, slot_a, slot_b, bytes, chunk;
+  int64_t v, parts, rows, off, tiles, sums, group, slot_a, slot_b, bytes, chunk, most;
 };
 
 BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
   BwdLayout b;
   b.chunk = outer_chunk(T);
+  b.most = (T < L ? T : L) + T / b.chunk;
   const int64_t slots = T <= b.chunk ? 0 : 2 * (T / b.chunk);
   b.v = 0;
   b.parts = b.v + align16(T * r * 4);
   b.rows = b.parts + parts_bytes(T, r);
   b.off = b.rows + align16(T * 4 + 256);  // read a step past a tile's end
-  b.group = b.off + align16((L + 1) * 4);
+  b.tiles = b.off + align16((L + 1) * 4);
+  b.sums = b.tiles + b.most * 16;
+  b.group = b.sums + align16(L * 8);
   b.slot_a = b.group + align16(group_rows_workspace(T, L));
   b.slot_b = b.slot_a + align16(slots * r * K * 4);
   b.bytes = b.slot_b + align16(slots * r * N * 4);
@@ -968,7 +1085,8 @@ hipError_t launch_adapter_fwd(const uint16_t *x, int64_t ldx, const int32_t *ids
     return small<bf16_t>(x, ldx, ids, a, b, scale, base, ldb, out, ldo, u, T, K, N, r, L, s);
   }
   uint16_t *parts = static_cast<uint16_t *>(workspace);
-  const hipError_t e = shrink(x, ldx, ids, a, scale, u, N > 0 ? parts : nullptr, T, K, r, L, s);
+  const hipError_t e = shrink(x, ldx, ids, a, scale, u, N > 0 ? parts : nullptr, T, K, r, L,
+                              Grouping{}, s);
   if (e != hipSuccess || N == 0) return e;
   return expand_as(dtype, parts, ids, b, base, ldb, out, ldo, T, N, r, L, s);
 }
@@ -982,12 +1100,16 @@ hipError_t launch_adapter_bwd(const AdapterGrad &q, void *workspace, int64_t T, 
   const BwdLayout b = bwd_layout(T, K, N, r, L);
   char *ws = static_cast<char *>(workspace);
   float *v = reinterpret_cast<float *>(ws + b.v);
-  int32_t *rows = reinterpret_cast<int32_t *>(ws + b.rows);
-  int32_t *off = reinterpret_cast<int32_t *>(ws + b.off);
+  const Grouping gr = {reinterpret_cast<int32_t *>(ws + b.rows),
+                       reinterpret_cast<int32_t *>(ws + b.off),
+                       reinterpret_cast<int4 *>(ws + b.tiles),
+                       reinterpret_cast<int2 *>(ws + b.sums), (int)b.most, (int)b.chunk};
   uint16_t *parts = reinterpret_cast<uint16_t *>(ws + b.parts);
+  const bool beside = q.sums && T > 0 && T <= kGroupedRows && L <= kGroupedMost;
   hipError_t e = hipSuccess;
   if (T > 0) {
-    e = shrink(q.dy, q.lddy, q.ids, q.b, q.scale, v, q.dx ? parts : nullptr, T, N, r, L, s);
+    e = shrink(q.dy, q.lddy, q.ids, q.b, q.scale, v, q.dx ? parts : nullptr, T, N, r, L,
+               beside ? gr : Grouping{}, s);
     if (e != hipSuccess) return e;
     if (q.dx) {
       e = expand_as(q.dtype, parts, q.ids, q.a, q.base, q.ldb, q.dx, q.lddx, T, K, r, L, s);
@@ -995,18 +1117,22 @@ hipError_t launch_adapter_bwd(const AdapterGrad &q, void *workspace, int64_t T, 
     }
   }
   if (!q.sums) return hipSuccess;
-  e = launch_group_rows(q.ids, rows, off, ws + b.group, T, L, s);
-  if (e != hipSuccess) return e;
+  if (!beside) {
+    e = launch_group_rows(q.ids, gr.rows, gr.off, ws + b.group, T, L, s);
+    if (e != hipSuccess) return e;
+    adapter_tiles_kernel<<<1, 64, 0, s>>>(gr, L);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const Side sa = {v, q.x, q.xs, q.ldx, K, q.da, reinterpret_cast<float *>(ws + b.slot_a)};
   const Side sb = {q.u, q.dy, nullptr, q.lddy, N, q.db, reinterpret_cast<float *>(ws + b.slot_b)};
   const int split = (int)((K + 511) / 512), cols = split + (int)((N + 511) / 512);
-  const int64_t most = (T < L ? T : L) + T / b.chunk;
-  if (most > 0) {
-    const unsigned ty = (unsigned)(most < 65535 ? most : 65535);
+  if (b.most > 0) {
+    const unsigned ty = (unsigned)(b.most < 65535 ? b.most : 65535);
 #define BNN_OUTER(RT, F8, LONG)                                                                  \
   adapter_outer_kernel<RT, F8, LONG>                                                             \
-      <<<dim3(cols, ty, (r + RT * 16 - 1) / (RT * 16)), 256, 0, s>>>(sa, sb, split, rows, off,   \
-                                                                     q.scale, r, L, (int)b.chunk)
+      <<<dim3(cols, ty, (r + RT * 16 - 1) / (RT * 16)), 256, 0, s>>>(sa, sb, split, gr.rows,     \
+                                                                     gr.tiles, gr.most, q.scale, r)
 #define BNN_OUTER_AS(RT)                                             \
   do {                                                               \
     if ((K < 8 && K > 0) || (N < 8 && N > 0)) {                      \
@@ -1024,10 +1150,10 @@ hipError_t launch_adapter_bwd(const AdapterGrad &q, void *workspace, int64_t T, 
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int64_t na = ((int64_t)r * K + 255) / 256, nb = ((int64_t)r * N + 255) / 256;
+  const int64_t na = ((int64_t)r * K + 1023) / 1024, nb = ((int64_t)r * N + 1023) / 1024;
   const int ja = (int)(na < 1024 ? na : 1024), jb = (int)(nb < 1024 ? nb : 1024);
-  adapter_join_kernel<<<dim3(ja + jb, L < 16 ? L : 16), 256, 0, s>>>(sa, sb, ja, off, r, L,
-                                                                     (int)b.chunk);
+  adapter_join_kernel<<<dim3(ja + jb, L < 16 ? L : 16), 256, 0, s>>>(sa, sb, ja, gr.sums, r,
+                                                                     L);
   return hipGetLastError();
 }
 
