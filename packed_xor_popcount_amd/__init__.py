@@ -624,12 +624,21 @@ def _call(name: str, t: torch.Tensor, *args) -> None:
 
 def _matrix(name: str, t, shape, dtype, device) -> None:
     _need_cuda(name, t)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
+def _new(rows: int, cols: int, dtype, device):
+    # a third of a microsecond less than torch.empty
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _new_vector(n: int, dtype, device):
+    return torch.empty_strided((n,), (1,), dtype=dtype, device=device)
+
+
 def _workspace(need: int, device):
-    return torch.empty((need,), dtype=torch.uint8, device=device) if need > 0 else None
+    return torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device) if need > 0 else None
 
 
 class Routing(NamedTuple):
@@ -664,13 +673,13 @@ def route_fwd(logits, k, valid=None, normalise=True, loss=True) -> Routing:
             raise ValueError(f"valid must be a contiguous bool or uint8 tensor of shape ({T},) on {dev}")
     if not (1 <= k <= E <= 1024 and k <= 32):
         raise BnnError(2, "bnn_route_fwd")
-    experts, place = torch.empty((2, T, k), dtype=torch.int32, device=dev).unbind(0)
-    rows, offsets, counts = torch.empty((T * k + 2 * E + 1,), dtype=torch.int32, device=dev).split((T * k, E + 1, E))
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    stats = torch.empty((T, 2), dtype=torch.float32, device=dev)
+    i32, f32 = torch.int32, torch.float32
+    experts, place, weights = _new(T, k, i32, dev), _new(T, k, i32, dev), _new(T, k, f32, dev)
+    rows, offsets, counts = _new_vector(T * k, i32, dev), _new_vector(E + 1, i32, dev), _new_vector(E, i32, dev)
+    stats = _new(T, 2, f32, dev)
     slope = total = None
     if loss:
-        slope, total = torch.empty((E + 1,), dtype=torch.float32, device=dev).split((E, 1))
+        slope, total = _new_vector(E, f32, dev), _new_vector(1, f32, dev)
     need = library().bnn_route_fwd_workspace(T, E, k)
     ws = _workspace(need, dev)
     _call("bnn_route_fwd", logits, _ptr(logits), dt, ldz, _ptr(valid), _ptr(experts), _ptr(weights), _ptr(place),
@@ -699,7 +708,7 @@ def route_bwd(logits, experts, weights, stats, slope=None, dweights=None, dloss=
         _need_cuda("dloss", dloss)
         if dloss.dtype != torch.float32 or dloss.numel() != 1 or dloss.device != dev:
             raise ValueError(f"dloss must be a float32 tensor of one element on {dev}")
-    dz = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    dz = _new(T, E, logits.dtype, dev)
     _call("bnn_route_bwd", logits, _ptr(logits), dt, ldz, _ptr(experts), _ptr(weights), _ptr(stats),
           None if dloss is None else _ptr(slope), _ptr(dweights), _ptr(dloss), _ptr(dz), max(E, 1), T, E, k,
           int(bool(normalise)))
@@ -767,7 +776,7 @@ def combine_bwd(dout, place, weights=None, y=None, rows=None, dtype=None):
     if data is not None and data.device != dev:
         raise ValueError(f"y must be on {dev}")
     dy, dtd = _real_out(R, N, dout.dtype if dtype is None else dtype, dev, None)
-    dw = None if y is None else torch.empty((T, k), dtype=torch.float32, device=dev)
+    dw = None if y is None else _new(T, k, torch.float32, dev)
     _call("bnn_combine_bwd", dout, _ptr(dout), dt, lddo, _ptr(data), _ptr(ys), dty, ldy, R, _ptr(place), _ptr(weights),
           _ptr(dy), dtd, max(N, 1), _ptr(dw), T, N, k)
     return dy, dw
@@ -827,7 +836,7 @@ def adapter_fwd(x, ids, a, b, scale=None, base=None, dtype=None, out=None):
         dtype = out.dtype if out is not None else base.dtype if base is not None else torch.float32
     out, dt, ldo = _rows_out("out", out, T, N, dtype, dev)
     ldb = _same_rows("base", base, T, N, dt, dev) if base is not None else 0
-    u = torch.empty((T, r), dtype=torch.float32, device=dev)
+    u = _new(T, r, torch.float32, dev)
     need = library().bnn_adapter_fwd_workspace(T, K, N, r, L)
     ws = _workspace(need, dev)
     _call("bnn_adapter_fwd", x, _ptr(x), ldx, _ptr(ids), _ptr(a), _ptr(b), _ptr(scale), _ptr(base), ldb, _ptr(out),
