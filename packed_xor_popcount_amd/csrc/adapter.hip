@@ -215,15 +215,74 @@ union ShrinkLds {
   v4f join[kShrinkWaves][kJoined<RT>][64];
 };
 
-// Sums of tile i by all eight waves.  done(j, t, s, sum) is called with the sums of
-// ranks j .. j + 3 of row t (zeros past r) by the lanes that hold them; the block is
+// The columns past the last whole step.
+template <int RT, bool LONG>
+__device__ __forceinline__ void last_columns(StepRows &buf, const uint16_t *const (&xr)[4],
+                                             const uint16_t *const (&wr)[RT][4], int64_t st,
+                                             int64_t C, v4f (&acc)[RT]) {
+  const int lane = threadIdx.x & 63;
+  const int c = (int)(st * 128) + 8 * (lane & 15);
+  Chunk<bf16_t> xc[4], wc[RT][4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    xc[m] = raw8<LONG>(xr[m], c, C);
+#pragma unroll
+    for (int q = 0; q < RT; ++q) wc[q][m] = raw8<LONG>(wr[q][m], c, C);
+  }
+  uint4 xv[4], wv[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    settle_chunk(xc[m], c, (int)C);
+    xv[m] = words(xc[m]);
+  }
+  to_operands(buf, xv);
+#pragma unroll
+  for (int q = 0; q < RT; ++q) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      settle_chunk(wc[q][m], c, (int)C);
+      wv[m] = words(wc[q][m]);
+    }
+    to_operands(buf, wv);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) acc[q] = mfma(wv[m], xv[m], acc[q]);
+  }
+}
+
+// The waves' sums of a tile.  done(j, t, s, sum) is called with the sums of ranks
+// j .. j + 3 of row t (zeros past r) by the lanes that hold them; the block is
 // synchronised afterwards.
+template <int RT, typename Done>
+__device__ __forceinline__ void join_tile(ShrinkLds<RT> &lds, const v4f (&acc)[RT], int64_t t,
+                                          bool mine, float s, int r, Done done) {
+  constexpr int JT = kJoined<RT>;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+#pragma unroll
+  for (int q0 = 0; q0 < RT; q0 += JT) {
+    __syncthreads();  // rows and sums before have been read
+#pragma unroll
+    for (int q = 0; q < JT; ++q) lds.join[wave][q][lane] = acc[q0 + q];
+    __syncthreads();
+    if (wave < JT && mine) {
+      v4f sum = lds.join[0][wave][lane];
+#pragma unroll
+      for (int k = 1; k < kShrinkWaves; ++k) sum += lds.join[k][wave][lane];
+      const int j = 16 * (q0 + wave) + 4 * g;
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (j + v >= r) sum[v] = 0.0f;  // rank r - 1 again
+      done(j, t, s, sum);
+    }
+  }
+  __syncthreads();  // the sums have been read
+}
+
+// Sums of tile i by all eight waves, up to STEPS of a wave's steps in flight.
 template <int RT, int STEPS, bool LONG, typename Done>
 __device__ __forceinline__ void contract_tile(ShrinkLds<RT> &lds, const Plan &plan, int i,
                                               int64_t t0, const uint16_t *x, int64_t ldx,
                                               const uint16_t *w, const float *scale, int64_t C,
                                               int r, int L, Done done) {
-  constexpr int JT = kJoined<RT>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
   const int64_t steps = (C + 127) / 128, whole = C / 128;
   const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
@@ -273,54 +332,9 @@ __device__ __forceinline__ void contract_tile(ShrinkLds<RT> &lds, const Plan &pl
       several(std::integral_constant<int, STEPS>());
     if (STEPS > 1)
       while (st < whole) several(std::integral_constant<int, 1>());
-    if (st < steps) {  // the last columns
-      const int c = (int)(st * 128) + 8 * (lane & 15);
-      Chunk<bf16_t> xc[4], wc[RT][4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        xc[m] = raw8<LONG>(xr[m], c, C);
-#pragma unroll
-        for (int q = 0; q < RT; ++q) wc[q][m] = raw8<LONG>(wr[q][m], c, C);
-      }
-      uint4 xv[4], wv[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        settle_chunk(xc[m], c, (int)C);
-        xv[m] = words(xc[m]);
-      }
-      to_operands(lds.rows[wave], xv);
-#pragma unroll
-      for (int q = 0; q < RT; ++q) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          settle_chunk(wc[q][m], c, (int)C);
-          wv[m] = words(wc[q][m]);
-        }
-        to_operands(lds.rows[wave], wv);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) acc[q] = mfma(wv[m], xv[m], acc[q]);
-      }
-    }
+    if (st < steps) last_columns<RT, LONG>(lds.rows[wave], xr, wr, st, C, acc);
   }
-  const float s = l < L && scale ? scale[l] : 1.0f;
-#pragma unroll
-  for (int q0 = 0; q0 < RT; q0 += JT) {
-    __syncthreads();  // rows and sums before have been read
-#pragma unroll
-    for (int q = 0; q < JT; ++q) lds.join[wave][q][lane] = acc[q0 + q];
-    __syncthreads();
-    if (wave < JT && mine) {
-      v4f sum = lds.join[0][wave][lane];
-#pragma unroll
-      for (int k = 1; k < kShrinkWaves; ++k) sum += lds.join[k][wave][lane];
-      const int j = 16 * (q0 + wave) + 4 * g;
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (j + v >= r) sum[v] = 0.0f;  // rank r - 1 again
-      done(j, t, s, sum);
-    }
-  }
-  __syncthreads();  // the sums have been read
+  join_tile<RT>(lds, acc, t, mine, l < L && scale ? scale[l] : 1.0f, r, done);
 }
 
 // The parts of s sum in a row of parts, from rank j on.
@@ -594,7 +608,7 @@ __device__ __forceinline__ void finish_tile(const Plan &plan, int s0, int len, b
 }
 
 template <typename O, int RP, bool LONG>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, RP <= 2 && sizeof(O) == 2 ? 3 : 1)
     adapter_expand_kernel(const uint16_t *__restrict__ parts, const int32_t *__restrict__ ids,
                           const uint16_t *__restrict__ w, const O *base, int64_t ldb, O *out,
                           int64_t ldo, int64_t T, int64_t C, int r, int L) {
