@@ -165,11 +165,19 @@ def test_bwd(T, K, N, r, L, ids):
 
 
 @pytest.mark.parametrize("T,L,ids", [(3000, 3, "sorted"), (3000, 1, "one"), (2600, 600, "mixed"), (9000, 5, "runs"),
-                                     (20000, 2, "mixed")])
+                                     (20000, 2, "mixed"), (300, 1010, "mixed"), (9000, 700, "mixed"), (8192, 1000, "runs"),
+                                     (8193, 1, "one")])
 def test_bwd_of_many_rows(T, L, ids):
     """Adapters whose rows are cut into several tiles, and many adapters."""
     for kept in ("bf16", "f8"):
         check_bwd(Case(T, T, 200, 136, 20, L, ids), kept)
+
+
+@pytest.mark.parametrize("T", [255, 256, 257, 512])
+@pytest.mark.parametrize("N,r,L", [(300, 16, 40), (1030, 32, 2), (2100, 33, 3), (9000, 16, 250)])
+def test_chunk_ends_and_the_choice_of_kernels(T, N, r, L):
+    for ids in ("mixed", "sorted"):
+        check_fwd(Case(T + N, T, 260, N, r, L, ids))
 
 
 def test_order_of_rows_does_not_matter_to_a_row():
