@@ -608,7 +608,7 @@ __device__ __forceinline__ void finish_tile(const Plan &plan, int s0, int len, b
 }
 
 template <typename O, int RP, bool LONG>
-__global__ void __launch_bounds__(256, RP <= 2 && sizeof(O) == 2 ? 3 : 1)
+__global__ void __launch_bounds__(256, RP <= 2 ? (sizeof(O) == 2 ? 3 : 2) : RP == 4 ? 2 : 1)
     adapter_expand_kernel(const uint16_t *__restrict__ parts, const int32_t *__restrict__ ids,
                           const uint16_t *__restrict__ w, const O *base, int64_t ldb, O *out,
                           int64_t ldo, int64_t T, int64_t C, int r, int L) {
@@ -672,8 +672,11 @@ __global__ void __launch_bounds__(256, RP <= 2 && sizeof(O) == 2 ? 3 : 1)
 
 // Few rows: both products in one launch.  Every block of 1024 columns sums u
 // again for its tiles, from the caches, which costs less than a second launch
-// waiting for the first (32 rows on 24 adapters, 4096 x 4096 rank 16: FUSED us,
-// the two kernels 12.4 us and a launch's 3.5 us on the host).
+// waiting for the first: 32 rows on 24 adapters, 4096 x 4096 rank 16, 10.3 us (the
+// two kernels 7.2 + 5.2 us, and 3.5 us more on the host); one row 8.6 us from HBM,
+// 5.3 from the caches.  Bound by the chain ids -> plan -> columns -> join -> factor.
+// More steps in flight, or the factor asked for ahead of the sums, need registers
+// that are not there (12.7 us with spills).
 template <typename O, int RT, bool LONG>
 __global__ void __launch_bounds__(64 * kShrinkWaves)
     adapter_small_kernel(const uint16_t *__restrict__ x, int64_t ldx,
@@ -697,17 +700,15 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
     const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
     const int l = plan.id(s0);
     const bool has = l < L, mine = c0 < N && (has || base != out);
-    Factor<RT, LONG> w8;
     Chunk<O> bs[4];
     if (mine) {  // under way during the first product
-      if (has) w8.load(b + (int64_t)l * r * N, 0, c, N, r, g);
       if (base) {
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           bs[v] = raw8<LONG>(base + (int64_t)plan.place(s0, len, 4 * g + v) * ldb, c, N);
       }
     }
-    contract_tile<RT, (RT == 1 ? 2 : 1), LONG>(lds, plan, i, 0, x, ldx, a, scale, K, r, L,
+    contract_tile<RT, 1, LONG>(lds, plan, i, 0, x, ldx, a, scale, K, r, L,
                                                [&](int j, int64_t t, float s, const v4f &sum) {
                                                  if (blockIdx.x == 0)
                                                    store_sums(u + t * r, j, r, sum);
@@ -718,6 +719,8 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
     rp.load(parts[lane & 15], g);
     uint4 f[operands(RT)][8];
     if (has) {
+      Factor<RT, LONG> w8;
+      w8.load(b + (int64_t)l * r * N, 0, c, N, r, g);
       w8.operand(0, c, N, r, g, edge, f[0]);
     }
     finish_tile<O, RT, LONG>(plan, s0, len, has, rp, f, bs, base != nullptr, out, ldo, 0, c, N,
