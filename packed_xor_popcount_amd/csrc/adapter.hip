@@ -222,30 +222,37 @@ __device__ __forceinline__ void last_columns(StepRows &buf, const uint16_t *cons
                                              int64_t C, v4f (&acc)[RT]) {
   const int lane = threadIdx.x & 63;
   const int c = (int)(st * 128) + 8 * (lane & 15);
-  Chunk<bf16_t> xc[4], wc[RT][4];
+  uint4 xv[4];
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    xc[m] = raw8<LONG>(xr[m], c, C);
-#pragma unroll
-    for (int q = 0; q < RT; ++q) wc[q][m] = raw8<LONG>(wr[q][m], c, C);
-  }
-  uint4 xv[4], wv[4];
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    settle_chunk(xc[m], c, (int)C);
-    xv[m] = words(xc[m]);
-  }
-  to_operands(buf, xv);
-#pragma unroll
-  for (int q = 0; q < RT; ++q) {
+  for (int q0 = 0; q0 < RT; q0 += kJoined<RT>) {
+    Chunk<bf16_t> xc[4], wc[kJoined<RT>][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      settle_chunk(wc[q][m], c, (int)C);
-      wv[m] = words(wc[q][m]);
-    }
-    to_operands(buf, wv);
+      if (q0 == 0) xc[m] = raw8<LONG>(xr[m], c, C);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) acc[q] = mfma(wv[m], xv[m], acc[q]);
+      for (int q = 0; q < kJoined<RT>; ++q) wc[q][m] = raw8<LONG>(wr[q0 + q][m], c, C);
+    }
+    if (q0 == 0) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        settle_chunk(xc[m], c, (int)C);
+        xv[m] = words(xc[m]);
+      }
+      to_operands(buf, xv);
+    }
+#pragma unroll
+    for (int q = 0; q < kJoined<RT>; ++q) {
+      uint4 wv[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        settle_chunk(wc[q][m], c, (int)C);
+        wv[m] = words(wc[q][m]);
+      }
+      to_operands(buf, wv);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) acc[q0 + q] = mfma(wv[m], xv[m], acc[q0 + q]);
+    }
+    if (RT > 4) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -304,27 +311,33 @@ __device__ __forceinline__ void contract_tile(ShrinkLds<RT> &lds, const Plan &pl
       }
     }
     int64_t st = wave;
-    auto several = [&](auto n) {  // n steps, all their loads in flight
-      uint4 xv[n][4], wv[n][RT][4];
+    auto several = [&](auto n) {  // n steps, the loads of up to four rank tiles in flight
+      uint4 xv[n][4];
 #pragma unroll
-      for (int k = 0; k < n; ++k) {
-        const int64_t c = (st + k * kShrinkWaves) * 128 + 8 * (lane & 15);
+      for (int q0 = 0; q0 < RT; q0 += kJoined<RT>) {
+        uint4 wv[n][kJoined<RT>][4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          __builtin_memcpy(&xv[k][m], xr[m] + c, 16);
+        for (int k = 0; k < n; ++k) {
+          const int64_t c = (st + k * kShrinkWaves) * 128 + 8 * (lane & 15);
 #pragma unroll
-          for (int q = 0; q < RT; ++q) __builtin_memcpy(&wv[k][q][m], wr[q][m] + c, 16);
+          for (int m = 0; m < 4; ++m) {
+            if (q0 == 0) __builtin_memcpy(&xv[k][m], xr[m] + c, 16);
+#pragma unroll
+            for (int q = 0; q < kJoined<RT>; ++q)
+              __builtin_memcpy(&wv[k][q][m], wr[q0 + q][m] + c, 16);
+          }
         }
-      }
 #pragma unroll
-      for (int k = 0; k < n; ++k) {
-        to_operands(lds.rows[wave], xv[k]);
+        for (int k = 0; k < n; ++k) {
+          if (q0 == 0) to_operands(lds.rows[wave], xv[k]);
 #pragma unroll
-        for (int q = 0; q < RT; ++q) {
-          to_operands(lds.rows[wave], wv[k][q]);
+          for (int q = 0; q < kJoined<RT>; ++q) {
+            to_operands(lds.rows[wave], wv[k][q]);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) acc[q] = mfma(wv[k][q][m], xv[k][m], acc[q]);
+            for (int m = 0; m < 4; ++m) acc[q0 + q] = mfma(wv[k][q][m], xv[k][m], acc[q0 + q]);
+          }
         }
+        if (RT > 4) __builtin_amdgcn_sched_barrier(0);
       }
       st += n * kShrinkWaves;
     };
