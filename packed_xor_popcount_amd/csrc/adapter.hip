@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(64) adapter_tiles_kernel(Grouping gr, int L) {
 }
 
 // Rows by adapter for the outer sums (what launch_group_rows makes), by one block
-// beside the contraction: 8192 rows make that 28 -> 33 us, where three launches
+// beside the contraction: 8192 rows make that 28 -> 29 us, where three launches
 // take 13 us and 10 us of the host's time.  Each wave counts and then places a stretch of the rows; `start`, its
 // next row of each id (L: none), holds kShrinkWaves x (L + 1).
 constexpr int64_t kGroupedRows = 8192;  // more would outlast the contraction
@@ -987,7 +987,9 @@ hipError_t shrink(const uint16_t *x, int64_t ldx, const int32_t *ids, const uint
                   const float *scale, float *u, uint16_t *parts, int64_t T, int64_t C, int r,
                   int L, const Grouping &gr, hipStream_t s) {
   const int64_t chunks = (T + kChunk - 1) / kChunk;
-  const dim3 grid((unsigned)chunks, tile_shares(T, L, chunks, 256) + (gr.rows ? 1 : 0));
+  // a block a CU, and a few CUs left for the one that groups the rows: 8192 rows in
+  // 224 blocks 29 us, in 256 (one more round then) 33
+  const dim3 grid((unsigned)chunks, tile_shares(T, L, chunks, 224) + (gr.rows ? 1 : 0));
 #define BNN_SHRINK_AS(RT, LONG)                                                                 \
   adapter_shrink_kernel<RT, LONG><<<grid, 64 * kShrinkWaves, 0, s>>>(x, ldx, ids, w, scale, u,  \
                                                                      parts, T, C, r, L, gr)
