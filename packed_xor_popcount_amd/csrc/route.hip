@@ -378,13 +378,15 @@ __global__ void __launch_bounds__(threads_of(LPT, V))
 
 // ... and the rows: every block sums the whole table itself (a launch less), four
 // experts a thread with eight rows in flight, and the first one takes the loss too.
-// 16384 x 128, 8 choices: 10.5 us (one expert a thread 22.8 us); the launch, the
-// table's latency and about ten barriers.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS)
+// 16384 x 128, 8 choices: 8.7 us (with 1024 threads 10.6, with 256 10.0; one expert a
+// thread 22.8); the launch, the table's latency and about ten barriers.
+constexpr int kPlaceThreads = 512;
+
+__global__ void __launch_bounds__(kPlaceThreads)
     route_place_kernel(RouteOut o, int64_t Tn, int E, int k, int64_t C,
                        const int *__restrict__ table, const int *__restrict__ block_routed,
                        const float *__restrict__ psum) {
+  constexpr int THREADS = kPlaceThreads;
   __shared__ Shared<THREADS> sh;
   __shared__ float sums[kRouteMaxExperts];
   const int B = gridDim.x, me = blockIdx.x, row = table_row(E);
@@ -475,10 +477,10 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 // Rows by group: counts of the block's ids for route_place_kernel.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(1024)
     group_count_kernel(const int32_t *__restrict__ ids, int64_t n, int G, int64_t C,
                        int *__restrict__ table) {
+  constexpr int THREADS = 1024;
   __shared__ int hist[kRouteMaxExperts];
   for (int g = threadIdx.x; g < G; g += THREADS) hist[g] = 0;
   __syncthreads();
@@ -598,7 +600,7 @@ hipError_t fwd(const void *z, int64_t ldz, const uint8_t *valid, const RouteOut 
                                                                  normalise, C, table, routed, psum);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  route_place_kernel<THREADS><<<(unsigned)B, THREADS, 0, s>>>(o, Tn, E, k, C, table, routed, psum);
+  route_place_kernel<<<(unsigned)B, kPlaceThreads, 0, s>>>(o, Tn, E, k, C, table, routed, psum);
   return hipGetLastError();
 }
 
@@ -652,17 +654,10 @@ hipError_t launch_group_rows(const int32_t *ids, int32_t *rows, int32_t *offsets
   o.experts = const_cast<int32_t *>(ids);
   o.rows = rows;
   o.offsets = offsets;
-  if (G <= 512) {
-    group_count_kernel<1024><<<B, 1024, 0, s>>>(ids, n, G, C, table);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    route_place_kernel<1024><<<B, 1024, 0, s>>>(o, n, G, 1, C, table, nullptr, nullptr);
-  } else {
-    group_count_kernel<512><<<B, 512, 0, s>>>(ids, n, G, C, table);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    route_place_kernel<512><<<B, 512, 0, s>>>(o, n, G, 1, C, table, nullptr, nullptr);
-  }
+  group_count_kernel<<<B, 1024, 0, s>>>(ids, n, G, C, table);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  route_place_kernel<<<B, kPlaceThreads, 0, s>>>(o, n, G, 1, C, table, nullptr, nullptr);
   return hipGetLastError();
 }
 
