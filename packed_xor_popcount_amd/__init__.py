@@ -611,26 +611,67 @@ def gemm_signw_grouped(x, wp, offsets, K=None, alpha=None, rows=None, row_scale=
     return out
 
 
-def _call(name: str, t: torch.Tensor, *args) -> None:
-    """One C call on the current stream of t's device, with that device current."""
-    fn = getattr(library(), name)
-    if torch.cuda.current_device() == t.device.index:
-        st = fn(*args, _stream(t))
-    else:
-        with torch.cuda.device(t.device):
-            st = fn(*args, _stream(t))
-    _check(st, name)
+# The calls below take a few microseconds on the device, so their checks are
+# written for few Python operations, and outputs are allocated by
+# torch.empty_strided (a third of a microsecond less than torch.empty).
+
+_CODES = {torch.float32: BNN_FP32, torch.bfloat16: BNN_BF16}
 
 
-def _matrix(name: str, t, shape, dtype, device) -> None:
-    _need_cuda(name, t)
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+def _index(name: str, t) -> int:
+    """Device index of a CUDA tensor."""
+    index = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if index < 0:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    return index
+
+
+def _rows_of(name: str, t, index: int):
+    """As _real_rows, of a tensor on device ``index``."""
+    if _index(name, t) != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D with unit stride along its last dimension")
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name} must be 2-D with unit stride along its last dimension")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return code, rows, cols, (ld if rows > 1 else max(cols, 1))
+
+
+def _matrix(name: str, t, shape, dtype, index: int) -> int:
+    """Pointer of a contiguous tensor of this shape and type on device ``index``."""
+    if _index(name, t) != index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
+    return t.data_ptr()
+
+
+def _same_rows(name: str, t, M: int, N: int, code: int, index: int):
+    """(pointer, row stride) of an input of the output's shape and type."""
+    d, Mt, Nt, ld = _rows_of(name, t, index)
+    if d != code or Mt != M or Nt != N:
+        raise ValueError(f"{name} must have the output's shape ({M}, {N}) and type")
+    return t.data_ptr(), ld
+
+
+def _out_rows(name: str, out, M: int, N: int, dtype, device, index: int):
+    """(tensor, type code, row stride) of an output, whose rows may be strided where it is given."""
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError("dtype must be float32 or bfloat16")
+    if out is None:
+        return _new(M, N, dtype, device), code, max(N, 1)
+    d, Mo, No, ld = _rows_of(name, out, index)
+    if d != code or Mo != M or No != N:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape ({M}, {N})")
+    return out, code, ld
 
 
 def _new(rows: int, cols: int, dtype, device):
-    # a third of a microsecond less than torch.empty
-    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+    return torch.empty_strided((rows, cols), (max(cols, 1), 1), dtype=dtype, device=device)
 
 
 def _new_vector(n: int, dtype, device):
@@ -638,7 +679,11 @@ def _new_vector(n: int, dtype, device):
 
 
 def _workspace(need: int, device):
-    return torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device) if need > 0 else None
+    """(tensor to keep until the call, pointer)."""
+    if need <= 0:
+        return None, None
+    ws = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr()
 
 
 class Routing(NamedTuple):
@@ -663,16 +708,19 @@ def route_fwd(logits, k, valid=None, normalise=True, loss=True) -> Routing:
     off for a token.  ``valid``: None or a contiguous bool or uint8 tensor (T,);
     a token that is not valid is not routed.  ``normalise``: the weights of a
     token's choices add up to 1."""
-    dt, T, E, ldz = _real_rows("logits", logits)
+    index = _index("logits", logits)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return route_fwd(logits, k, valid, normalise, loss)
+    dt, T, E, ldz = _rows_of("logits", logits, index)
     dev = logits.device
     k = int(k)
-    if valid is not None:
-        _need_cuda("valid", valid)
-        if (valid.dtype not in (torch.bool, torch.uint8) or tuple(valid.shape) != (T,)
-                or not valid.is_contiguous() or valid.device != dev):
-            raise ValueError(f"valid must be a contiguous bool or uint8 tensor of shape ({T},) on {dev}")
     if not (1 <= k <= E <= 1024 and k <= 32):
         raise BnnError(2, "bnn_route_fwd")
+    mask = None
+    if valid is not None:
+        _index("valid", valid)
+        mask = _matrix("valid", valid, (T,), torch.uint8 if valid.dtype is torch.uint8 else torch.bool, index)
     i32, f32 = torch.int32, torch.float32
     experts, place, weights = _new(T, k, i32, dev), _new(T, k, i32, dev), _new(T, k, f32, dev)
     rows, offsets, counts = _new_vector(T * k, i32, dev), _new_vector(E + 1, i32, dev), _new_vector(E, i32, dev)
@@ -680,11 +728,13 @@ def route_fwd(logits, k, valid=None, normalise=True, loss=True) -> Routing:
     slope = total = None
     if loss:
         slope, total = _new_vector(E, f32, dev), _new_vector(1, f32, dev)
-    need = library().bnn_route_fwd_workspace(T, E, k)
-    ws = _workspace(need, dev)
-    _call("bnn_route_fwd", logits, _ptr(logits), dt, ldz, _ptr(valid), _ptr(experts), _ptr(weights), _ptr(place),
-          _ptr(rows), _ptr(offsets), _ptr(counts), _ptr(stats), _ptr(slope), _ptr(total), _ptr(ws), need, T, E, k,
-          int(bool(normalise)))
+    lib = library()
+    need = lib.bnn_route_fwd_workspace(T, E, k)
+    ws, wp = _workspace(need, dev)
+    st = lib.bnn_route_fwd(logits.data_ptr(), dt, ldz, mask, experts.data_ptr(), weights.data_ptr(), place.data_ptr(),
+                           rows.data_ptr(), offsets.data_ptr(), counts.data_ptr(), stats.data_ptr(), _ptr(slope),
+                           _ptr(total), wp, need, T, E, k, 1 if normalise else 0, _stream(logits))
+    _check(st, "bnn_route_fwd")
     return Routing(experts, weights, place, rows, offsets, counts, stats, slope, total)
 
 
@@ -694,24 +744,27 @@ def route_bwd(logits, experts, weights, stats, slope=None, dweights=None, dloss=
     ``dweights`` (T, k) is the weights' gradient or None, ``dloss`` (a float32
     tensor of one element) the balance loss's or None.  Every tensor but the
     logits is contiguous; ``normalise`` as in the forward pass."""
-    dt, T, E, ldz = _real_rows("logits", logits)
-    dev = logits.device
-    _need_cuda("experts", experts)
+    index = _index("logits", logits)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return route_bwd(logits, experts, weights, stats, slope, dweights, dloss, normalise)
+    dt, T, E, ldz = _rows_of("logits", logits, index)
+    _index("experts", experts)
     k = experts.shape[1] if experts.dim() == 2 else -1
-    _matrix("experts", experts, (T, k), torch.int32, dev)
-    _matrix("weights", weights, (T, k), torch.float32, dev)
-    _matrix("stats", stats, (T, 2), torch.float32, dev)
-    if dweights is not None:
-        _matrix("dweights", dweights, (T, k), torch.float32, dev)
+    pe = _matrix("experts", experts, (T, k), torch.int32, index)
+    pw = _matrix("weights", weights, (T, k), torch.float32, index)
+    ps = _matrix("stats", stats, (T, 2), torch.float32, index)
+    pd = _matrix("dweights", dweights, (T, k), torch.float32, index) if dweights is not None else None
+    sl = dl = None
     if dloss is not None:
-        _vector("slope", slope, E, dev)
-        _need_cuda("dloss", dloss)
-        if dloss.dtype != torch.float32 or dloss.numel() != 1 or dloss.device != dev:
-            raise ValueError(f"dloss must be a float32 tensor of one element on {dev}")
-    dz = _new(T, E, logits.dtype, dev)
-    _call("bnn_route_bwd", logits, _ptr(logits), dt, ldz, _ptr(experts), _ptr(weights), _ptr(stats),
-          None if dloss is None else _ptr(slope), _ptr(dweights), _ptr(dloss), _ptr(dz), max(E, 1), T, E, k,
-          int(bool(normalise)))
+        sl = _matrix("slope", slope, (E,), torch.float32, index)
+        if _index("dloss", dloss) != index or dloss.dtype is not torch.float32 or dloss.numel() != 1:
+            raise ValueError(f"dloss must be a float32 tensor of one element on cuda:{index}")
+        dl = dloss.data_ptr()
+    dz = _new(T, E, logits.dtype, logits.device)
+    st = library().bnn_route_bwd(logits.data_ptr(), dt, ldz, pe, pw, ps, sl, pd, dl, dz.data_ptr(), max(E, 1), T, E, k,
+                                 1 if normalise else 0, _stream(logits))
+    _check(st, "bnn_route_bwd")
     return dz
 
 
@@ -723,23 +776,26 @@ def combine_fwd(y, place, weights=None, residual=None, dtype=None, out=None):
     or contiguous float32 (T, k); ``residual`` None or (T, N) of the output's
     type.  ``dtype`` of the output: float32 or bfloat16, the residual's or y's
     by default; ``out`` may be the residual itself."""
-    dty, R, N, ldy = _real_rows("y", y)
-    dev = y.device
-    _need_cuda("place", place)
+    index = _index("y", y)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return combine_fwd(y, place, weights, residual, dtype, out)
+    dty, R, N, ldy = _rows_of("y", y, index)
+    _index("place", place)
     if place.dim() != 2:
         raise ValueError("place must be 2-D")
     T, k = place.shape
-    _matrix("place", place, (T, k), torch.int32, dev)
-    if weights is not None:
-        _matrix("weights", weights, (T, k), torch.float32, dev)
+    pp = _matrix("place", place, (T, k), torch.int32, index)
+    pw = _matrix("weights", weights, (T, k), torch.float32, index) if weights is not None else None
     if dtype is None:
         dtype = out.dtype if out is not None else residual.dtype if residual is not None else y.dtype
-    out, dt, ldo = _rows_out("out", out, T, N, dtype, dev)
-    ldr = 0
+    out, dt, ldo = _out_rows("out", out, T, N, dtype, y.device, index)
+    pr, ldr = None, 0
     if residual is not None:
-        ldr = _same_rows("residual", residual, T, N, dt, dev)
-    _call("bnn_combine_fwd", y, _ptr(y), dty, ldy, R, _ptr(place), _ptr(weights), _ptr(residual), ldr, _ptr(out), dt,
-          ldo, T, N, k)
+        pr, ldr = _same_rows("residual", residual, T, N, dt, index)
+    st = library().bnn_combine_fwd(y.data_ptr(), dty, ldy, R, pp, pw, pr, ldr, out.data_ptr(), dt, ldo, T, N, k,
+                                   _stream(y))
+    _check(st, "bnn_combine_fwd")
     return out
 
 
@@ -752,67 +808,50 @@ def combine_bwd(dout, place, weights=None, y=None, rows=None, dtype=None):
     or missing.  Every row of dy is written if ``place`` names each row once,
     as route_fwd's does (rows without an expert: zeros); others are left
     undefined.  The residual's gradient is dout itself."""
-    dt, T, N, lddo = _real_rows("dout", dout)
+    index = _index("dout", dout)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return combine_bwd(dout, place, weights, y, rows, dtype)
+    dt, T, N, lddo = _rows_of("dout", dout, index)
     dev = dout.device
-    _need_cuda("place", place)
+    _index("place", place)
     k = place.shape[1] if place.dim() == 2 else -1
-    _matrix("place", place, (T, k), torch.int32, dev)
-    if weights is not None:
-        _matrix("weights", weights, (T, k), torch.float32, dev)
-    data = ys = None
+    pp = _matrix("place", place, (T, k), torch.int32, index)
+    pw = _matrix("weights", weights, (T, k), torch.float32, index) if weights is not None else None
+    py = ys = None
     dty, ldy = BNN_BF16, N
     if y is None:
         R = T * k if rows is None else int(rows)
     elif isinstance(y, (tuple, list)):
-        data, ys = y
-        R = _quantised("y", data, ys, N)
-        dty = BNN_F8
+        q, s = y
+        R = _quantised("y", q, s, N)
+        if q.get_device() != index:
+            raise ValueError(f"y must be on cuda:{index}")
+        py, ys, dty = q.data_ptr(), s.data_ptr(), BNN_F8
     else:
-        data = y
-        dty, R, Ny, ldy = _real_rows("y", y)
+        dty, R, Ny, ldy = _rows_of("y", y, index)
         if Ny != N:
             raise ValueError(f"y has {Ny} columns, dout {N}")
+        py = y.data_ptr()
         dtype = y.dtype if dtype is None else dtype
-    if data is not None and data.device != dev:
-        raise ValueError(f"y must be on {dev}")
-    dy, dtd = _real_out(R, N, dout.dtype if dtype is None else dtype, dev, None)
+    dy, dtd, lddy = _out_rows("dy", None, R, N, dout.dtype if dtype is None else dtype, dev, index)
     dw = None if y is None else _new(T, k, torch.float32, dev)
-    _call("bnn_combine_bwd", dout, _ptr(dout), dt, lddo, _ptr(data), _ptr(ys), dty, ldy, R, _ptr(place), _ptr(weights),
-          _ptr(dy), dtd, max(N, 1), _ptr(dw), T, N, k)
+    st = library().bnn_combine_bwd(dout.data_ptr(), dt, lddo, py, ys, dty, ldy, R, pp, pw, dy.data_ptr(), dtd, lddy,
+                                   _ptr(dw), T, N, k, _stream(dout))
+    _check(st, "bnn_combine_bwd")
     return dy, dw
 
 
-def _rows_out(name: str, out, M: int, N: int, dtype, device):
-    """(tensor, dtype code, row stride) of an output whose rows may be strided."""
-    if out is None:
-        out, dt = _real_out(M, N, dtype, device, None)
-        return out, dt, max(N, 1)
-    dt, Mo, No, ld = _real_rows(name, out)
-    if (Mo, No) != (M, N) or out.dtype != dtype or out.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape ({M}, {N}) on {device}")
-    return out, dt, ld
-
-
-def _same_rows(name: str, t, M: int, N: int, dt: int, device) -> int:
-    """Row stride of an input of the output's shape and type."""
-    d, Mt, Nt, ld = _real_rows(name, t)
-    if (d, Mt, Nt) != (dt, M, N) or t.device != device:
-        raise ValueError(f"{name} must have the output's shape ({M}, {N}), type and device")
-    return ld
-
-
-def _factors(ids, a, b, scale, T: int, K: int, N: int, device):
-    """(adapters, rank) of checked adapter factors."""
-    _vector("ids", ids, T, device, torch.int32)
-    _need_cuda("a", a)
+def _factors(ids, a, b, scale, T: int, K: int, N: int, index: int):
+    """(adapters, rank, pointers of ids, a, b and scale) of checked adapter factors."""
+    pi = _matrix("ids", ids, (T,), torch.int32, index)
+    _index("a", a)
     if a.dim() != 3:
         raise ValueError("a must be 3-D: (adapters, rank, K)")
-    L, r = a.shape[0], a.shape[1]
-    _matrix("a", a, (L, r, K), torch.bfloat16, device)
-    _matrix("b", b, (L, r, N), torch.bfloat16, device)
-    if scale is not None:
-        _vector("scale", scale, L, device)
-    return L, r
+    L, r, _ = a.shape
+    pa = _matrix("a", a, (L, r, K), torch.bfloat16, index)
+    pb = _matrix("b", b, (L, r, N), torch.bfloat16, index)
+    return L, r, pi, pa, pb, (_matrix("scale", scale, (L,), torch.float32, index) if scale is not None else None)
 
 
 def adapter_fwd(x, ids, a, b, scale=None, base=None, dtype=None, out=None):
@@ -825,22 +864,30 @@ def adapter_fwd(x, ids, a, b, scale=None, base=None, dtype=None, out=None):
     float32 (L,); ``base`` None (0) or (T, N), the projection's output, of type
     ``dtype`` (float32 or bfloat16; the base's by default, else float32).
     ``out`` may be the base itself: rows without an adapter stay as they are."""
-    dtx, T, K, ldx = _real_rows("x", x)
+    index = _index("x", x)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return adapter_fwd(x, ids, a, b, scale, base, dtype, out)
+    dtx, T, K, ldx = _rows_of("x", x, index)
     if dtx != BNN_BF16:
         raise TypeError("x must be bfloat16")
     dev = x.device
-    _need_cuda("b", b)
+    _index("b", b)
     N = b.shape[2] if b.dim() == 3 else -1
-    L, r = _factors(ids, a, b, scale, T, K, N, dev)
+    L, r, pi, pa, pb, ps = _factors(ids, a, b, scale, T, K, N, index)
     if dtype is None:
         dtype = out.dtype if out is not None else base.dtype if base is not None else torch.float32
-    out, dt, ldo = _rows_out("out", out, T, N, dtype, dev)
-    ldb = _same_rows("base", base, T, N, dt, dev) if base is not None else 0
+    out, dt, ldo = _out_rows("out", out, T, N, dtype, dev, index)
+    pbase, ldb = None, 0
+    if base is not None:
+        pbase, ldb = _same_rows("base", base, T, N, dt, index)
     u = _new(T, r, torch.float32, dev)
-    need = library().bnn_adapter_fwd_workspace(T, K, N, r, L)
-    ws = _workspace(need, dev)
-    _call("bnn_adapter_fwd", x, _ptr(x), ldx, _ptr(ids), _ptr(a), _ptr(b), _ptr(scale), _ptr(base), ldb, _ptr(out),
-          ldo, dt, _ptr(u), _ptr(ws), need, T, K, N, r, L)
+    lib = library()
+    need = lib.bnn_adapter_fwd_workspace(T, K, N, r, L)
+    ws, wp = _workspace(need, dev)
+    st = lib.bnn_adapter_fwd(x.data_ptr(), ldx, pi, pa, pb, ps, pbase, ldb, out.data_ptr(), ldo, dt, u.data_ptr(), wp,
+                             need, T, K, N, r, L, _stream(x))
+    _check(st, "bnn_adapter_fwd")
     return out, u
 
 
@@ -854,52 +901,53 @@ def adapter_bwd(dy, x, u, ids, a, b, scale=None, base=None, dtype=None, dx=True,
     ``db[l] = scale[l] * sum_t outer(u[t], dy[t])`` over l's rows (float32).
     ``base`` None (0) or (T, K): the gradient that reaches x by the shared
     projection, of type ``dtype`` (the base's by default, else float32).
-    ``dx=False`` and ``params=False`` leave those out (None).  With ``params``
-    at most 1024 adapters."""
-    dtd, T, N, lddy = _real_rows("dy", dy)
+    ``dx=False`` and ``params=False`` leave those out (None).  At most 1024
+    adapters."""
+    index = _index("dy", dy)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return adapter_bwd(dy, x, u, ids, a, b, scale, base, dtype, dx, params)
+    dtd, T, N, lddy = _rows_of("dy", dy, index)
     if dtd != BNN_BF16:
         raise TypeError("dy must be bfloat16")
     dev = dy.device
-    _need_cuda("a", a)
+    _index("a", a)
     K = a.shape[2] if a.dim() == 3 else -1
-    L, r = _factors(ids, a, b, scale, T, K, N, dev)
-    data = xs = None
+    L, r, pi, pa, pb, ps = _factors(ids, a, b, scale, T, K, N, index)
+    px = pxs = pu = None
     dtx, ldx = BNN_BF16, max(K, 1)
     if params:
-        _matrix("u", u, (T, r), torch.float32, dev)
+        pu = _matrix("u", u, (T, r), torch.float32, index)
         if isinstance(x, (tuple, list)):
-            data, xs = x
-            if _quantised("x", data, xs, K) != T:
+            q, s = x
+            if _quantised("x", q, s, K) != T:
                 raise ValueError(f"x must have {T} rows")
-            dtx = BNN_F8
+            if q.get_device() != index:
+                raise ValueError(f"x must be on cuda:{index}")
+            px, pxs, dtx = q.data_ptr(), s.data_ptr(), BNN_F8
         else:
-            data = x
-            dtx, Tx, Kx, ldx = _real_rows("x", x)
+            dtx, Tx, Kx, ldx = _rows_of("x", x, index)
             if dtx != BNN_BF16:
                 raise TypeError("x must be bfloat16")
             if (Tx, Kx) != (T, K):
                 raise ValueError(f"x must have shape ({T}, {K})")
-        if data.device != dev:
-            raise ValueError(f"x must be on {dev}")
-    out, dt, ldo, ldb = None, BNN_FP32, max(K, 1), 0
+            px = x.data_ptr()
+    out, dt, ldo = None, BNN_FP32, max(K, 1)
+    pbase, ldb = None, 0
     if dx:
         if dtype is None:
             dtype = base.dtype if base is not None else torch.float32
-        out, dt, ldo = _rows_out("dx", None, T, K, dtype, dev)
+        out, dt, ldo = _out_rows("dx", None, T, K, dtype, dev, index)
         if base is not None:
-            ldb = _same_rows("base", base, T, K, dt, dev)
-    else:
-        base = None
+            pbase, ldb = _same_rows("base", base, T, K, dt, index)
     da = db = None
-    need = 0
-    ws = None
-    if dx or params:
-        need = library().bnn_adapter_bwd_workspace(T, K, N, r, L)
-        ws = _workspace(need, dev)
     if params:
         da = torch.empty((L, r, K), dtype=torch.float32, device=dev)
         db = torch.empty((L, r, N), dtype=torch.float32, device=dev)
-    _call("bnn_adapter_bwd", dy, _ptr(dy), lddy, _ptr(data), _ptr(xs), dtx, ldx, _ptr(u) if params else None,
-          _ptr(ids), _ptr(a), _ptr(b), _ptr(scale), _ptr(base), ldb, _ptr(out), ldo, dt, _ptr(da), _ptr(db), _ptr(ws),
-          need, T, K, N, r, L)
+    lib = library()
+    need = lib.bnn_adapter_bwd_workspace(T, K, N, r, L)
+    ws, wp = _workspace(need, dev)
+    st = lib.bnn_adapter_bwd(dy.data_ptr(), lddy, px, pxs, dtx, ldx, pu, pi, pa, pb, ps, pbase, ldb, _ptr(out), ldo, dt,
+                             _ptr(da), _ptr(db), wp, need, T, K, N, r, L, _stream(dy))
+    _check(st, "bnn_adapter_bwd")
     return out, da, db
