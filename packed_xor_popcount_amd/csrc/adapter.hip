@@ -8,7 +8,8 @@
 //   dA_l = s_l sum_t v_t x_t'            dB_l = s_l sum_t u_t dy_t'
 //
 // Three kernels: shrink (u, v: sums over the long side), expand (out, dx: sums
-// over the rank) and outer (dA, dB: sums over an adapter's rows).  All sums are
+// over the rank) and outer (dA, dB: sums over an adapter's rows); a gradient runs
+// the last two side by side in one launch.  All sums are
 // fp32 on the matrix cores from exact products of bf16 values: u and v, which
 // are fp32, are split into three bf16 parts (8 + 8 + 8 significant bits), so that
 // no rounding comes between the two factors.  The order of every sum goes by
@@ -633,18 +634,32 @@ __device__ __forceinline__ void finish_tile(const Plan &plan, int s0, int len, b
   }
 }
 
+template <typename O>
+struct Expand {
+  const uint16_t *parts;  // of w's side, T x parts_kept x 16 RP
+  const int32_t *ids;
+  const uint16_t *w;
+  const O *base;
+  O *out;
+  int64_t ldb, ldo, T, C;
+  int r, L;
+};
+
+// Block: 512 columns, a chunk of rows, a share of its tiles.
 template <typename O, int RP, bool LONG>
-__global__ void __launch_bounds__(256, RP <= 2 ? (sizeof(O) == 2 ? 3 : 2) : RP == 4 ? 2 : 1)
-    adapter_expand_kernel(const uint16_t *__restrict__ parts, const int32_t *__restrict__ ids,
-                          const uint16_t *__restrict__ w, const O *base, int64_t ldb, O *out,
-                          int64_t ldo, int64_t T, int64_t C, int r, int L) {
-  __shared__ Plan plan;
+__device__ __forceinline__ void expand_block(const Expand<O> &e, Plan &plan, dim3 block,
+                                             int shares) {
+  const uint16_t *__restrict__ parts = e.parts, *__restrict__ w = e.w;
+  const O *base = e.base;
+  O *out = e.out;
+  const int64_t ldb = e.ldb, ldo = e.ldo, T = e.T, C = e.C;
+  const int r = e.r, L = e.L;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.y * kChunk;
-  make_plan(plan, ids, t0, T, L);
-  const int lo = (int)((int64_t)plan.tiles * blockIdx.z / gridDim.z);
-  const int hi = (int)((int64_t)plan.tiles * (blockIdx.z + 1) / gridDim.z);
-  const int64_t c0 = ((int64_t)blockIdx.x * 4 + wave) * 128;
+  const int64_t t0 = (int64_t)block.y * kChunk;
+  make_plan(plan, e.ids, t0, T, L);
+  const int lo = (int)((int64_t)plan.tiles * block.z / shares);
+  const int hi = (int)((int64_t)plan.tiles * (block.z + 1) / shares);
+  const int64_t c0 = ((int64_t)block.x * 4 + wave) * 128;
   if (c0 >= C || lo >= hi) return;
   const int64_t c = c0 + 8 * (lane & 15);
   const bool edge = c0 + 128 > C;
@@ -694,6 +709,13 @@ __global__ void __launch_bounds__(256, RP <= 2 ? (sizeof(O) == 2 ? 3 : 2) : RP =
     __builtin_amdgcn_sched_barrier(0);
     tile(i + 1, two);
   }
+}
+
+template <typename O, int RP, bool LONG>
+__global__ void __launch_bounds__(256, RP <= 2 ? (sizeof(O) == 2 ? 3 : 2) : RP == 4 ? 2 : 1)
+    adapter_expand_kernel(Expand<O> e) {
+  __shared__ Plan plan;
+  expand_block<O, RP, LONG>(e, plan, blockIdx, gridDim.z);
 }
 
 // Few rows: both products in one launch.  Every block of 1024 columns sums u
@@ -894,27 +916,60 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
     }
 }
 
-// blockIdx.x: 512 columns of the first or (from `split` on) the second side;
-// blockIdx.y: a tile; blockIdx.z: RT x 16 of the ranks.
+struct Outer {
+  Side first, second;
+  const int32_t *rows;
+  const int4 *tiles;
+  const float *scale;
+  int split, most, r;
+};
+
+// Block: 512 columns of the first or (from `split` on) the second side, a tile,
+// RT x 16 of the ranks.
 template <int RT, bool F8, bool LONG>
-__global__ void __launch_bounds__(256)
-    adapter_outer_kernel(Side first, Side second, int split, const int32_t *__restrict__ rows,
-                         const int4 *__restrict__ tiles, int most,
-                         const float *__restrict__ scale, int r) {
-  const bool two = (int)blockIdx.x >= split;
-  const int wave = threadIdx.x >> 6;
-  const Side &sd = two ? second : first;
-  const int64_t c0 = ((int64_t)(two ? blockIdx.x - split : blockIdx.x) * 4 + wave) * 128;
+__device__ __forceinline__ void outer_block(const Outer &o, dim3 block, int step) {
+  const bool two = (int)block.x >= o.split;
+  const int wave = threadIdx.x >> 6, r = o.r;
+  const Side &sd = two ? o.second : o.first;
+  const int64_t c0 = ((int64_t)(two ? block.x - o.split : block.x) * 4 + wave) * 128;
   if (c0 >= sd.C) return;
-  for (int i = blockIdx.y; i < most; i += gridDim.y) {
-    const int4 t = tiles[i];
+  for (int i = block.y; i < o.most; i += step) {
+    const int4 t = o.tiles[i];
     if (t.x < 0) return;
-    const float s = scale ? scale[t.x] : 1.0f;
+    const float s = o.scale ? o.scale[t.x] : 1.0f;
     float *out = t.w < 0 ? sd.d + (int64_t)t.x * r * sd.C : sd.slot + (int64_t)t.w * r * sd.C;
-    const int j0 = blockIdx.z * RT * 16;
-    if (two || !F8) outer_tile<RT, false, LONG>(sd, rows, t.y, t.z, s, c0, j0, r, out);
-    else outer_tile<RT, F8, LONG>(sd, rows, t.y, t.z, s, c0, j0, r, out);
+    const int j0 = block.z * RT * 16;
+    if (two || !F8) outer_tile<RT, false, LONG>(sd, o.rows, t.y, t.z, s, c0, j0, r, out);
+    else outer_tile<RT, F8, LONG>(sd, o.rows, t.y, t.z, s, c0, j0, r, out);
   }
+}
+
+template <int RT, bool F8, bool LONG>
+__global__ void __launch_bounds__(256) adapter_outer_kernel(Outer o) {
+  outer_block<RT, F8, LONG>(o, blockIdx, gridDim.y);
+}
+
+// The input's gradient and the outer sums in one launch: neither waits for the
+// other, the first is bound by memory, the second by its steps' latency.  Their
+// blocks alternate, so that a CU has one of each: 8192 rows, 4096 bf16 and 4096 in 8
+// bits, rank 32: the call 94 us, as two launches 102; 20000 rows, rank 16: 186 us
+// (outer sums first 201, last 209, two launches 227).
+struct Grid {
+  unsigned x, y, z;
+  __host__ __device__ unsigned blocks() const { return x * y * z; }
+  __device__ dim3 at(unsigned i) const { return dim3(i % x, i / x % y, i / x / y); }
+};
+
+template <typename O, int RP, bool F8, bool LONG>
+__global__ void __launch_bounds__(256, 2)
+    adapter_both_kernel(Expand<O> e, Grid ge, Outer o, Grid go) {
+  __shared__ Plan plan;
+  const uint64_t i = blockIdx.x, no = go.blocks(), n = no + ge.blocks();
+  const unsigned k = (unsigned)(i * no / n);  // outer sums before this block
+  if ((unsigned)((i + 1) * no / n) > k)
+    outer_block<RP == 1 ? 1 : 2, F8, LONG>(o, go.at(k), go.y);
+  else
+    expand_block<O, RP, LONG>(e, plan, ge.at((unsigned)i - k), ge.z);
 }
 
 // The sums of adapters with several tiles, and zeros for those without rows.  A
@@ -1023,10 +1078,10 @@ hipError_t expand(const uint16_t *parts, const int32_t *ids, const uint16_t *w, 
     const int64_t n = T - t < chunks * kChunk ? T - t : chunks * kChunk;
     const dim3 grid((unsigned)cols, (unsigned)chunks, tile_shares(n, L, cols * chunks, 384));
     const uint16_t *pt = parts + parts_bytes(t, r) / 2;
-#define BNN_EXPAND_AS(RP, LONG)                                                                  \
-  adapter_expand_kernel<O, RP, LONG><<<grid, 256, 0, s>>>(pt, ids + t, w,                        \
-                                                          bt ? bt + t * ldb : nullptr, ldb,      \
-                                                          ot + t * ldo, ldo, n, C, r, L)
+    const Expand<O> e = {pt,  ids + t, w, bt ? bt + t * ldb : nullptr, ot + t * ldo,
+                         ldb, ldo,     n, C,                           r,
+                         L};
+#define BNN_EXPAND_AS(RP, LONG) adapter_expand_kernel<O, RP, LONG><<<grid, 256, 0, s>>>(e)
 #define BNN_EXPAND(RP)                    \
   do {                                    \
     if (C >= 8) BNN_EXPAND_AS(RP, true);  \
@@ -1040,8 +1095,8 @@ hipError_t expand(const uint16_t *parts, const int32_t *ids, const uint16_t *w, 
     }
 #undef BNN_EXPAND
 #undef BNN_EXPAND_AS
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    const hipError_t st = hipGetLastError();
+    if (st != hipSuccess) return st;
   }
   return hipSuccess;
 }
@@ -1084,6 +1139,30 @@ BwdLayout bwd_layout(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
   b.slot_b = b.slot_a + align16(slots * r * K * 4);
   b.bytes = b.slot_b + align16(slots * r * N * 4);
   return b;
+}
+
+template <typename O>
+hipError_t both(Expand<O> e, const Grid &ge, const Outer &o, const Grid &go, hipStream_t s) {
+  const unsigned blocks = ge.blocks() + go.blocks();
+  const bool f8 = o.first.ys != nullptr;
+  const bool wide = (o.first.C >= 8 || o.first.C == 0) && (o.second.C >= 8 || o.second.C == 0);
+#define BNN_BOTH_AS(RP, F8, LONG) \
+  adapter_both_kernel<O, RP, F8, LONG><<<blocks, 256, 0, s>>>(e, ge, o, go)
+#define BNN_BOTH(RP)                                  \
+  do {                                                \
+    if (wide && f8) BNN_BOTH_AS(RP, true, true);      \
+    else if (wide) BNN_BOTH_AS(RP, false, true);      \
+    else if (f8) BNN_BOTH_AS(RP, true, false);        \
+    else BNN_BOTH_AS(RP, false, false);               \
+  } while (0)
+  switch (rank_tiles(o.r)) {
+    case 1: BNN_BOTH(1); break;
+    case 2: BNN_BOTH(2); break;
+    default: BNN_BOTH(4);
+  }
+#undef BNN_BOTH
+#undef BNN_BOTH_AS
+  return hipGetLastError();
 }
 
 bool adapter_small(int64_t T, int64_t N, int64_t r, int64_t L) {
@@ -1151,12 +1230,22 @@ hipError_t launch_adapter_bwd(const AdapterGrad &q, void *workspace, int64_t T, 
                        reinterpret_cast<int2 *>(ws + b.sums), (int)b.most, (int)b.chunk};
   uint16_t *parts = reinterpret_cast<uint16_t *>(ws + b.parts);
   const bool beside = q.sums && T > 0 && T <= kGroupedRows && L <= kGroupedMost;
+  const int split = (int)((K + 511) / 512), cols = split + (int)((N + 511) / 512);
+  const Side sa = {v, q.x, q.xs, q.ldx, K, q.da, reinterpret_cast<float *>(ws + b.slot_a)};
+  const Side sb = {q.u, q.dy, nullptr, q.lddy, N, q.db, reinterpret_cast<float *>(ws + b.slot_b)};
+  const Outer o = {sa, sb, gr.rows, gr.tiles, q.scale, split, gr.most, r};
+  const Grid go = {(unsigned)cols, (unsigned)(b.most < 65535 ? b.most : 65535),
+                   (unsigned)((r + (r <= 16 ? 15 : 31)) / (r <= 16 ? 16 : 32))};
+  const int64_t kc = (K + 511) / 512, chunks = (T + kChunk - 1) / kChunk;
+  // one launch for both, unless its blocks are too many for one line of them
+  const bool joined = q.sums && q.dx && T > 0 && K > 0 && r <= 64 && kc * chunks <= (1 << 20) &&
+                      cols * b.most <= (1 << 20);
   hipError_t e = hipSuccess;
   if (T > 0) {
     e = shrink(q.dy, q.lddy, q.ids, q.b, q.scale, v, q.dx ? parts : nullptr, T, N, r, L,
                beside ? gr : Grouping{}, s);
     if (e != hipSuccess) return e;
-    if (q.dx) {
+    if (q.dx && !joined) {
       e = expand_as(q.dtype, parts, q.ids, q.a, q.base, q.ldb, q.dx, q.lddx, T, K, r, L, s);
       if (e != hipSuccess) return e;
     }
@@ -1169,15 +1258,22 @@ hipError_t launch_adapter_bwd(const AdapterGrad &q, void *workspace, int64_t T, 
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const Side sa = {v, q.x, q.xs, q.ldx, K, q.da, reinterpret_cast<float *>(ws + b.slot_a)};
-  const Side sb = {q.u, q.dy, nullptr, q.lddy, N, q.db, reinterpret_cast<float *>(ws + b.slot_b)};
-  const int split = (int)((K + 511) / 512), cols = split + (int)((N + 511) / 512);
-  if (b.most > 0) {
-    const unsigned ty = (unsigned)(b.most < 65535 ? b.most : 65535);
-#define BNN_OUTER(RT, F8, LONG)                                                                  \
-  adapter_outer_kernel<RT, F8, LONG>                                                             \
-      <<<dim3(cols, ty, (r + RT * 16 - 1) / (RT * 16)), 256, 0, s>>>(sa, sb, split, gr.rows,     \
-                                                                     gr.tiles, gr.most, q.scale, r)
+  if (joined) {
+    // 640 shorter blocks of dx beside the sums' (384: 4096 rows on 16 adapters in random
+    // order, rank 16, 72 us, here 68; 8192 in order 91, here 93)
+    const Grid ge = {(unsigned)kc, (unsigned)chunks, tile_shares(T, L, kc * chunks, 640)};
+    if (q.dtype == BNN_FP32)
+      e = both<float>({parts, q.ids, q.a, static_cast<const float *>(q.base),
+                       static_cast<float *>(q.dx), q.ldb, q.lddx, T, K, r, L},
+                      ge, o, go, s);
+    else
+      e = both<bf16_t>({parts, q.ids, q.a, static_cast<const bf16_t *>(q.base),
+                        static_cast<bf16_t *>(q.dx), q.ldb, q.lddx, T, K, r, L},
+                       ge, o, go, s);
+    if (e != hipSuccess) return e;
+  } else if (b.most > 0) {
+    const dim3 grid(go.x, go.y, go.z);
+#define BNN_OUTER(RT, F8, LONG) adapter_outer_kernel<RT, F8, LONG><<<grid, 256, 0, s>>>(o)
 #define BNN_OUTER_AS(RT)                                             \
   do {                                                               \
     if ((K < 8 && K > 0) || (N < 8 && N > 0)) {                      \

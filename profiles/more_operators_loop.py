@@ -19,7 +19,8 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 CALLS = 24
 KERNELS = tuple(k + "_kernel" for k in (
     "route_one", "route_choose", "route_place", "route_bwd", "group_count", "combine_fwd", "combine_bwd",
-    "adapter_small", "adapter_shrink", "adapter_expand", "adapter_outer", "adapter_join", "adapter_tiles"))
+    "adapter_small", "adapter_shrink", "adapter_expand", "adapter_both", "adapter_outer",
+    "adapter_join", "adapter_tiles"))
 
 
 def run(path, only=""):
@@ -57,6 +58,7 @@ def run(path, only=""):
             "pad": 0, "kept": "bf16"}
     case("adapter_bwd 1024 rows 4096 x 4096 rank 16", more)
     case("adapter_bwd 4096 rows 4096 x 4096 rank 64", dict(more, rows=4096, rank=64))
+    case("adapter_bwd 2048 rows 4096 x 4096 rank 128", dict(more, rows=2048, rank=128))
     route = dict(ops.listed()[1])
     case("combine_fwd 4096 x 4096, 8, fp32", dict(ops.listed()[5], tokens=4096, k=8, dtype="fp32"))
     case("combine_bwd 2000 x 4096, 4, bf16", dict(ops.listed()[7], tokens=2000, dtype="bf16"))

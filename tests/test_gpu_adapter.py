@@ -173,6 +173,38 @@ def test_bwd_of_many_rows(T, L, ids):
         check_bwd(Case(T, T, 200, 136, 20, L, ids), kept)
 
 
+@pytest.mark.parametrize("r", [3, 16, 17, 64, 65])
+@pytest.mark.parametrize("T,K,N", [(300, 5, 300), (300, 300, 5), (90, 3, 2), (700, 8, 1024), (700, 1500, 7)])
+def test_bwd_of_narrow_sides(T, K, N, r):
+    """The input's gradient and the parameters' in one launch (ranks up to 64) and in two, at uneven widths."""
+    for kept, dt in (("bf16", "fp32"), ("f8", "bf16")):
+        check_bwd(Case(K + r, T, K, N, r, 6, "runs", pad=1, integers=False, dtype=DT[dt]), kept)
+
+
+def test_bwd_of_many_adapters_and_columns():
+    """More blocks than one launch takes for both gradients; whole numbers below 2^24, so every sum is exact."""
+    T, K, N, L = 1030, 266000, 271003, 1024
+    c = Case(5, T, K, N, 1, L, "mixed")
+    at = (c.ids >= 0).nonzero().flatten()
+    l = c.ids[at].long()
+    _, u = bnn.adapter_fwd(c.x, c.ids, c.a, c.b, scale=c.scale)
+    dx, da, db = bnn.adapter_bwd(c.dy, c.x, u, c.ids, c.a, c.b, scale=c.scale, base=c.dbase)
+    ref = c.dbase.clone()
+    sums = [torch.zeros(L, K, device=DEV), torch.zeros(L, N, device=DEV)]
+    most = 0.0
+    for i in range(0, len(at), 64):
+        t, m = at[i:i + 64], l[i:i + 64]
+        s = c.scale[m][:, None]
+        v = (c.dy[t].float() * c.b[m, 0].float()).sum(1, keepdim=True)
+        ref[t] += s * v * c.a[m, 0].float()
+        for d, w, y in ((sums[0], v, c.x), (sums[1], u[t], c.dy)):
+            p = s * w * y[t].float()
+            most = max(most, float(p.abs().max()))
+            d.index_add_(0, m, p)
+    assert most * int(torch.bincount(l).max()) < 2 ** 24
+    assert torch.equal(dx, ref) and torch.equal(da[:, 0], sums[0]) and torch.equal(db[:, 0], sums[1])
+
+
 @pytest.mark.parametrize("T", [255, 256, 257, 512])
 @pytest.mark.parametrize("N,r,L", [(300, 16, 40), (1030, 32, 2), (2100, 33, 3), (9000, 16, 250)])
 def test_chunk_ends_and_the_choice_of_kernels(T, N, r, L):
