@@ -79,15 +79,16 @@ struct Rows {
   }
 };
 
-// The 8-bit form: eight neighbours share a block's scale, which multiplies
-// their sum, so that a value of 2^128 (what magnitudes from 1.9375 * 2^127 on
-// decode to) is never formed.
+// The 8-bit form.  Eight neighbours share a block's scale, which each is multiplied
+// by before its product (exactly: 448 * 2^119 and 2^-9 * 2^-127 are fp32 values), so
+// that a sum leaves fp32's range only where the rows' own values take it there.  Of a
+// scale byte over 246 the rest of the power of two multiplies the sum: a value of
+// 2^128 (what magnitudes from 1.9375 * 2^127 on decode to) is never formed.
 struct Rows8 {
   const uint8_t *q, *s;
   int64_t ldq, lds;
   struct Piece {
-    uint32_t lo, hi;
-    float scale;
+    uint32_t lo, hi, e;
   };
   __device__ __forceinline__ Piece load(int64_t row, int n, int) const {
     Piece p;
@@ -95,8 +96,7 @@ struct Rows8 {
     __builtin_memcpy(&v, q + row * ldq + n, 8);  // rows are padded to whole blocks
     p.lo = v.x;
     p.hi = v.y;
-    const uint32_t e = s[row * lds + n / kF8Block];
-    p.scale = __uint_as_float(e ? e << 23 : 0x00400000u);
+    p.e = s[row * lds + n / kF8Block];
     return p;
   }
   static __device__ __forceinline__ float dot(const Piece &p, const float (&d)[8], int n, int N,
@@ -106,10 +106,13 @@ struct Rows8 {
     const v2f c = __builtin_amdgcn_cvt_pk_f32_fp8(p.hi, false);
     const v2f e = __builtin_amdgcn_cvt_pk_f32_fp8(p.hi, true);
     const float v[8] = {a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
+    const uint32_t held = p.e < 246 ? p.e : 246;
+    const float scale = __uint_as_float(held ? held << 23 : 0x00400000u);
+    const float rest = __uint_as_float((127 + p.e - held) << 23);
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(d[i], n + i < N ? v[i] : 0.0f, sum);
-    return fmaf(sum, p.scale, s);
+    for (int i = 0; i < 8; ++i) sum = fmaf(d[i], n + i < N ? v[i] * scale : 0.0f, sum);
+    return fmaf(sum, rest, s);
   }
 };
 
