@@ -799,6 +799,15 @@ __device__ __forceinline__ bf16x2 widen2(uint32_t v, float scale, bool high) {
 // two goes to w, so that no value leaves bf16's range on either side.
 __device__ __forceinline__ int held_scale(int s) { return s < 27 ? 27 : s > 245 ? 245 : s; }
 
+// A finite w that the rest 2^(e - 245) of a scale byte e > 245 would take out of fp32's
+// range (what is not zero in the block is at least 2^109, and overflows beside it): the
+// largest that it does not, so that the block's zeros give zeros.
+__device__ __forceinline__ float held_factor(float w, int e) {
+  if (e <= 245 || (__float_as_uint(w) & 0x7F800000u) == 0x7F800000u) return w;
+  const float most = __uint_as_float(0x7F7FFFFFu - ((uint32_t)(e - 245) << 23));
+  return fminf(fmaxf(w, -most), most);
+}
+
 // Rows, values of y and of w for 32 rows of a tile, as they are in memory.
 template <int RT, bool F8>
 struct Step {
@@ -860,6 +869,17 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
     __builtin_amdgcn_sched_barrier(0);
     uint4 y[8], f[8];
     float rest[8];
+    if (F8) {
+      int e = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e = (int)cur.y[k].z > e ? (int)cur.y[k].z : e;
+      if (__any(e > 245)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int q = 0; q < RT; ++q) cur.w[q][k] = held_factor(cur.w[q][k], (int)cur.y[k].z);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       y[k] = cur.y[k];

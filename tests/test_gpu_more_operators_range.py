@@ -50,3 +50,27 @@ def test_sum_of_experts_from_8_bits_at_every_scale(byte):
     _, dw = bnn.combine_bwd(dout, place, y=(q.view(torch.uint8), s))
     want = [448 * 2.0 ** (byte - 127 + up), -448 * 2.0 ** (byte - 127 + up), 2.0 ** (byte - 127 - 9 + up2)]
     assert dw.flatten().tolist() == want
+
+
+@pytest.mark.parametrize("big", [2.0 ** 126, 2.0 ** 127, -2.0 ** 127, 3.38e38])
+@pytest.mark.parametrize("T", [2, 300])
+def test_gradient_from_8_bits_leaves_zeros_beside_large_factors(big, T):
+    """A block of the largest scale byte: its zeros give zeros whatever finite value they meet."""
+    x = torch.zeros(T, 130, device=DEV)
+    x[0, 3], x[1, 3], x[1, 128] = 3.3e38, -3.3e38, 2.0 ** -100
+    q = bnn.quant_f8(x)
+    assert int(q[1][0, 0]) == 247
+    ids = torch.zeros(T, dtype=torch.int32, device=DEV)
+    ids[1] = 1
+    a = torch.ones(2, 2, 130, dtype=torch.bfloat16, device=DEV)
+    b = torch.ones(2, 2, 8, dtype=torch.bfloat16, device=DEV)
+    b[:, 1] = 0
+    dy = torch.zeros(T, 8, dtype=torch.bfloat16, device=DEV)
+    dy[:2, 0] = big
+    v = dy[0, 0].item()
+    for dx in (True, False):
+        _, da, _ = bnn.adapter_bwd(dy, q, torch.zeros(T, 2, device=DEV), ids, a, b, dx=dx)
+        want = torch.zeros(2, 2, 130, device=DEV)
+        want[0, 0, 3], want[1, 0, 3] = math.copysign(INF, v), -math.copysign(INF, v)
+        want[1, 0, 128] = v * 2.0 ** -100
+        assert torch.equal(da, want)
