@@ -500,10 +500,10 @@ bnn_status bnn_gemm_signw_grouped(const void *x, int64_t ldx, int64_t xrows, con
  *   workspace    at least bnn_route_fwd_workspace(T, E, k) bytes, 16-byte aligned,
  *            used on `stream` until the call's kernels have run; may be NULL when
  *            that is 0.
- * A valid token with a NaN or +inf among its logits has the weights NaN, and the
- * loss is NaN.  1 <= k <= E, k <= 32, E <= 1024, T k < 2^30.  T = 0 writes offsets,
- * counts, slope and loss.  Errors: BNN_E_DTYPE, BNN_E_ARG (normalise not 0 or
- * 1), BNN_E_SHAPE, BNN_E_NULL, BNN_E_ALIGN, BNN_E_LAUNCH.
+ * A valid token with a NaN or +inf among its logits makes the loss NaN, and its
+ * weights where it has an expert.  1 <= k <= E, k <= 32, E <= 1024, T k < 2^30.
+ * T = 0 writes offsets, counts, slope and loss.  Errors: BNN_E_DTYPE, BNN_E_ARG
+ * (normalise not 0 or 1), BNN_E_SHAPE, BNN_E_NULL, BNN_E_ALIGN, BNN_E_LAUNCH.
  */
 int64_t bnn_route_fwd_workspace(int64_t T, int64_t E, int64_t k);
 bnn_status bnn_route_fwd(const void *z, int dtype, int64_t ldz, const uint8_t *valid,
@@ -518,7 +518,7 @@ bnn_status bnn_route_fwd(const void *z, int dtype, int64_t ldz, const uint8_t *v
  *   g_e = dloss slope[e]  (+ dweights at the choices, normalise = 0)
  *   dz_e = p_e (g_e - sum_i p_i g_i)
  *          (+ w_j (dweights_j - sum_i w_i dweights_i) at the choices, normalise = 1)
- * Zero for a token without an expert.
+ * Zero for a token without an expert, whatever dloss is.
  *
  *   experts, weights, stats, slope   from the forward pass, of the same z.
  *   dweights  T x k fp32 or NULL (0).  dloss  1 fp32; slope and dloss both

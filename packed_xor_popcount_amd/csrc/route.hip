@@ -159,8 +159,9 @@ __device__ void choose(const T *z, int64_t ldz, const uint8_t *valid, const Rout
     }
     float best = largest<V>(key);
     float top = token_max<LPT>(best);
-    const float mz = top > -INFINITY ? top : 0.0f;
-    routed += top > -INFINITY && sub == 0;
+    const bool some = top > -INFINITY;  // an expert is open
+    const float mz = some ? top : 0.0f;
+    routed += some && sub == 0;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     // the k largest, one after the other
     for (int j = 0; j < k; ++j) {
@@ -215,7 +216,7 @@ __device__ void choose(const T *z, int64_t ldz, const uint8_t *valid, const Rout
     }
     if (in && sub == 0) {
       o.stats[2 * t] = mz;
-      o.stats[2 * t + 1] = rsum;
+      o.stats[2 * t + 1] = some ? rsum : 0.0f;  // 0 for NaN alone too: no gradient
     }
   }
   if (routed) atomicAdd(&sh.routed, routed);
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(256)
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] *= gl[i] - s;
+    for (int i = 0; i < V; ++i) v[i] = rsum == 0.0f ? 0.0f : v[i] * (gl[i] - s);
     if (dweights) {
       float add[V];
       __builtin_memcpy(add, __builtin_assume_aligned(mine + e0, 4 * (V < 4 ? V : 4)), sizeof(add));

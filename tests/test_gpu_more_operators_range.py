@@ -74,3 +74,36 @@ def test_gradient_from_8_bits_leaves_zeros_beside_large_factors(big, T):
         want[0, 0, 3], want[1, 0, 3] = math.copysign(INF, v), -math.copysign(INF, v)
         want[1, 0, 128] = v * 2.0 ** -100
         assert torch.equal(da, want)
+
+
+@pytest.mark.parametrize("T", [40, 3000])
+@pytest.mark.parametrize("E", [5, 20, 600])
+@pytest.mark.parametrize("normalise", [True, False])
+def test_router_tokens_of_nan_have_no_expert(T, E, normalise):
+    """NaN alone, or beside -inf: no expert is left, so zeros everywhere but in the loss."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T + E)
+    z = torch.randn(T, E, generator=g, device=DEV)
+    z[3], z[17] = math.nan, -INF
+    z[17, 2] = math.nan
+    r = bnn.route_fwd(z, 3, normalise=normalise)
+    dw = torch.randn(T, 3, generator=g, device=DEV)
+    dz = bnn.route_bwd(z, r.experts, r.weights, r.stats, r.slope, dw, torch.ones(1, device=DEV), normalise)
+    for t in (3, 17):
+        assert (r.experts[t] == -1).all() and not r.weights[t].any() and (r.place[t] < -1).all()
+        assert torch.equal(r.stats[t], torch.zeros(2, device=DEV))
+        assert torch.equal(dz[t], torch.zeros(E, device=DEV))
+    rest = torch.ones(T, dtype=torch.bool, device=DEV)
+    rest[[3, 17]] = False
+    assert torch.isfinite(dz[rest]).all() and r.loss.isnan().all()
+
+
+@pytest.mark.parametrize("dl", [math.nan, INF])
+def test_router_gradient_is_zero_without_an_expert(dl):
+    z = torch.randn(50, 12, device=DEV)
+    z[4] = -INF
+    valid = torch.ones(50, dtype=torch.bool, device=DEV)
+    valid[9] = False
+    r = bnn.route_fwd(z, 2, valid=valid)
+    dz = bnn.route_bwd(z, r.experts, r.weights, r.stats, r.slope, None, torch.full((1,), dl, device=DEV))
+    assert not dz[[4, 9]].any() and not torch.isfinite(dz[0]).all()
