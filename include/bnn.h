@@ -543,7 +543,8 @@ bnn_status bnn_route_bwd(const void *z, int dtype, int64_t ldz, const int32_t *e
  *   place     T x k int32 (bnn_route_fwd).  weights  T x k fp32, or NULL (1).
  *   residual  T rows of type dtype, row stride ldr >= N, or NULL (0).
  *   out       T rows of type dtype (BNN_FP32 / BNN_BF16), row stride ldo >= N;
- *             it may be the residual itself (same pointer and stride).
+ *             it may be the residual itself (same pointer and stride; with
+ *             another stride BNN_E_SHAPE).
  * k >= 1, T k < 2^30.  T = 0 or N = 0 launches nothing.  Errors: BNN_E_DTYPE,
  * BNN_E_SHAPE, BNN_E_NULL, BNN_E_ALIGN, BNN_E_LAUNCH.
  */

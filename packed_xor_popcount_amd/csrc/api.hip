@@ -361,7 +361,7 @@ bnn_status bnn_combine_fwd(const void *y, int ydtype, int64_t ldy, int64_t R,
   if ((dtype != BNN_FP32 && dtype != BNN_BF16) || (ydtype != BNN_FP32 && ydtype != BNN_BF16))
     return BNN_E_DTYPE;
   if (!combine_sizes_ok(R, T, N, k) || ldy < N || ldy >= kMaxDim || ldo < N || ldo >= kMaxDim ||
-      (residual && (ldr < N || ldr >= kMaxDim)))
+      (residual && (ldr < N || ldr >= kMaxDim)) || (residual && residual == out && ldr != ldo))
     return BNN_E_SHAPE;
   if (T > 0 && N > 0 && (!place || !out || (R > 0 && !y))) return BNN_E_NULL;
   const uintptr_t es = dtype == BNN_FP32 ? 4 : 2;

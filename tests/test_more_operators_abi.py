@@ -150,3 +150,12 @@ def test_bindings_refuse_cpu_tensors():
                  lambda: bnn.adapter_fwd(h, ids, w, w), lambda: bnn.adapter_bwd(h, h, f, ids, w, w)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_combine_fwd_in_place_takes_one_stride(lib):
+    """The output may be the residual with its own stride only: rows would be read after others were written."""
+    def f(res, ldr, out, ldo, T=3):
+        return lib.bnn_combine_fwd(FAKE, 0, 8, 6, FAKE, FAKE, res, ldr, out, 0, ldo, T, 8, 2, None)
+    assert f(FAKE, 9, FAKE, 8) == E_SHAPE and f(FAKE, 8, FAKE, 9) == E_SHAPE
+    assert f(FAKE, 8, FAKE, 8, T=0) == OK and f(FAKE, 8, P(0x2000), 9, T=0) == OK
+    assert f(None, 8, FAKE, 9, T=0) == OK
