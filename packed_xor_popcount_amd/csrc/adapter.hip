@@ -172,7 +172,7 @@ __device__ __forceinline__ void make_plan(Plan &p, const int32_t *ids, int64_t t
 }
 
 // ---------------------------------------------------------------------------
-// shrink: u_t[j] = sum_c x_t[c] w_id,j[c], and the parts of s u_t for expand.
+// shrink: u_t[j] = sum_c x_t[c] w_id,j[c], and the parts of u_t for expand.
 // The eight waves of a block take every eighth step of 128 columns of a tile and
 // join their sums in LDS.  blockIdx: chunk, share of the chunk's tiles.
 //
@@ -263,12 +263,12 @@ __device__ __forceinline__ void last_columns(StepRows &buf, const uint16_t *cons
   }
 }
 
-// The waves' sums of a tile.  done(j, t, s, sum) is called with the sums of ranks
+// The waves' sums of a tile.  done(j, t, sum) is called with the sums of ranks
 // j .. j + 3 of row t (zeros past r) by the lanes that hold them; the block is
 // synchronised afterwards.
 template <int RT, typename Done>
 __device__ __forceinline__ void join_tile(ShrinkLds<RT> &lds, const v4f (&acc)[RT], int64_t t,
-                                          bool mine, float s, int r, Done done) {
+                                          bool mine, int r, Done done) {
   constexpr int JT = kJoined<RT>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
 #pragma unroll
@@ -285,7 +285,7 @@ __device__ __forceinline__ void join_tile(ShrinkLds<RT> &lds, const v4f (&acc)[R
 #pragma unroll
       for (int v = 0; v < 4; ++v)
         if (j + v >= r) sum[v] = 0.0f;  // rank r - 1 again
-      done(j, t, s, sum);
+      done(j, t, sum);
     }
   }
   __syncthreads();  // the sums have been read
@@ -295,8 +295,8 @@ __device__ __forceinline__ void join_tile(ShrinkLds<RT> &lds, const v4f (&acc)[R
 template <int RT, int STEPS, bool LONG, typename Done>
 __device__ __forceinline__ void contract_tile(ShrinkLds<RT> &lds, const Plan &plan, int i,
                                               int64_t t0, const uint16_t *x, int64_t ldx,
-                                              const uint16_t *w, const float *scale, int64_t C,
-                                              int r, int L, Done done) {
+                                              const uint16_t *w, int64_t C, int r, int L,
+                                              Done done) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
   const int64_t steps = (C + 127) / 128, whole = C / 128;
   const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
@@ -354,14 +354,14 @@ __device__ __forceinline__ void contract_tile(ShrinkLds<RT> &lds, const Plan &pl
       while (st < whole) several(std::integral_constant<int, 1>());
     if (st < steps) last_columns<RT, LONG>(lds.rows[wave], xr, wr, st, C, acc);
   }
-  join_tile<RT>(lds, acc, t, mine, l < L && scale ? scale[l] : 1.0f, r, done);
+  join_tile<RT>(lds, acc, t, mine, r, done);
 }
 
-// The parts of s sum in a row of parts, from rank j on.
+// The parts of sum in a row of parts, from rank j on.
 template <int RT>
-__device__ __forceinline__ void store_parts(uint16_t *row, int j, float s, const v4f &sum) {
-  const Parts a = parts_of(sum[0] * s), b = parts_of(sum[1] * s);
-  const Parts c = parts_of(sum[2] * s), d = parts_of(sum[3] * s);
+__device__ __forceinline__ void store_parts(uint16_t *row, int j, const v4f &sum) {
+  const Parts a = parts_of(sum[0]), b = parts_of(sum[1]);
+  const Parts c = parts_of(sum[2]), d = parts_of(sum[3]);
   *reinterpret_cast<uint2 *>(row + j) = make_uint2(
       __builtin_amdgcn_perm(b.hi, a.hi, 0x07060302u), __builtin_amdgcn_perm(d.hi, c.hi, 0x07060302u));
   *reinterpret_cast<uint2 *>(row + j + 16 * RT) =
@@ -509,9 +509,8 @@ template <int RT, bool LONG>
 __global__ void __launch_bounds__(64 * kShrinkWaves)
     adapter_shrink_kernel(const uint16_t *__restrict__ x, int64_t ldx,
                           const int32_t *__restrict__ ids, const uint16_t *__restrict__ w,
-                          const float *__restrict__ scale, float *__restrict__ u,
-                          uint16_t *__restrict__ parts, int64_t T, int64_t C, int r, int L,
-                          Grouping gr) {
+                          float *__restrict__ u, uint16_t *__restrict__ parts, int64_t T, int64_t C,
+                          int r, int L, Grouping gr) {
   __shared__ Plan plan;
   __shared__ ShrinkLds<RT> lds;
   int shares = gridDim.y, share = blockIdx.y;
@@ -530,18 +529,18 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
   const int hi = (int)((int64_t)plan.tiles * (share + 1) / shares);
   for (int i = lo; i < hi; ++i)
     contract_tile<RT, (RT == 1 ? 4 : RT == 2 ? 2 : 1), LONG>(
-        lds, plan, i, t0, x, ldx, w, scale, C, r, L,
-        [&](int j, int64_t t, float s, const v4f &sum) {
+        lds, plan, i, t0, x, ldx, w, C, r, L, [&](int j, int64_t t, const v4f &sum) {
           store_sums(u + t * r, j, r, sum);
-          if (parts) store_parts<RT>(parts + t * (parts_kept(RT) * 16 * RT), j, s, sum);
+          if (parts) store_parts<RT>(parts + t * (parts_kept(RT) * 16 * RT), j, sum);
         });
 }
 
 // ---------------------------------------------------------------------------
-// expand: out_t[c] = base_t[c] + sum_j (s u_t[j]) w_id,j[c], the bracket from the
-// parts that shrink left.  A wave has 128 columns; the operand of its adapter's
-// factor stays in registers while the adapter does not change.  A lane ends up
-// with eight neighbouring columns of four rows.  The next tile's operands and
+// expand: out_t[c] = base_t[c] + s sum_j u_t[j] w_id,j[c], u from the parts that shrink
+// left.  (s multiplies the sum, not u: s u may leave fp32's range where out does not.)
+// A wave has 128 columns; the operand of its adapter's factor stays in registers while
+// the adapter does not change.  A lane ends up with eight neighbouring columns of four
+// rows.  The next tile's operands and
 // base are on their way while a tile is computed.  blockIdx: 512 columns, chunk,
 // share of the chunk's tiles.
 //
@@ -602,9 +601,22 @@ struct Factor {
   }
 };
 
-// base + the products of a tile: lane g holds rows 4 g .. 4 g + 3 of it, eight columns.
+// An adapter's scale, l the same in all lanes: a scalar load, beside the vector loads in
+// flight instead of behind them, and without a choice ahead of it (`ids`, of at least one
+// row, is read where there is no scale).
+__device__ __forceinline__ float scale_of(const float *scale, int l, bool has,
+                                          const int32_t *ids) {
+  typedef const __attribute__((address_space(4))) uint32_t constant_t;
+  has = has && scale;
+  const uintptr_t at = has ? (uintptr_t)(scale + l) : (uintptr_t)ids;
+  const uint32_t v = *(constant_t *)at;
+  return has ? __uint_as_float(v) : 1.0f;
+}
+
+// base + s times the products of a tile: lane g holds rows 4 g .. 4 g + 3 of it, eight
+// columns.
 template <typename O, int RP, bool LONG>
-__device__ __forceinline__ void finish_tile(const Plan &plan, int s0, int len, bool has,
+__device__ __forceinline__ void finish_tile(const Plan &plan, int s0, int len, bool has, float s,
                                             const RowParts<RP> &u,
                                             const uint4 (&f)[operands(RP)][8], Chunk<O> (&b)[4],
                                             bool base, O *out, int64_t ldo, int64_t t0, int64_t c,
@@ -627,8 +639,8 @@ __device__ __forceinline__ void finish_tile(const Plan &plan, int s0, int len, b
     float val[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      val[j] = acc[j][v];
-      if (base) val[j] = has ? chunk_value(b[v], j) + val[j] : chunk_value(b[v], j);
+      const float from = base ? chunk_value(b[v], j) : 0.0f;
+      val[j] = has ? fmaf(acc[j][v], s, from) : from;
     }
     store_chunk(out + (t0 + plan.place(s0, len, 4 * g + v)) * ldo, (int)c, (int)C, val);
   }
@@ -639,6 +651,7 @@ struct Expand {
   const uint16_t *parts;  // of w's side, T x parts_kept x 16 RP
   const int32_t *ids;
   const uint16_t *w;
+  const float *scale;
   const O *base;
   O *out;
   int64_t ldb, ldo, T, C;
@@ -678,15 +691,17 @@ __device__ __forceinline__ void expand_block(const Expand<O> &e, Plan &plan, dim
         f.b[v] = raw8<LONG>(base + (t0 + plan.place(s0, len, 4 * g + v)) * ldb, c, C);
     }
   };
-  int now = -1;  // the adapter whose factor is in wf
+  int now = -1;  // the adapter whose factor is in wf, and its scale
+  float s = 1.0f;
   uint4 wf[operands(RP)][8];
   auto tile = [&](int i, Fetch &f) {
     const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
-    const int l = plan.id(s0);
+    const int l = __builtin_amdgcn_readfirstlane(plan.id(s0));  // the tile's: of all lanes
     const bool has = l < L;
     if (!has && base == out) return;  // in place, rows without an adapter stay as they are
     if (has && l != now) {
       now = l;
+      s = scale_of(e.scale, l, true, e.ids);
 #pragma unroll
       for (int q = 0; q < operands(RP); ++q) {
         Factor<RP, LONG> w8;
@@ -695,8 +710,8 @@ __device__ __forceinline__ void expand_block(const Expand<O> &e, Plan &plan, dim
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    finish_tile<O, RP, LONG>(plan, s0, len, has, f.u, wf, f.b, base != nullptr, out, ldo, t0, c, C,
-                             edge, g);
+    finish_tile<O, RP, LONG>(plan, s0, len, has, s, f.u, wf, f.b, base != nullptr, out, ldo, t0, c,
+                             C, edge, g);
   };
   Fetch one, two;
   fetch(lo, one);
@@ -746,7 +761,7 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
   const bool edge = c0 + 128 > N;
   for (int i = lo; i < hi; ++i) {
     const int s0 = plan.start[i], len = plan.start[i + 1] - s0;
-    const int l = plan.id(s0);
+    const int l = __builtin_amdgcn_readfirstlane(plan.id(s0));
     const bool has = l < L, mine = c0 < N && (has || base != out);
     Chunk<O> bs[4];
     if (mine && base) {  // under way during the first product
@@ -754,12 +769,13 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
       for (int v = 0; v < 4; ++v)
         bs[v] = raw8<LONG>(base + (int64_t)plan.place(s0, len, 4 * g + v) * ldb, c, N);
     }
-    contract_tile<RT, 1, LONG>(lds, plan, i, 0, x, ldx, a, scale, K, r, L,
-                               [&](int j, int64_t t, float s, const v4f &sum) {
+    contract_tile<RT, 1, LONG>(lds, plan, i, 0, x, ldx, a, K, r, L,
+                               [&](int j, int64_t t, const v4f &sum) {
                                  if (blockIdx.x == 0) store_sums(u + t * r, j, r, sum);
-                                 store_parts<RT>(parts[lane & 15], j, s, sum);
+                                 store_parts<RT>(parts[lane & 15], j, sum);
                                });
     if (!mine) continue;
+    const float s = scale_of(scale, l, has, ids);
     RowParts<RT> rp;
     rp.load(parts[lane & 15], g);
     uint4 f[operands(RT)][8];
@@ -768,7 +784,7 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
       w8.load(b + (int64_t)l * r * N, 0, c, N, r, g);
       w8.operand(0, c, N, r, g, edge, f[0]);
     }
-    finish_tile<O, RT, LONG>(plan, s0, len, has, rp, f, bs, base != nullptr, out, ldo, 0, c, N,
+    finish_tile<O, RT, LONG>(plan, s0, len, has, s, rp, f, bs, base != nullptr, out, ldo, 0, c, N,
                              edge, g);
   }
 }
@@ -1059,15 +1075,15 @@ unsigned tile_shares(int64_t T, int L, int64_t blocks, int64_t want) {
 }
 
 hipError_t shrink(const uint16_t *x, int64_t ldx, const int32_t *ids, const uint16_t *w,
-                  const float *scale, float *u, uint16_t *parts, int64_t T, int64_t C, int r,
-                  int L, const Grouping &gr, hipStream_t s) {
+                  float *u, uint16_t *parts, int64_t T, int64_t C, int r, int L,
+                  const Grouping &gr, hipStream_t s) {
   const int64_t chunks = (T + kChunk - 1) / kChunk;
   // a block a CU, and a few CUs left for the one that groups the rows: 8192 rows in
   // 224 blocks 29 us, in 256 (one more round then) 33
   const dim3 grid((unsigned)chunks, tile_shares(T, L, chunks, 224) + (gr.rows ? 1 : 0));
 #define BNN_SHRINK_AS(RT, LONG)                                                                 \
-  adapter_shrink_kernel<RT, LONG><<<grid, 64 * kShrinkWaves, 0, s>>>(x, ldx, ids, w, scale, u,  \
-                                                                     parts, T, C, r, L, gr)
+  adapter_shrink_kernel<RT, LONG><<<grid, 64 * kShrinkWaves, 0, s>>>(x, ldx, ids, w, u, parts,  \
+                                                                     T, C, r, L, gr)
 #define BNN_SHRINK(RT)                    \
   do {                                    \
     if (C >= 8) BNN_SHRINK_AS(RT, true);  \
@@ -1087,9 +1103,9 @@ hipError_t shrink(const uint16_t *x, int64_t ldx, const int32_t *ids, const uint
 constexpr int64_t kMostChunks = 65535;  // of a launch
 
 template <typename O>
-hipError_t expand(const uint16_t *parts, const int32_t *ids, const uint16_t *w, const void *base,
-                  int64_t ldb, void *out, int64_t ldo, int64_t T, int64_t C, int r, int L,
-                  hipStream_t s) {
+hipError_t expand(const uint16_t *parts, const int32_t *ids, const uint16_t *w, const float *scale,
+                  const void *base, int64_t ldb, void *out, int64_t ldo, int64_t T, int64_t C, int r,
+                  int L, hipStream_t s) {
   const int64_t all = (T + kChunk - 1) / kChunk, cols = (C + 511) / 512;
   const O *bt = static_cast<const O *>(base);
   O *ot = static_cast<O *>(out);
@@ -1098,9 +1114,8 @@ hipError_t expand(const uint16_t *parts, const int32_t *ids, const uint16_t *w, 
     const int64_t n = T - t < chunks * kChunk ? T - t : chunks * kChunk;
     const dim3 grid((unsigned)cols, (unsigned)chunks, tile_shares(n, L, cols * chunks, 384));
     const uint16_t *pt = parts + parts_bytes(t, r) / 2;
-    const Expand<O> e = {pt,  ids + t, w, bt ? bt + t * ldb : nullptr, ot + t * ldo,
-                         ldb, ldo,     n, C,                           r,
-                         L};
+    const Expand<O> e = {pt,  ids + t, w, scale, bt ? bt + t * ldb : nullptr, ot + t * ldo,
+                         ldb, ldo,     n, C,     r,                           L};
 #define BNN_EXPAND_AS(RP, LONG) adapter_expand_kernel<O, RP, LONG><<<grid, 256, 0, s>>>(e)
 #define BNN_EXPAND(RP)                    \
   do {                                    \
@@ -1122,11 +1137,11 @@ hipError_t expand(const uint16_t *parts, const int32_t *ids, const uint16_t *w, 
 }
 
 hipError_t expand_as(int dtype, const uint16_t *parts, const int32_t *ids, const uint16_t *w,
-                     const void *base, int64_t ldb, void *out, int64_t ldo, int64_t T, int64_t C,
-                     int r, int L, hipStream_t s) {
+                     const float *scale, const void *base, int64_t ldb, void *out, int64_t ldo,
+                     int64_t T, int64_t C, int r, int L, hipStream_t s) {
   if (dtype == BNN_FP32)
-    return expand<float>(parts, ids, w, base, ldb, out, ldo, T, C, r, L, s);
-  return expand<bf16_t>(parts, ids, w, base, ldb, out, ldo, T, C, r, L, s);
+    return expand<float>(parts, ids, w, scale, base, ldb, out, ldo, T, C, r, L, s);
+  return expand<bf16_t>(parts, ids, w, scale, base, ldb, out, ldo, T, C, r, L, s);
 }
 
 // Rows of a tile of the outer sums: about 16 tiles, which with the columns' blocks
@@ -1229,10 +1244,9 @@ hipError_t launch_adapter_fwd(const uint16_t *x, int64_t ldx, const int32_t *ids
     return small<bf16_t>(x, ldx, ids, a, b, scale, base, ldb, out, ldo, u, T, K, N, r, L, s);
   }
   uint16_t *parts = static_cast<uint16_t *>(workspace);
-  const hipError_t e = shrink(x, ldx, ids, a, scale, u, N > 0 ? parts : nullptr, T, K, r, L,
-                              Grouping{}, s);
+  const hipError_t e = shrink(x, ldx, ids, a, u, N > 0 ? parts : nullptr, T, K, r, L, Grouping{}, s);
   if (e != hipSuccess || N == 0) return e;
-  return expand_as(dtype, parts, ids, b, base, ldb, out, ldo, T, N, r, L, s);
+  return expand_as(dtype, parts, ids, b, scale, base, ldb, out, ldo, T, N, r, L, s);
 }
 
 int64_t adapter_bwd_workspace(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
@@ -1262,11 +1276,11 @@ hipError_t launch_adapter_bwd(const AdapterGrad &q, void *workspace, int64_t T, 
                       cols * b.most <= (1 << 20);
   hipError_t e = hipSuccess;
   if (T > 0) {
-    e = shrink(q.dy, q.lddy, q.ids, q.b, q.scale, v, q.dx ? parts : nullptr, T, N, r, L,
+    e = shrink(q.dy, q.lddy, q.ids, q.b, v, q.dx ? parts : nullptr, T, N, r, L,
                beside ? gr : Grouping{}, s);
     if (e != hipSuccess) return e;
     if (q.dx && !joined) {
-      e = expand_as(q.dtype, parts, q.ids, q.a, q.base, q.ldb, q.dx, q.lddx, T, K, r, L, s);
+      e = expand_as(q.dtype, parts, q.ids, q.a, q.scale, q.base, q.ldb, q.dx, q.lddx, T, K, r, L, s);
       if (e != hipSuccess) return e;
     }
   }
@@ -1283,11 +1297,11 @@ hipError_t launch_adapter_bwd(const AdapterGrad &q, void *workspace, int64_t T, 
     // order, rank 16, 72 us, here 68; 8192 in order 91, here 93)
     const Grid ge = {(unsigned)kc, (unsigned)chunks, tile_shares(T, L, kc * chunks, 640)};
     if (q.dtype == BNN_FP32)
-      e = both<float>({parts, q.ids, q.a, static_cast<const float *>(q.base),
+      e = both<float>({parts, q.ids, q.a, q.scale, static_cast<const float *>(q.base),
                        static_cast<float *>(q.dx), q.ldb, q.lddx, T, K, r, L},
                       ge, o, go, s);
     else
-      e = both<bf16_t>({parts, q.ids, q.a, static_cast<const bf16_t *>(q.base),
+      e = both<bf16_t>({parts, q.ids, q.a, q.scale, static_cast<const bf16_t *>(q.base),
                         static_cast<bf16_t *>(q.dx), q.ldb, q.lddx, T, K, r, L},
                        ge, o, go, s);
     if (e != hipSuccess) return e;

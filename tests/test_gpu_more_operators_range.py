@@ -107,3 +107,39 @@ def test_router_gradient_is_zero_without_an_expert(dl):
     r = bnn.route_fwd(z, 2, valid=valid)
     dz = bnn.route_bwd(z, r.experts, r.weights, r.stats, r.slope, None, torch.full((1,), dl, device=DEV))
     assert not dz[[4, 9]].any() and not torch.isfinite(dz[0]).all()
+
+
+# one launch (few rows), two launches, ranks of one operand, of two and of four
+ADAPTERS = [(1, 16), (40, 5), (40, 20), (300, 16), (300, 30), (300, 40), (300, 70)]
+
+
+@pytest.mark.parametrize("T,r", ADAPTERS)
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_adapters_scale_the_sum(T, r, out):
+    """scale * u leaves fp32's range, scale * sum u b does not."""
+    K, N = 136, 260
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device=DEV)
+    x[:, 3] = 2.0 ** 120
+    a = torch.zeros(2, r, K, dtype=torch.bfloat16, device=DEV)
+    a[0, :, 3] = 1.0
+    a[1, :, 3] = 2.0 ** -126
+    b = torch.zeros(2, r, N, dtype=torch.bfloat16, device=DEV)
+    b[0, r - 1], b[1, r - 1] = 2.0 ** -60, 2.0 ** 120
+    x[1::2, 3] = 2.0 ** 20
+    scale = torch.tensor([2.0 ** 30, 2.0 ** -40], device=DEV)
+    ids = (torch.arange(T, device=DEV) % 2).to(torch.int32)
+    base = torch.full((T, N), 2.0 ** 80, dtype=out, device=DEV)
+    base[1::2] = 2.0 ** -30
+    got, u = bnn.adapter_fwd(x, ids, a, b, scale=scale, base=base)
+    assert u[0, 0].item() == 2.0 ** 120 and (T == 1 or u[1, 0].item() == 2.0 ** -106)
+    want = torch.full((T, N), 2.0 ** 90 + 2.0 ** 80, device=DEV).to(out)
+    want[1::2] = 2.0 ** -26 + 2.0 ** -30
+    assert torch.equal(got, want.to(out))
+    got, _ = bnn.adapter_fwd(x, ids, a, b, scale=scale, dtype=out)
+    assert got[0, 0].item() == 2.0 ** 90 and (T == 1 or got[1, 0].item() == 2.0 ** -26)
+    # the gradient by x is the same product: dy in x's place, b and a in a's and b's
+    got, _, _ = bnn.adapter_bwd(x, None, None, ids, b, a, scale=scale, base=base, params=False)
+    assert torch.equal(got, want.to(out))
+    q, u0 = torch.zeros(T, N, dtype=torch.bfloat16, device=DEV), torch.zeros(T, r, device=DEV)
+    got, _, _ = bnn.adapter_bwd(x, q, u0, ids, b, a, scale=scale, base=base)
+    assert torch.equal(got, want.to(out))
