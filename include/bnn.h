@@ -584,8 +584,9 @@ bnn_status bnn_combine_bwd(const void *dout, int dtype, int64_t lddo, const void
  *   u[t] = A_l x[t],   out[t] = base[t] + scale[l] sum_j u[t][j] B_l[j].
  * Rows whose id lies outside [0, L) have no adapter: u = 0, out = base.  The ids
  * may come in any order; rows of one adapter that follow one another are
- * faster.  Products are exact and sums fp32 (within the bound of fp32 sums of K
- * and of rank terms); out is rounded once.
+ * faster.  Products are exact (but for bits of u below 2^-133) and sums fp32
+ * (within the bound of fp32 sums of K and of rank terms); out is rounded once.
+ * Infinities and NaN in x and the factors give what fp32 products and sums give.
  *
  *   x      T rows of K bf16 values, row stride ldx >= K, 2-byte aligned.
  *   ids    T int32.
@@ -614,8 +615,8 @@ bnn_status bnn_adapter_fwd(const void *x, int64_t ldx, const int32_t *ids, const
  * bnn_adapter_bwd -- the gradient of bnn_adapter_fwd.  With v[t] = B_l dy[t]:
  *   dx[t] = base[t] + scale[l] sum_j v[t][j] A_l[j]
  *   da[l] = scale[l] sum_t v[t] x[t]',   db[l] = scale[l] sum_t u[t] dy[t]'
- * over the rows t of adapter l.  Products are exact and sums fp32, in a fixed
- * order: equal inputs give equal bits.
+ * over the rows t of adapter l.  Products, infinities and NaN as in the forward
+ * pass; sums are fp32, in a fixed order: equal inputs give equal bits.
  *
  *   dy     T rows of N bf16 values, row stride lddy >= N.
  *   x, xs  the forward pass's input, of type xdtype: BNN_BF16 with row stride

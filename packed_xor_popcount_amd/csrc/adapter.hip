@@ -80,6 +80,13 @@ __device__ __forceinline__ void split8(const float (&v)[8], uint4 (&o)[3]) {
   for (int i = 0; i < 3; ++i) o[i] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
 }
 
+// A middle or low part is often 0 where v is not, and 0 times an infinity is NaN where v
+// times it is an infinity.  A sum that holds a product of an infinity or NaN is one of
+// these itself, which one the high parts' products alone tell: they replace a NaN.
+__device__ __forceinline__ float unless_nan(float sum, float high) {
+  return sum != sum && !(fabsf(high) <= 3.402823466e38f) ? high : sum;
+}
+
 // Operands of eight columns from eight rows of them (rows r[0..7], columns
 // two to a register): f[j] holds column j's eight rows.
 __device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&f)[8]) {
@@ -631,6 +638,28 @@ __device__ __forceinline__ void finish_tile(const Plan &plan, int s0, int len, b
       for (int q = 0; q < operands(RP); ++q)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = mfma(u.v[q][p], f[q][j], acc[j]);
+    bool nan = false;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      float all = acc[0][v];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) all += acc[j][v];
+      nan |= 4 * g + v < len && all != all;
+    }
+    if (__any(nan)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v4f high = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < operands(RP); ++q) {
+          const bool lower = RP == 1 && g >= 2;  // the operand's other half: middle parts
+          high = mfma(u.v[q][0], lower ? make_uint4(0, 0, 0, 0) : f[q][j], high);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[j][v] = unless_nan(acc[j][v], high[v]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
   }
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
@@ -831,6 +860,52 @@ struct Step {
   float w[RT][8];
 };
 
+// The high parts' sums of a tile, where a sum in `out` is NaN.
+template <int RT, bool LONG>
+__device__ __forceinline__ void outer_high(const Side &sd, const int32_t *rows, int r0, int r1,
+                                           float s, int64_t c0, int j0, int r, float *out) {
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  const int64_t c = c0 + 8 * (lane & 15), C = sd.C;
+#pragma unroll 1
+  for (int q = 0; q < RT; ++q) {
+    const int jw = j0 + 16 * q + (lane & 15);
+    v4f high[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) high[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int i0 = r0; i0 < r1; i0 += 32) {
+      uint4 y[8], f[8];
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + 8 * g + k;
+        const int64_t t = rows[i < r1 ? i : r1 - 1];
+        Chunk<bf16_t> h = raw8<LONG>(static_cast<const uint16_t *>(sd.y) + t * sd.ldy, c, C);
+        settle_chunk(h, (int)c, (int)C);
+        y[k] = i < r1 ? words(h) : make_uint4(0, 0, 0, 0);
+        const float v = sd.w[t * r + (jw < r ? jw : r - 1)];
+        w[k] = i < r1 && jw < r ? parts_of(v).hi : 0;
+      }
+      transpose8(y, f);
+      uint32_t o[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) o[m] = __builtin_amdgcn_perm(w[2 * m + 1], w[2 * m], 0x07060302u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) high[j] = mfma(make_uint4(o[0], o[1], o[2], o[3]), f[j], high[j]);
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int j = j0 + 16 * q + 4 * g + v;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (j < r && c + k < C) {
+          float *at = out + (int64_t)j * C + c + k;
+          *at = unless_nan(*at, high[k][v] * s);
+        }
+    }
+  }
+}
+
 template <int RT, bool F8, bool LONG>
 __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, int r0, int r1,
                                            float s, int64_t c0, int j0, int r, float *out) {
@@ -939,17 +1014,24 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
     }
     cur = next;
   }
+  bool nan = false;
 #pragma unroll
   for (int q = 0; q < RT; ++q)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int j = j0 + 16 * q + 4 * g + v;
       if (j >= r) continue;
-      float val[8];
+      float val[8], all = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) val[k] = acc[q][k][v] * s;
+      for (int k = 0; k < 8; ++k) {
+        val[k] = acc[q][k][v] * s;
+        all += acc[q][k][v];
+      }
+      nan |= all != all;
       store_chunk(out + (int64_t)j * C, (int)c, (int)C, val);
     }
+  // infinities in y's rows (8 bits hold none)
+  if (!F8 && __any(nan)) outer_high<RT, LONG>(sd, rows, r0, r1, s, c0, j0, r, out);
 }
 
 struct Outer {

@@ -143,3 +143,84 @@ def test_adapters_scale_the_sum(T, r, out):
     q, u0 = torch.zeros(T, N, dtype=torch.bfloat16, device=DEV), torch.zeros(T, r, device=DEV)
     got, _, _ = bnn.adapter_bwd(x, q, u0, ids, b, a, scale=scale, base=base)
     assert torch.equal(got, want.to(out))
+
+
+@pytest.mark.parametrize("T,r", ADAPTERS)
+def test_infinite_factors_give_infinities(T, r):
+    """An infinity times a number is an infinity, times zero NaN; columns without one are as before."""
+    K, N = 140, 261
+    g = torch.Generator(device=DEV)
+    g.manual_seed(r)
+    x = torch.randint(1, 3, (T, K), generator=g, device=DEV).to(torch.bfloat16)
+    a = torch.randint(1, 3, (2, r, K), generator=g, device=DEV).to(torch.bfloat16)
+    b = torch.randint(1, 3, (2, r, N), generator=g, device=DEV).to(torch.bfloat16)
+    ids = (torch.arange(T, device=DEV) // 20 % 2).to(torch.int32)
+    base = torch.randint(-4, 5, (T, N), generator=g, device=DEV).float()
+    clean, u = bnn.adapter_fwd(x, ids, a, b, base=base)
+    assert (u > 0).all()
+    bad = b.clone()
+    bad[0, r - 1, 0], bad[0, 0, 7], bad[0, r // 2, 260] = INF, -INF, INF
+    bad[1, r - 1, 130], bad[1, 0, 255] = -INF, math.nan
+    want = clean.clone()
+    one, two = ids == 0, ids == 1
+    want[one, 0], want[one, 7], want[one, 260] = INF, -INF, INF
+    want[two, 130], want[two, 255] = -INF, math.nan
+    got, u2 = bnn.adapter_fwd(x, ids, a, bad, base=base)
+    assert torch.equal(u, u2)
+    assert torch.equal(got.nan_to_num(7.5, 1e30, -1e30), want.nan_to_num(7.5, 1e30, -1e30))
+    # u = 0 meets the infinity: NaN
+    zero = x.clone()
+    zero[0] = 0
+    got, _ = bnn.adapter_fwd(zero, ids, a, bad, base=base)
+    assert got[0, [0, 7, 260]].isnan().all() and torch.equal(got[0, 8:260], base[0, 8:260])
+    # an infinite u: infinities in every column
+    x2 = x.clone()
+    x2[0, 5] = INF
+    got, u2 = bnn.adapter_fwd(x2, ids, a, b, base=base)
+    assert (u2[0] == INF).all() and (got[0] == INF).all() and torch.equal(got[1:], clean[1:])
+
+
+@pytest.mark.parametrize("kept", ["bf16", "f8"])
+@pytest.mark.parametrize("T,r", ADAPTERS + [(1500, 12)])
+def test_infinite_gradients_give_infinities(T, r, kept):
+    """Infinities in the output's gradient and in the kept input: no NaN where the sum has none."""
+    K, N = 261, 140
+    g = torch.Generator(device=DEV)
+    g.manual_seed(r)
+    x = torch.randint(1, 3, (T, K), generator=g, device=DEV).to(torch.bfloat16)
+    dy = torch.randint(1, 3, (T, N), generator=g, device=DEV).to(torch.bfloat16)
+    a = torch.randint(1, 3, (2, r, K), generator=g, device=DEV).to(torch.bfloat16)
+    b = torch.randint(1, 3, (2, r, N), generator=g, device=DEV).to(torch.bfloat16)
+    u = torch.randint(1, 3, (T, r), generator=g, device=DEV).float()
+    ids = (torch.arange(T, device=DEV) // 20 % 2).to(torch.int32)
+
+    def call(x, dy, a=a, base=None):
+        return bnn.adapter_bwd(dy, bnn.quant_f8(x) if kept == "f8" else x, u, ids, a, b)
+
+    dx0, da0, db0 = call(x, dy)
+    last = int(torch.nonzero(ids == ids[-1])[-1])
+    l = int(ids[last])
+    bad = dy.clone()
+    bad[last, 3] = INF
+    dx, da, db = call(x, bad)  # v is infinite, so dx and da of the row's adapter are
+    want = db0.clone()
+    want[l, :, 3] = INF
+    assert torch.equal(db, want)
+    rest = torch.arange(T, device=DEV) != last
+    assert (dx[last] == INF).all() and torch.equal(dx[rest], dx0[rest])
+    want = da0.clone()
+    want[l] = INF
+    assert torch.equal(da, want)
+    if kept == "bf16":
+        bad = x.clone()
+        bad[last, 0], bad[last, 260] = INF, -INF
+        dx, da, db = call(bad, dy)
+        want = da0.clone()
+        want[l, :, 0], want[l, :, 260] = INF, -INF
+        assert torch.equal(da, want) and torch.equal(dx, dx0) and torch.equal(db, db0)
+    bad = a.clone()
+    bad[l, r - 1, 9], bad[l, 0, 260] = INF, -INF
+    dx, da, db = call(x, dy, a=bad)
+    want = dx0.clone()
+    want[ids == l, 9], want[ids == l, 260] = INF, -INF
+    assert torch.equal(dx, want) and torch.equal(da, da0) and torch.equal(db, db0)
