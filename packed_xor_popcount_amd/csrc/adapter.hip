@@ -860,48 +860,45 @@ struct Step {
   float w[RT][8];
 };
 
-// The high parts' sums of a tile, where a sum in `out` is NaN.
-template <int RT, bool LONG>
+// The high parts' sums of a tile, where a sum in `out` is NaN.  In little code, a column
+// at a time: what a kernel holds beside its way costs it too (all eight columns at once,
+// 777 rows, rank 12: 0.7 us).
 __device__ __forceinline__ void outer_high(const Side &sd, const int32_t *rows, int r0, int r1,
-                                           float s, int64_t c0, int j0, int r, float *out) {
+                                           float s, int64_t c0, int j0, int tiles, int r,
+                                           float *out) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
-  const int64_t c = c0 + 8 * (lane & 15), C = sd.C;
 #pragma unroll 1
-  for (int q = 0; q < RT; ++q) {
-    const int jw = j0 + 16 * q + (lane & 15);
-    v4f high[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) high[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int n = 0; n < 8 * tiles; ++n) {
+    const int64_t c = c0 + 8 * (lane & 15) + (n & 7);
+    const uint16_t *y = static_cast<const uint16_t *>(sd.y) + (c < sd.C ? c : 0);
+    const int first = j0 + 16 * (n >> 3), j = first + (lane & 15);
+    const float *w = sd.w + (j < r ? j : r - 1);
+    v4f high = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
     for (int i0 = r0; i0 < r1; i0 += 32) {
-      uint4 y[8], f[8];
-      uint32_t w[8];
+      uint32_t a[8], b[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int i = i0 + 8 * g + k;
         const int64_t t = rows[i < r1 ? i : r1 - 1];
-        Chunk<bf16_t> h = raw8<LONG>(static_cast<const uint16_t *>(sd.y) + t * sd.ldy, c, C);
-        settle_chunk(h, (int)c, (int)C);
-        y[k] = i < r1 ? words(h) : make_uint4(0, 0, 0, 0);
-        const float v = sd.w[t * r + (jw < r ? jw : r - 1)];
-        w[k] = i < r1 && jw < r ? parts_of(v).hi : 0;
+        a[k] = __float_as_uint(w[t * r]);
+        b[k] = y[t * sd.ldy];
+        if (i >= r1) a[k] = b[k] = 0;
       }
-      transpose8(y, f);
-      uint32_t o[4];
+      uint32_t o[4], f[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) o[m] = __builtin_amdgcn_perm(w[2 * m + 1], w[2 * m], 0x07060302u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) high[j] = mfma(make_uint4(o[0], o[1], o[2], o[3]), f[j], high[j]);
+      for (int m = 0; m < 4; ++m) {
+        o[m] = __builtin_amdgcn_perm(a[2 * m + 1], a[2 * m], 0x07060302u);
+        f[m] = __builtin_amdgcn_perm(b[2 * m + 1], b[2 * m], 0x05040100u);
+      }
+      high = mfma(make_uint4(o[0], o[1], o[2], o[3]), make_uint4(f[0], f[1], f[2], f[3]), high);
     }
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int j = j0 + 16 * q + 4 * g + v;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (j < r && c + k < C) {
-          float *at = out + (int64_t)j * C + c + k;
-          *at = unless_nan(*at, high[k][v] * s);
-        }
+      if (c < sd.C && first + 4 * g + v < r) {
+        float *at = out + (int64_t)(first + 4 * g + v) * sd.C + c;
+        *at = unless_nan(*at, high[v] * s);
+      }
     }
   }
 }
@@ -1031,7 +1028,7 @@ __device__ __forceinline__ void outer_tile(const Side &sd, const int32_t *rows, 
       store_chunk(out + (int64_t)j * C, (int)c, (int)C, val);
     }
   // infinities in y's rows (8 bits hold none)
-  if (!F8 && __any(nan)) outer_high<RT, LONG>(sd, rows, r0, r1, s, c0, j0, r, out);
+  if (!F8 && __any(nan)) outer_high(sd, rows, r0, r1, s, c0, j0, RT, r, out);
 }
 
 struct Outer {
