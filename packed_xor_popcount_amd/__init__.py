@@ -775,7 +775,8 @@ def combine_fwd(y, place, weights=None, residual=None, dtype=None, out=None):
     (T, k) as route_fwd makes it (negative: no expert); ``weights`` None (1)
     or contiguous float32 (T, k); ``residual`` None or (T, N) of the output's
     type.  ``dtype`` of the output: float32 or bfloat16, the residual's or y's
-    by default; ``out`` may be the residual itself."""
+    by default; ``out`` may be the residual itself (the same rows, stride
+    included)."""
     index = _index("y", y)
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):

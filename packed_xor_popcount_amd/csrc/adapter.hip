@@ -183,8 +183,8 @@ __device__ __forceinline__ void make_plan(Plan &p, const int32_t *ids, int64_t t
 // The eight waves of a block take every eighth step of 128 columns of a tile and
 // join their sums in LDS.  blockIdx: chunk, share of the chunk's tiles.
 //
-// 4096 rows of 4096, rank 16: 15 us; 8192 of 4096, rank 32: 28 us (x's bytes take 6.5
-// and 13).  Without any load it would still take 9 and 15 us (the plan 5 us, then each
+// 4096 rows of 4096, rank 16: 15 us; 8192 of 4096, rank 32: 29 us (x's bytes take 6.5
+// and 13; ranks over 64 spill 95 registers).  Without any load it would still take 9 and 15 us (the plan 5 us, then each
 // tile's exchange, sums and join), on top of which come the loads; tiles in one
 // pipeline, four waves a block, two blocks a CU and more or fewer shares were no
 // faster.
@@ -547,16 +547,16 @@ __global__ void __launch_bounds__(64 * kShrinkWaves)
 // left.  (s multiplies the sum, not u: s u may leave fp32's range where out does not.)
 // A wave has 128 columns; the operand of its adapter's factor stays in registers while
 // the adapter does not change.  A lane ends up with eight neighbouring columns of four
-// rows.  The next tile's operands and
-// base are on their way while a tile is computed.  blockIdx: 512 columns, chunk,
-// share of the chunk's tiles.
+// rows.  The next tile's operands and base are on their way while a tile is computed.
+// blockIdx: 512 columns, chunk, share of the chunk's tiles.
 //
-// Bound by HBM: 4096 rows of 11008 bf16, rank 16, 37 us, 4.9 TB/s (48 us with the two
+// Bound by HBM: 4096 rows of 11008 bf16, rank 16, 38 us, 4.9 TB/s (48 us with the two
 // blocks a CU that the compiler's own choice of registers allows; 127 us for the
 // first form, which loaded u one value at a time); 8192 of 4096, rank 32, 31 us;
-// 4096 of 4096 fp32 on 16 adapters in random order 43 us.  The blocks a CU are chosen
-// by the registers that a type and rank need without spilling (rank 64, 2048 of
-// 4096: one 21 us, two 15).
+// 4096 of 4096 fp32 on 16 adapters in random order 43 us.  The blocks a CU are those
+// whose registers hold a type and rank, to within a few spills: at ranks 33 .. 64 in
+// fp32, where two leave 8 spilled, 2048 of 4096 take 20.8 us, with one 24.0 (bf16, none
+// spilled: the call 28 us, with one 34); from 65 on one.
 
 constexpr int operands(int rp) { return (rp + 1) / 2; }     // of 32 ranks
 constexpr int parts_of_operand(int rp) { return rp == 1 ? 2 : 3; }
@@ -1068,7 +1068,10 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(Outer o) {
 // other, the first is bound by memory, the second by its steps' latency.  Their
 // blocks alternate, so that a CU has one of each: 8192 rows, 4096 bf16 and 4096 in 8
 // bits, rank 32: the call 94 us, as two launches 102; 20000 rows, rank 16: 186 us
-// (outer sums first 201, last 209, two launches 227).
+// (outer sums first 201, last 209, two launches 227).  Two blocks a CU, although that
+// spills 6 to 26 registers at ranks 17 .. 32 with x in 8 bits and at 33 .. 64 with that or
+// fp32 outputs: the first case with one 117 us, 4096 rows, rank 64, x in bf16 85 (one
+// 105), in 8 bits with fp32 outputs 107 (one 110).
 struct Grid {
   unsigned x, y, z;
   __host__ __device__ unsigned blocks() const { return x * y * z; }

@@ -122,8 +122,8 @@ struct Shared {
 // A token's logits stay in registers: the largest is found k times over (rotations
 // within 16 lanes, four tokens a wave at once), its lane takes it out, without a
 // branch.  Bound by that chain of dependent instructions, not by the 2 us that the
-// logits' bytes take: 16384 x 128 fp32, 8 choices 11 us (a wave a token 19 us; with a
-// branch for the lane that wins 11.8), 8192 x 256 bf16 15.6 us.
+// logits' bytes take: 16384 x 128 fp32, 8 choices 11 to 12 us (a wave a token 19 us;
+// with a branch for the lane that wins 11.8 where this took 10.9), 8192 x 256 bf16 15.9 us.
 //
 // Choices, weights and statistics of the block's tokens, their counts in
 // sh.hist, the number of tokens with an expert in sh.routed and the sums of p
