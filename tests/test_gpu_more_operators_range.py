@@ -224,3 +224,47 @@ def test_infinite_gradients_give_infinities(T, r, kept):
     want = dx0.clone()
     want[ids == l, 9], want[ids == l, 260] = INF, -INF
     assert torch.equal(dx, want) and torch.equal(da, da0) and torch.equal(db, db0)
+
+
+@pytest.mark.parametrize("T", [3, 400])
+@pytest.mark.parametrize("K,N", [(0, 9), (9, 0), (0, 0)])
+def test_gradient_of_empty_sides(T, K, N):
+    """No columns on one side: its gradients are empty, the other's as for any width."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    dy = torch.randint(-2, 3, (T, N), generator=g, device=DEV).to(torch.bfloat16)
+    x = torch.randint(-2, 3, (T, K), generator=g, device=DEV).to(torch.bfloat16)
+    u = torch.randint(-2, 3, (T, 2), generator=g, device=DEV).float()
+    base = torch.randint(-2, 3, (T, K), generator=g, device=DEV).float()
+    ids = (torch.arange(T, device=DEV) % 3 - 1).to(torch.int32)
+    a, b = (torch.ones(2, 2, n, dtype=torch.bfloat16, device=DEV) for n in (K, N))
+    dx, da, db = bnn.adapter_bwd(dy, x, u, ids, a, b, base=base)
+    assert torch.equal(dx, base) and da.shape == (2, 2, K) and db.shape == (2, 2, N) and not da.any()
+    for l in range(2):
+        mine = ids == l
+        assert torch.equal(db[l], u[mine].t() @ dy[mine].float())
+
+
+def test_most_adapters():
+    """The largest number of adapters: an id and a row's place in its chunk share a word."""
+    L, T = 2 ** 20 - 1, 1000
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    ids = torch.randint(-1, L, (T,), generator=g, device=DEV).to(torch.int32)
+    ids[::7], ids[3::7] = L - 1, 0
+    a, b = (torch.randint(-3, 4, (L, 1, n), generator=g, device=DEV).to(torch.bfloat16) for n in (2, 3))
+    x = torch.randint(-3, 4, (T, 2), generator=g, device=DEV).to(torch.bfloat16)
+    for rows in (T, 30):
+        out, u = bnn.adapter_fwd(x[:rows], ids[:rows], a, b)
+        l, has = ids[:rows].long().clamp(min=0), (ids[:rows] >= 0).float()[:, None]
+        want = (a[l, 0].float() * x[:rows].float()).sum(1, keepdim=True) * has
+        assert torch.equal(u, want) and torch.equal(out, want * b[l, 0].float())
+
+
+def test_sum_in_place_with_another_stride_is_refused():
+    buf = torch.zeros(200, device=DEV)
+    residual, out = buf.as_strided((8, 10), (12, 1)), buf.as_strided((8, 10), (20, 1))
+    y, place = torch.ones(8, 10, device=DEV), torch.arange(8, dtype=torch.int32, device=DEV).view(8, 1)
+    with pytest.raises(bnn.BnnError):
+        bnn.combine_fwd(y, place, residual=residual, out=out)
+    assert not buf.any()
