@@ -82,8 +82,8 @@ def table(trace, notes):
             at += 1
         else:
             cases[at].append(r)
-    print("| call | kernel | median us | 10 % .. 90 % | LDS bytes | threads |")
-    print("|---|---|---|---|---|---|")
+    print("| call | kernel | median us | 10 % .. 90 % | threads |")
+    print("|---|---|---|---|---|")
     for label, part in zip(labels, cases):
         n = len(part) // CALLS
         assert n * CALLS == len(part), "the trace and the notes do not fit"
@@ -93,7 +93,7 @@ def table(trace, notes):
             name = next(k for k in KERNELS if k in mine[0]["Kernel_Name"])
             grid = " x ".join(mine[0]["Grid_Size_" + d] for d in "XYZ")
             print(f"| {label if j == 0 else ''} | `{name}` | {us[CALLS // 2]:.2f} | {us[CALLS // 10]:.2f} .. "
-                  f"{us[-1 - CALLS // 10]:.2f} | {mine[0]['LDS_Block_Size']} | {grid} |")
+                  f"{us[-1 - CALLS // 10]:.2f} | {grid} |")
 
 
 if __name__ == "__main__":
